@@ -23,7 +23,8 @@ STATUS = {
 
 # every symbol include/gdn.h declares
 EXPORTS = ("gdn_fwd", "gdn_fwd_f32", "gdn_step", "gdn_step_f32", "gdn_fwd_ex", "gdn_fwd_host",
-           "gdn_apply_maps", "gdn_workspace_bytes", "gdn_status_string", "gdn_last_error", "gdn_version")
+           "gdn_apply_maps", "gdn_workspace_bytes", "gdn_status_string", "gdn_last_error", "gdn_version",
+           "gdn_decode", "gdn_packed", "gdn_bwd", "gdn_seq_workspace_bytes")
 
 
 class GdnError(RuntimeError):
@@ -51,6 +52,31 @@ class GdnArgs(ctypes.Structure):
         ("status_dev", ctypes.c_void_p),
         ("phase", ctypes.c_int), ("segment_map", ctypes.c_void_p),
     ]
+
+
+class GdnSeqArgs(ctypes.Structure):
+    """Mirror of ``gdn_seq_args`` in include/gdn.h (same field order and types)."""
+    _fields_ = [
+        ("struct_size", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("alpha", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+        ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong),
+        ("o", ctypes.c_void_p), ("S_in", ctypes.c_void_p), ("S_out", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("fresh", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_int), ("n_slots", ctypes.c_int),
+        ("seq_len", ctypes.c_longlong), ("n_tokens", ctypes.c_longlong),
+        ("H", ctypes.c_int), ("Hk", ctypes.c_int), ("d_k", ctypes.c_int), ("d_v", ctypes.c_int),
+        ("d_o", ctypes.c_void_p), ("dS_out", ctypes.c_void_p),
+        ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p),
+        ("dalpha", ctypes.c_void_p), ("dbeta", ctypes.c_void_p), ("dS_in", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p), ("status_dev", ctypes.c_void_p),
+    ]
+
+
+GDN_SEQ_BAD_SLOT = 1
+GDN_SEQ_SAME_SLOT = 2
+GDN_SEQ_BAD_ROWS = 4
 
 GDN_MODE_TOKEN = 0
 GDN_MODE_FRAME = 1
@@ -88,6 +114,12 @@ def load_library(path: str = LIB_PATH):
     lib.gdn_apply_maps.restype = I
     lib.gdn_workspace_bytes.argtypes = [I, I, LL, I, I, I, I]
     lib.gdn_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("gdn_decode", "gdn_packed", "gdn_bwd"):
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.POINTER(GdnSeqArgs)]
+        fn.restype = I
+    lib.gdn_seq_workspace_bytes.argtypes = [ctypes.POINTER(GdnSeqArgs), I]
+    lib.gdn_seq_workspace_bytes.restype = ctypes.c_size_t
     lib.gdn_status_string.argtypes = [I]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
@@ -283,3 +315,246 @@ def bidirectional(q, k, v, alpha, beta, frame_len, *, chunk_len=0, S_in=None, st
     gdn_fwd(q, k, v, alpha, beta, frame_len, None, o=o, reverse=True, accumulate=True,
             reset_every=chunk_len, stream=stream)
     return o, S
+
+
+# ---------------------------------------------------------------- sequences of any length
+def _need(ok, status, text):
+    if not ok:
+        raise GdnError(status, text)
+
+
+def _tokens(name, t, q, lead, heads, d):
+    """A q/k/v-like tensor [*lead, heads, d]: checked; returns the elements between its token rows."""
+    if t.device != q.device or t.dtype != q.dtype:
+        raise GdnError(1, "%s must have q's device and dtype (%s, %s)" % (name, q.device, q.dtype))
+    if t.shape != (*lead, heads, d):
+        raise GdnError(2, "%s must have shape %s, got %s" % (name, (*lead, heads, d), tuple(t.shape)))
+    if t.is_contiguous():
+        return heads * d
+    st = t.stride()
+    if st[-1] != 1 or (st[-2] != d and heads > 1) or (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * st[1]):
+        raise GdnError(1, "%s: the heads of a token must be contiguous and the tokens equally far apart" % name)
+    # of a single sequence or token a stride says nothing
+    return st[-3] if lead[-1] > 1 or len(lead) == 1 else st[0]
+
+
+def _plain(name, t, dtype, shape, device):
+    """A contiguous tensor of one type and shape (None in a shape: any size), or None."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype != dtype or not t.is_contiguous():
+        raise GdnError(1, "%s must be a contiguous %s tensor on %s" % (name, str(dtype).replace("torch.", ""), device))
+    if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise GdnError(2, "%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _seq_args(q, k, v, alpha, beta, lead):
+    """The arguments that the sequence entries share; `lead` is the tokens' leading shape."""
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v), ("alpha", alpha), ("beta", beta)):
+        if t is None:
+            raise GdnError(1, "%s is required" % name)
+    if not q.is_cuda:
+        raise GdnError(1, "q is not a CUDA tensor")
+    if q.dtype is not torch.bfloat16 and q.dtype is not torch.float32:
+        raise GdnError(1, "q/k/v must share one dtype, bf16 or fp32")
+    n = len(lead)
+    if q.dim() != n + 2 or v.dim() != n + 2:
+        raise GdnError(2, "q and v must have %d dimensions, got %s and %s" % (n + 2, tuple(q.shape), tuple(v.shape)))
+    Hk, d_k = q.shape[n:]
+    H, d_v = v.shape[n:]
+    a = GdnSeqArgs()
+    a.struct_size = ctypes.sizeof(GdnSeqArgs)
+    a.dtype = GDN_DTYPE_BF16 if q.dtype is torch.bfloat16 else GDN_DTYPE_F32
+    a.q_stride = _tokens("q", q, q, lead, Hk, d_k)
+    a.k_stride = _tokens("k", k, q, lead, Hk, d_k)
+    a.v_stride = _tokens("v", v, q, lead, H, d_v)
+    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
+    a.alpha = _plain("alpha", alpha, torch.float32, (*lead, H), q.device)
+    a.beta = _plain("beta", beta, torch.float32, (*lead, H), q.device)
+    a.H, a.Hk, a.d_k, a.d_v = H, Hk, d_k, d_v
+    return a
+
+
+def _lead(q, cu_seqlens):
+    """Leading shape of the tokens, and (n_seqs, seq_len, n_tokens)."""
+    import torch
+    if cu_seqlens is None:
+        if q.dim() != 4:
+            raise GdnError(2, "without cu_seqlens q is [B, T, Hk, d_k], got %s" % (tuple(q.shape),))
+        B, T = q.shape[:2]
+        return (B, T), B, T, B * T
+    if q.dim() != 3:
+        raise GdnError(2, "with cu_seqlens q is [tokens, Hk, d_k], got %s" % (tuple(q.shape),))
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise GdnError(2, "cu_seqlens must have shape [sequences + 1], got %s" % (tuple(cu_seqlens.shape),))
+    return (q.shape[0],), cu_seqlens.numel() - 1, 0, q.shape[0]
+
+
+class _On:
+    """The device of the tensors made current, and `stream` (None: its current one) for the
+    call's own allocations, so that their memory is reused in that stream's order."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.outer = []
+        if stream is not None:
+            self.outer.append(torch.cuda.stream(stream))
+        elif device.index != torch.cuda.current_device():
+            self.outer.append(torch.cuda.device(device))
+        self.handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+    def __enter__(self):
+        for c in self.outer:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *e):
+        for c in reversed(self.outer):
+            c.__exit__(*e)
+
+
+def _stream_device(stream, device):
+    if stream is not None and stream.device != device:
+        raise GdnError(1, "stream is on %s, the tensors on %s" % (stream.device, device))
+
+
+def gdn_decode(q, k, v, alpha, beta, S, slots=None, *, o=None, status=None, stream=None):
+    """The next one or few tokens of a batch of sequences, in the recurrent form.
+
+    q, k [B, n, Hk, d_k], v [B, n, H, d_v] (bf16 or fp32), alpha, beta [B, n, H] fp32; for n = 1
+    the n dimension may be left out of all of them.  H is a multiple of Hk: head h reads q/k head
+    h // (H // Hk).  The heads of a token are contiguous; the tokens of q, k, v may be slices of a
+    fused projection (equally far apart, a multiple of 16 bytes).
+    S fp32 [n_slots, H, d_v, d_k] holds the states and is updated in place: sequence b's is
+    S[slots[b]] (slots int32 [B]; None: S[b]).  A negative slot is a padding entry: its o rows and
+    every state are left alone.  So is a sequence with a slot >= n_slots or the slot of an earlier
+    sequence; `status` (a CUDA int32 tensor) then receives GDN_SEQ_BAD_SLOT / GDN_SEQ_SAME_SLOT.
+    Returns (o, S).
+    """
+    import torch
+    lead = q.shape[:-2]
+    _need(len(lead) in (1, 2), 2, "q is [B, n, Hk, d_k] or [B, Hk, d_k], got %s" % (tuple(q.shape),))
+    a = _seq_args(q, k, v, alpha, beta, tuple(lead))
+    dev = q.device
+    _need(S is not None, 1, "S is required")
+    a.n_seqs, a.seq_len = lead[0], lead[1] if len(lead) == 2 else 1
+    a.n_tokens = a.n_seqs * a.seq_len
+    a.S_in = a.S_out = _plain("S", S, torch.float32, (None, a.H, a.d_v, a.d_k), dev)
+    a.n_slots = S.shape[0]
+    a.slots = _plain("slots", slots, torch.int32, (lead[0],), dev)
+    a.status_dev = _plain("status", status, torch.int32, (1,), dev)
+    _stream_device(stream, dev)
+    with _On(dev, stream) as a.stream:
+        if o is None:
+            o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        a.o = _plain("o", o, v.dtype, v.shape, dev)
+        check(load_library().gdn_decode(ctypes.byref(a)))
+    return o, S
+
+
+def gdn_packed(q, k, v, alpha, beta, cu_seqlens=None, S_in=None, *, S_out=None, slots=None, fresh=None, o=None,
+               return_state=False, workspace=None, status=None, stream=None):
+    """The forward pass over sequences of different lengths packed behind one another.
+
+    q, k [N, Hk, d_k], v [N, H, d_v] (bf16 or fp32), alpha, beta [N, H] fp32; sequence s covers
+    the tokens cu_seqlens[s] .. cu_seqlens[s+1] - 1 (int32 [n + 1], on the GPU and read there only).
+    Without cu_seqlens: [B, T, heads, d] tensors, B sequences of T tokens.  Heads, strides and slots
+    as in ``gdn_decode``; o rows of tokens that no sequence covers are left as they were.
+    S_in, S_out fp32 [n_slots, H, d_v, d_k] hold the states that enter (None: zeros) and leave
+    (None: not stored, unless ``return_state`` makes a tensor of n_slots = n); they may be the same
+    tensor.  ``fresh`` (bool or uint8 [n]) starts the marked sequences from zero without reading S_in.
+    ``status`` may also receive GDN_SEQ_BAD_ROWS (a range out of order or out of the tensors).
+    Returns (o, S_out or None).
+    """
+    import torch
+    lead, n, T, N = _lead(q, cu_seqlens)
+    a = _seq_args(q, k, v, alpha, beta, lead)
+    dev = q.device
+    a.n_seqs, a.seq_len, a.n_tokens = n, T, N
+    a.cu_seqlens = _plain("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
+    a.slots = _plain("slots", slots, torch.int32, (n,), dev)
+    if fresh is not None and fresh.dtype == torch.bool:
+        fresh = fresh.view(torch.uint8)
+    a.fresh = _plain("fresh", fresh, torch.uint8, (n,), dev)
+    a.status_dev = _plain("status", status, torch.int32, (1,), dev)
+    _stream_device(stream, dev)
+    with _On(dev, stream) as a.stream:
+        if o is None:
+            o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        if S_out is None and return_state:
+            _need(slots is None, 1, "return_state makes one state a sequence: with slots pass S_out")
+            S_out = torch.empty((n, a.H, a.d_v, a.d_k), dtype=torch.float32, device=dev)
+        a.o = _plain("o", o, v.dtype, v.shape, dev)
+        pools = [t for t in (S_in, S_out) if t is not None]
+        a.n_slots = pools[0].shape[0] if pools else n
+        a.S_in = _plain("S_in", S_in, torch.float32, (a.n_slots, a.H, a.d_v, a.d_k), dev)
+        a.S_out = _plain("S_out", S_out, torch.float32, (a.n_slots, a.H, a.d_v, a.d_k), dev)
+        _seq_workspace(a, workspace, dev, 0)
+        check(load_library().gdn_packed(ctypes.byref(a)))
+    return o, S_out
+
+
+def _seq_workspace(a, workspace, device, bwd):
+    """The caller's workspace, or the library's stream-ordered scratch (the pointer stays NULL);
+    a call being captured takes it from torch's allocator, so that the graph keeps its own."""
+    import torch
+    if workspace is None and torch.cuda.is_current_stream_capturing():
+        workspace = torch.empty(seq_workspace_args(a, bwd), dtype=torch.uint8, device=device)
+    if workspace is not None and workspace.numel():
+        _need(workspace.device == device and workspace.is_contiguous(), 1, "workspace must be a contiguous tensor on %s" % device)
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+
+
+def seq_workspace_args(a, bwd) -> int:
+    return int(load_library().gdn_seq_workspace_bytes(ctypes.byref(a), bwd))
+
+
+def gdn_bwd(q, k, v, alpha, beta, do, cu_seqlens=None, S_in=None, *, dS_out=None, need_dS_in=None, workspace=None,
+            status=None, stream=None):
+    """Gradients of ``gdn_packed``: tensors as there, ``do`` the gradient of o and ``dS_out`` that of
+    the states that leave (None: zeros); S_in and dS_out are fp32 [n, H, d_v, d_k], one state a
+    sequence.  The forward pass is recomputed; nothing of it needs to be kept.
+    Returns (dq, dk, dv, dalpha, dbeta, dS_in): the first three in q's dtype, the gates' in fp32, and
+    dS_in (fp32) when S_in is given or ``need_dS_in`` asks for it, else None.  Gradients of q/k heads
+    that several heads share are summed in fp32; of tokens that no sequence covers they are zeros.
+    """
+    import torch
+    lead, n, T, N = _lead(q, cu_seqlens)
+    a = _seq_args(q, k, v, alpha, beta, lead)
+    dev = q.device
+    a.n_seqs, a.seq_len, a.n_tokens = n, T, N
+    a.cu_seqlens = _plain("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
+    state = (n, a.H, a.d_v, a.d_k)
+    a.n_slots = n
+    a.S_in = _plain("S_in", S_in, torch.float32, state, dev)
+    a.dS_out = _plain("dS_out", dS_out, torch.float32, state, dev)
+    _need(do is not None, 1, "do is required")
+    a.d_o = _plain("do", do, v.dtype, v.shape, dev)
+    a.status_dev = _plain("status", status, torch.int32, (1,), dev)
+    _stream_device(stream, dev)
+    with _On(dev, stream) as a.stream:
+        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k))
+        dv = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        dalpha, dbeta = (torch.empty(alpha.shape, dtype=torch.float32, device=dev) for _ in range(2))
+        dS_in = None
+        if need_dS_in or (need_dS_in is None and S_in is not None):
+            dS_in = torch.empty(state, dtype=torch.float32, device=dev)
+        a.dq, a.dk, a.dv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
+        a.dalpha, a.dbeta, a.dS_in = dalpha.data_ptr(), dbeta.data_ptr(), _ptr(dS_in)
+        _seq_workspace(a, workspace, dev, 1)
+        check(load_library().gdn_bwd(ctypes.byref(a)))
+    return dq, dk, dv, dalpha, dbeta, dS_in
+
+
+def seq_workspace_bytes(n_tokens, H, Hk, d_k, d_v, *, n_seqs, packed=True, bwd=False, dtype="bf16") -> int:
+    """Scratch of a ``gdn_packed`` (or, with ``bwd``, ``gdn_bwd``) call of these sizes; ``packed``:
+    with cu_seqlens, else n_seqs sequences of n_tokens // n_seqs tokens."""
+    a = GdnSeqArgs()
+    a.dtype = GDN_DTYPE_BF16 if dtype in ("bf16", GDN_DTYPE_BF16) else GDN_DTYPE_F32
+    a.n_seqs, a.n_tokens, a.seq_len = n_seqs, n_tokens, 0 if packed or not n_seqs else n_tokens // n_seqs
+    a.cu_seqlens = 16 if packed else None  # looked at for NULL only
+    a.H, a.Hk, a.d_k, a.d_v = H, Hk, d_k, d_v
+    return seq_workspace_args(a, int(bool(bwd)))

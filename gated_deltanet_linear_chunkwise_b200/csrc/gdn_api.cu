@@ -410,6 +410,7 @@ namespace gdn {
 // Validation and error text shared with the other entry-point files.
 int validate_args(const gdn_args &a, Problem &p) { return validate(a, p); }
 void set_error_text(const char *msg) { set_err("%s", msg); }
+cudaError_t pool_scratch(void **ptr, size_t bytes, cudaStream_t s) { return scratch_alloc(ptr, bytes, s); }
 
 int debug_drop_signal() {
     const char *e = getenv("GDN_DEBUG_DROP_SIGNAL");

@@ -120,6 +120,8 @@ int debug_drop_signal();
 int validate_args(const gdn_args &a, Problem &p);
 // Sets the thread-local text gdn_last_error() returns.
 void set_error_text(const char *msg);
+// Stream-ordered scratch from the library's pool (gdn_api.cu); freed with cudaFreeAsync.
+cudaError_t pool_scratch(void **ptr, size_t bytes, cudaStream_t s);
 
 // Scratch layout of the CUDA-core path (byte offsets into the workspace).
 struct SimtLayout {

@@ -1,0 +1,147 @@
+// seq_internal.h -- the gated delta rule over packed sequences: what its
+// entry points (seq_api.cu) and kernels (seq_*.cu) share.
+#pragma once
+
+#include "gdn_internal.h"
+
+namespace gdn {
+
+constexpr int kSeqChunk = 64;  // tokens of a chunk in the chunked kernels
+
+struct SeqProblem {
+    int dtype;
+    const void *q, *k, *v;
+    const float *alpha, *beta;
+    long long q_stride, k_stride, v_stride;  // elements between token rows
+    void *o;
+    const float *S_in;
+    float *S_out;
+    const int *cu, *slots;
+    const unsigned char *fresh;
+    int n_seqs, n_slots;
+    long long seq_len, n_tokens;
+    int H, Hk, dk, dv;
+    const void *d_o;
+    const float *dS_out;
+    void *dq, *dk_out, *dv_out;
+    float *dalpha, *dbeta, *dS_in;
+    int *status;
+};
+
+// Rows and state entry of a sequence.  slot < 0: the sequence is skipped.
+struct SeqRange {
+    long long first;
+    long long len;
+    int slot;
+    int bad;  // GDN_SEQ_* bits
+};
+
+// Rows of sequence s, 0 of them where they are no ordered range inside the tensors.
+__device__ __forceinline__ SeqRange seq_rows(const SeqProblem &p, int s) {
+    SeqRange r;
+    r.bad = 0;
+    r.slot = s;
+    if (p.cu) {
+        const long long a = p.cu[s], b = p.cu[s + 1];
+        const bool ok = a >= 0 && b >= a && b <= p.n_tokens;
+        r.first = ok ? a : 0;
+        r.len = ok ? b - a : 0;
+        if (!ok) {
+            r.bad = GDN_SEQ_BAD_ROWS;
+            r.slot = -1;
+        }
+    } else {
+        r.first = (long long)s * p.seq_len;
+        r.len = p.seq_len;
+    }
+    return r;
+}
+
+// seq_rows with the slot looked up and checked; called by a whole block (it votes on an
+// earlier sequence of the same slot, so that of two writers of one state only the first runs).
+__device__ __forceinline__ SeqRange seq_range(const SeqProblem &p, int s) {
+    SeqRange r = seq_rows(p, s);
+    if (p.slots) {
+        const int slot = p.slots[s];
+        bool same = false;
+        if (slot >= 0)
+            for (int i = threadIdx.x; i < s; i += blockDim.x) same |= p.slots[i] == slot;
+        same = __syncthreads_or(same);
+        if (slot >= p.n_slots) r.bad |= GDN_SEQ_BAD_SLOT;
+        if (same) r.bad |= GDN_SEQ_SAME_SLOT;
+        r.slot = (r.bad || slot < 0) ? -1 : slot;
+    }
+    return r;
+}
+
+// One block of a launch reports a sequence's bits.
+__device__ __forceinline__ void seq_report(const SeqProblem &p, const SeqRange &r, bool reporter) {
+    if (r.bad && p.status && reporter) atomicOr(p.status, r.bad);
+}
+
+__device__ __forceinline__ bool seq_starts_zero(const SeqProblem &p, int s) {
+    return !p.S_in || (p.fresh && p.fresh[s]);
+}
+
+// Chunks.  Chunk i of sequence s has the index seq_chunk_base(s) + i, unique without a table:
+// ceil(len / 64) <= floor(end / 64) - floor(first / 64) + 1.
+__host__ __device__ __forceinline__ long long seq_chunks_of(long long len) {
+    return (len + kSeqChunk - 1) / kSeqChunk;
+}
+__device__ __forceinline__ long long seq_chunk_base(const SeqProblem &p, int s, long long first) {
+    return p.cu ? first / kSeqChunk + s : s * seq_chunks_of(p.seq_len);
+}
+__host__ inline long long seq_max_chunks(const SeqProblem &p) {
+    return p.cu ? p.n_tokens / kSeqChunk + p.n_seqs : p.n_seqs * seq_chunks_of(p.seq_len);
+}
+
+// The chunk that has index c: its first row and how many rows it has (0: no chunk has it).
+struct SeqChunk {
+    long long first;
+    int rows;
+    int seq;
+};
+// Called by a whole block.  Every sequence is looked at, so that ranges out of order hide no other one.
+__device__ __forceinline__ SeqChunk seq_chunk(const SeqProblem &p, long long c) {
+    __shared__ SeqChunk found;
+    if (!p.cu) {
+        const long long n = seq_chunks_of(p.seq_len);
+        const int s = (int)(c / n);
+        const long long t = (c % n) * kSeqChunk;
+        return {s * p.seq_len + t, (int)min((long long)kSeqChunk, p.seq_len - t), s};
+    }
+    if (threadIdx.x == 0) found = {0, 0, -1};
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {
+        const SeqRange r = seq_rows(p, s);
+        const long long t = (c - seq_chunk_base(p, s, r.first)) * kSeqChunk;
+        if (t >= 0 && t < r.len) found = {r.first + t, (int)min((long long)kSeqChunk, r.len - t), s};
+    }
+    __syncthreads();
+    return found;
+}
+
+// What the chunk kernels keep of each (chunk, head), index chunk * H + head (fp32):
+struct SeqWork {
+    float *T, *P;      // [64][64]: (I + A)^-1 and tril(Q K^T o decay)
+    float *eg, *el;    // [64]: e^{G_i}, e^{G_last - G_i}
+    float *Sig, *D;    // [dv][dk]: the state entering the chunk; the gradient of the one leaving it
+    float *U, *Y, *dR; // [64][dv]
+    float *dqh, *dkh;  // [n_tokens][H][dk]: the gradients before heads are summed (shared heads only)
+};
+size_t seq_bwd_workspace(const SeqProblem &p, void *base, SeqWork *w);
+
+constexpr float kSeqBwdLogFloor = -60.f;  // log alpha in gdn_bwd; see gdn.h
+
+// gdn_bwd on the CUDA cores (seq_simt.cu).
+cudaError_t launch_seq_bwd_simt(const SeqProblem &p, void *ws, cudaStream_t s);
+// Zeros in the gradients of rows that no sequence covers; with cu_seqlens only.
+// (also in dqh / dkh, where they are given).
+cudaError_t launch_seq_zero_rows(const SeqProblem &p, float *dqh, float *dkh, cudaStream_t s);
+// dq, dk from the heads' dqh, dkh.
+cudaError_t launch_seq_share(const SeqProblem &p, const SeqWork &w, cudaStream_t s);
+
+// The recurrent form (seq_recurrent.cu).  `few`: one or a few tokens of each sequence.
+cudaError_t launch_seq_recurrent(const SeqProblem &p, bool few, cudaStream_t s);
+
+}  // namespace gdn

@@ -1,0 +1,214 @@
+// seq_recurrent.cu -- the token-wise rule walked token by token, the state in registers.
+//
+//   S <- alpha S;  u = beta (v - S k);  S <- S + u k^T;  o = S q
+//
+// Row r of S (one of the d_v) meets only k, q and its own v_r, so rows are independent: four
+// lanes hold a row, a quarter of its 16-byte pieces each, and two shuffles finish each of the
+// two dot products.  Everything is fp32.
+//
+// k_few: one or a few tokens (gdn_decode).  The state is read and written once and dominates
+// (2 x 4 d_k d_v bytes a head against 2 (2 d_k + 2 d_v)): the bound is HBM.
+// k_many: sequences of tokens (gdn_packed, where the chunked form does not serve), with the
+// tokens' rows staged in shared memory a block ahead.  Its bound is the fp32 pipe: 4 d_k d_v
+// instructions' lanes a token and head.
+#include <cuda_bf16.h>
+
+#include "seq_internal.h"
+
+namespace gdn {
+namespace {
+
+__device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16 *p) {
+    const uint2 r = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
+}
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    return x;
+}
+
+// One token on a lane's piece of a row; k and q are this lane's pieces of the token's rows.
+// Returns u's row value's output sum (already over the row).
+template <int NF>
+__device__ __forceinline__ float token_step(float4 (&S)[NF], const float4 (&k)[NF], const float4 (&q)[NF], float alpha,
+                                            float beta, float v) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+        S[j].x *= alpha; S[j].y *= alpha; S[j].z *= alpha; S[j].w *= alpha;
+        a.x = fmaf(S[j].x, k[j].x, a.x); a.y = fmaf(S[j].y, k[j].y, a.y);
+        a.z = fmaf(S[j].z, k[j].z, a.z); a.w = fmaf(S[j].w, k[j].w, a.w);
+    }
+    const float u = beta * (v - quad_sum((a.x + a.y) + (a.z + a.w)));
+    a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+        S[j].x = fmaf(u, k[j].x, S[j].x); S[j].y = fmaf(u, k[j].y, S[j].y);
+        S[j].z = fmaf(u, k[j].z, S[j].z); S[j].w = fmaf(u, k[j].w, S[j].w);
+        a.x = fmaf(S[j].x, q[j].x, a.x); a.y = fmaf(S[j].y, q[j].y, a.y);
+        a.z = fmaf(S[j].z, q[j].z, a.z); a.w = fmaf(S[j].w, q[j].w, a.w);
+    }
+    return quad_sum((a.x + a.y) + (a.z + a.w));
+}
+
+constexpr int kFewThreads = 64;  // 16 rows: d_v is a multiple of 16, so a block stays in one head
+
+template <typename T, int NF>
+__global__ void __launch_bounds__(kFewThreads) k_few(const __grid_constant__ SeqProblem p) {
+    const int per_seq = p.H * (p.dv / 16);
+    const int s = blockIdx.x / per_seq, rb = blockIdx.x % per_seq;
+    const int row = rb * 16 + threadIdx.x / 4, part = threadIdx.x & 3;
+    const int h = rb / (p.dv / 16), r = row - h * p.dv, hk = h / (p.H / p.Hk);
+    const int slot = p.slots ? p.slots[s] : s;
+    const bool inside = slot >= 0 && (!p.slots || slot < p.n_slots);
+    // the state's loads start before the slots are compared: they need only an index in range
+    float4 S[NF];
+    const size_t soff = ((size_t)(inside ? slot : 0) * p.H * p.dv + row) * p.dk + part * 4;
+    if (inside) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) S[j] = ld4(p.S_in + soff + 16 * j);
+    }
+    const SeqRange range = seq_range(p, s);
+    seq_report(p, range, rb == 0 && threadIdx.x == 0);
+    if (range.slot < 0) return;
+    for (long long t = 0; t < range.len; ++t) {
+        const long long tok = range.first + t;
+        const T *kp = (const T *)p.k + tok * p.k_stride + (size_t)hk * p.dk + part * 4;
+        const T *qp = (const T *)p.q + tok * p.q_stride + (size_t)hk * p.dk + part * 4;
+        const float v = to_f(((const T *)p.v)[tok * p.v_stride + (size_t)h * p.dv + r]);
+        const float alpha = p.alpha[tok * p.H + h], beta = p.beta[tok * p.H + h];
+        float4 k[NF], q[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) k[j] = ld4(kp + 16 * j);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) q[j] = ld4(qp + 16 * j);
+        const float o = token_step<NF>(S, k, q, alpha, beta, v);
+        if (part == 0) put((T *)p.o + (tok * p.H + h) * p.dv + r, o);
+    }
+#pragma unroll
+    for (int j = 0; j < NF; ++j) *reinterpret_cast<float4 *>(p.S_out + soff + 16 * j) = S[j];
+}
+
+// 16 tokens' k and q rows (fp32), v values of the block's 16 rows and gates, one stage.
+constexpr int kTok = 16;
+constexpr int kManyThreads = 64;
+
+template <typename T, int NF>
+__global__ void __launch_bounds__(kManyThreads) k_many(const __grid_constant__ SeqProblem p) {
+    constexpr int DK = 16 * NF;
+    __shared__ __align__(16) float sk[2][kTok][DK], sq[2][kTok][DK];
+    __shared__ float sv[2][kTok][16], sg[2][kTok][2];
+    const int per_seq = p.H * (p.dv / 16);
+    const int s = blockIdx.x / per_seq, rb = blockIdx.x % per_seq;
+    const int h = rb / (p.dv / 16), r0 = (rb % (p.dv / 16)) * 16, hk = h / (p.H / p.Hk);
+    const int lr = threadIdx.x / 4, part = threadIdx.x & 3;
+    const SeqRange range = seq_range(p, s);
+    seq_report(p, range, rb == 0 && threadIdx.x == 0);
+    if (range.slot < 0) return;
+    const size_t soff = (((size_t)range.slot * p.H + h) * p.dv + r0 + lr) * DK + part * 4;
+    float4 S[NF];
+    const bool zero = seq_starts_zero(p, s);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) S[j] = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : ld4(p.S_in + soff + 16 * j);
+
+    // a thread's share of a stage: NF 16-byte (fp32) / 8-byte (bf16) pieces of k and of q, 4 of v
+    constexpr int PIECES = kTok * DK / 4 / kManyThreads;  // = NF
+    float4 nk[PIECES], nq[PIECES];
+    float nv[4], ng = 0.f;
+    auto fetch = [&](long long t0) {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int i = j * kManyThreads + threadIdx.x, tt = i / (DK / 4), c = (i % (DK / 4)) * 4;
+            const bool on = t0 + tt < range.len;
+            const long long tok = range.first + t0 + tt;
+            nk[j] = on ? ld4((const T *)p.k + tok * p.k_stride + (size_t)hk * DK + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+            nq[j] = on ? ld4((const T *)p.q + tok * p.q_stride + (size_t)hk * DK + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = j * kManyThreads + threadIdx.x, tt = i / 16;
+            nv[j] = t0 + tt < range.len
+                        ? to_f(((const T *)p.v)[(range.first + t0 + tt) * p.v_stride + (size_t)h * p.dv + r0 + i % 16])
+                        : 0.f;
+        }
+        if (threadIdx.x < 2 * kTok && t0 + threadIdx.x / 2 < range.len)
+            ng = ((threadIdx.x & 1) ? p.beta : p.alpha)[(range.first + t0 + threadIdx.x / 2) * p.H + h];
+    };
+    auto stash = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int i = j * kManyThreads + threadIdx.x, tt = i / (DK / 4), c = (i % (DK / 4)) * 4;
+            *reinterpret_cast<float4 *>(&sk[b][tt][c]) = nk[j];
+            *reinterpret_cast<float4 *>(&sq[b][tt][c]) = nq[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = j * kManyThreads + threadIdx.x;
+            sv[b][i / 16][i % 16] = nv[j];
+        }
+        if (threadIdx.x < 2 * kTok) sg[b][threadIdx.x / 2][threadIdx.x & 1] = ng;
+    };
+    if (range.len > 0) {
+        fetch(0);
+        stash(0);
+    }
+    __syncthreads();
+    int b = 0;
+    for (long long t0 = 0; t0 < range.len; t0 += kTok, b ^= 1) {
+        const bool more = t0 + kTok < range.len;
+        if (more) fetch(t0 + kTok);
+        const int n = (int)min((long long)kTok, range.len - t0);
+        for (int t = 0; t < n; ++t) {
+            float4 k[NF], q[NF];
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                k[j] = ld4(&sk[b][t][part * 4 + 16 * j]);
+                q[j] = ld4(&sq[b][t][part * 4 + 16 * j]);
+            }
+            const float o = token_step<NF>(S, k, q, sg[b][t][0], sg[b][t][1], sv[b][t][lr]);
+            if (part == 0) put((T *)p.o + ((range.first + t0 + t) * p.H + h) * p.dv + r0 + lr, o);
+        }
+        if (more) stash(b ^ 1);
+        __syncthreads();
+    }
+    if (p.S_out) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) *reinterpret_cast<float4 *>(p.S_out + soff + 16 * j) = S[j];
+    }
+}
+
+template <typename T, int NF> cudaError_t launch(const SeqProblem &p, bool few, cudaStream_t s) {
+    const long long blocks = (long long)p.n_seqs * p.H * (p.dv / 16);
+    if (few) k_few<T, NF><<<(unsigned)blocks, kFewThreads, 0, s>>>(p);
+    else k_many<T, NF><<<(unsigned)blocks, kManyThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch_t(const SeqProblem &p, bool few, cudaStream_t s) {
+    switch (p.dk / 16) {
+        case 1: return launch<T, 1>(p, few, s);
+        case 2: return launch<T, 2>(p, few, s);
+        case 3: return launch<T, 3>(p, few, s);
+        case 4: return launch<T, 4>(p, few, s);
+        case 5: return launch<T, 5>(p, few, s);
+        case 6: return launch<T, 6>(p, few, s);
+        case 7: return launch<T, 7>(p, few, s);
+        default: return launch<T, 8>(p, few, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_seq_recurrent(const SeqProblem &p, bool few, cudaStream_t s) {
+    return p.dtype == GDN_DTYPE_BF16 ? launch_t<__nv_bfloat16>(p, few, s) : launch_t<float>(p, few, s);
+}
+
+}  // namespace gdn

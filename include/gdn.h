@@ -303,6 +303,113 @@ int gdn_apply_maps(float *S, const float *maps, int n_maps, int B, int H, int d_
  * sizes are invalid). */
 size_t gdn_workspace_bytes(int B, int H, long long T, int frame_len, int d_k, int d_v, int dtype);
 
+/* ------------------------------------------------------------------------
+ * The token-wise rule over sequences of any length: serving and training.
+ *
+ * gdn_decode   the recurrent form: the next one or few tokens of a batch of
+ *              sequences, states in a pool, updated in place.
+ * gdn_packed   the forward pass over sequences of different lengths packed
+ *              behind one another (prompts), from their states to their states.
+ * gdn_bwd      the gradients of gdn_packed's pass.
+ *
+ * Same operation, dtypes and head sizes as gdn_fwd; no frames.  (The SANA-WM
+ * pages describe the rule and its chunk-causal rollout, SANA-WM summary,
+ * sections 3.1 and 3.2; packing, state pools and shared heads are this
+ * library's.)
+ *
+ * Tokens are rows.  Row r of q and k holds Hk heads of d_k, row r of v and o
+ * H heads of d_v, H a multiple of Hk: head h reads q/k head h / (H / Hk).
+ * The heads of a row are contiguous; rows of q, k and v may lie further
+ * apart (*_stride), as slices of one fused projection do.
+ *
+ * Sequence s covers rows [cu_seqlens[s], cu_seqlens[s+1]) of the n_tokens
+ * rows, or [s * seq_len, (s+1) * seq_len) when cu_seqlens is NULL; rows that
+ * no sequence covers are not read, their o rows are left as they were, and
+ * their gradients are written as zeros.  A sequence may be empty: its state
+ * passes through.
+ *
+ * Sequence s's state is entry slots[s] of S_in and S_out ([n_slots, H, d_v,
+ * d_k] fp32), or entry s when slots is NULL.  A negative slot marks a padding
+ * entry: the sequence is skipped, its o rows and states are left alone (its
+ * gradients are zeros).
+ *
+ * Device-side checks.  slots and cu_seqlens are read on the GPU only.  A
+ * sequence is skipped like a padding entry, and its bit set in *status_dev,
+ * when its slot is >= n_slots (GDN_SEQ_BAD_SLOT), when an earlier sequence
+ * has the same slot (GDN_SEQ_SAME_SLOT; the first one runs), or when its rows
+ * are not an ordered range inside the n_tokens rows (GDN_SEQ_BAD_ROWS).  Two
+ * sequences may not share rows.
+ *
+ * Calls are asynchronous on `stream`, whose device must be the current one.
+ * gdn_decode's and gdn_packed's results do not depend on how sequences are
+ * batched, and no result depends on the order in which blocks run.
+ */
+enum { GDN_SEQ_BAD_SLOT = 1, GDN_SEQ_SAME_SLOT = 2, GDN_SEQ_BAD_ROWS = 4 };
+
+/*
+ *   struct_size     sizeof(gdn_seq_args) as compiled by the caller.
+ *   dtype           of q, k, v, o, d_o, dq, dk, dv.
+ *   *_stride        elements between consecutive rows of q, k, v; a multiple of
+ *                   16 bytes; 0: the rows are contiguous.
+ *   n_seqs, seq_len, n_tokens
+ *                   sequences; tokens of each when cu_seqlens is NULL (then
+ *                   n_tokens = n_seqs * seq_len); rows of the tensors.  At most
+ *                   2^31 - 1 rows.
+ *   cu_seqlens      device int [n_seqs + 1] or NULL.
+ *   slots, n_slots  device int [n_seqs] or NULL; entries of S_in / S_out.
+ *   fresh           optional device bytes [n_seqs]: nonzero starts the sequence
+ *                   from a zero state without reading S_in (a recycled slot).
+ *   S_in            states that enter (NULL: zeros).  gdn_decode: required.
+ *   S_out           states that leave (NULL: not stored); may be S_in itself.
+ *                   gdn_decode: must be S_in.
+ *   d_o             gdn_bwd: gradient of o, like v (contiguous).
+ *   dS_out          gdn_bwd: gradient of the states that leave, [n_seqs, H, d_v,
+ *                   d_k] (entry s, not a slot), or NULL: zeros.
+ *   dq, dk, dv, dalpha, dbeta
+ *                   gdn_bwd: gradients, contiguous, like q, k, v, alpha, beta.
+ *   dS_in           gdn_bwd: gradient of the states that enter, [n_seqs, H, d_v,
+ *                   d_k], or NULL.
+ *   workspace, workspace_bytes
+ *                   device scratch, 256-byte aligned, of at least
+ *                   gdn_seq_workspace_bytes(); NULL takes stream-ordered scratch
+ *                   from the library's pool.
+ *   status_dev      optional device int: receives the GDN_SEQ_* bits.
+ */
+typedef struct gdn_seq_args {
+    int struct_size;
+    int dtype;
+    const void *q, *k, *v;
+    const float *alpha, *beta;
+    long long q_stride, k_stride, v_stride;
+    void *o;
+    const float *S_in;
+    float *S_out;
+    const int *cu_seqlens;
+    const int *slots;
+    const unsigned char *fresh;
+    int n_seqs, n_slots;
+    long long seq_len, n_tokens;
+    int H, Hk, d_k, d_v;
+    const void *d_o;
+    const float *dS_out;
+    void *dq, *dk, *dv;
+    float *dalpha, *dbeta, *dS_in;
+    void *workspace;
+    size_t workspace_bytes;
+    gdn_stream_t stream;
+    int *status_dev;
+} gdn_seq_args;
+
+int gdn_decode(const gdn_seq_args *a);
+int gdn_packed(const gdn_seq_args *a);
+/* alpha is floored at e^-60 here: o and S_out are affine in every alpha, so the
+ * floor keeps the gradient of a full reset (alpha = 0) finite and exact. */
+int gdn_bwd(const gdn_seq_args *a);
+
+/* Scratch of a call with these sizes (pointers are not looked at; 0 where none
+ * is needed or a size is invalid).  `bwd`: of gdn_bwd, else of gdn_packed. */
+size_t gdn_seq_workspace_bytes(const gdn_seq_args *a, int bwd);
+
 /* Static text for a status code; never NULL. */
 const char *gdn_status_string(int status);
 
@@ -312,8 +419,9 @@ const char *gdn_last_error(void);
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH.  The gdn_args layout
  * belongs to the version: 0.2.0 added mode, gamma, qk_norm, the RMSNorm
  * weights and status_dev; 0.3.0 added phase and segment_map (struct_size
- * guards a caller built against another layout). */
-#define GDN_VERSION 300
+ * guards a caller built against another layout); 0.4.0 added gdn_seq_args and
+ * its entry points. */
+#define GDN_VERSION 400
 int gdn_version(void);
 
 #ifdef __cplusplus
