@@ -1,0 +1,768 @@
+// seq_chunk.cu -- the chunked gated delta rule over packed sequences on the tensor cores (bf16 q, k, v).
+//
+// Notation and formulas as in seq_simt.cu; chunks of 64 tokens.  Three kernels:
+//
+// k_prep       every (chunk, head) by itself: T, P and the decays.
+// k_chunk_fwd  a block walks the chunks of one sequence and head with 16 columns of the state
+//              (d_v columns are independent), S = Sig^T's 16 rows in registers:
+//                X^T = S [K;Q]^T,  Y = V - e^G X_K,  U^T = (beta Y)^T T^T,
+//                O^T = e^G X_Q^T + U^T P^T,  S <- e^{G_L} S + (e^{G_L-G} U)^T K
+// k_chunk_bwd  the same walk backwards with 16 rows of D^T:
+//                dU^T = e^{G_L-G} D^T K^T + dO^T P,  dR^T = dU^T T,
+//                D^T <- e^{G_L} D^T + (e^G dO)^T Q - (beta e^G dR)^T K
+//
+// The state leaves in fp32 and has to be as exact as a fp32 recurrence, so its products are split ones
+// (seq_mma.cuh); what only reaches a bf16 output (Q S, P U) takes two terms.  Every operand on the state's
+// side has 16 rows and every other one is read as it lies (K, Q by ldmatrix; T and P are
+// stored by k_prep in the order in which a lane needs them, and go to registers directly).
+//
+// Why warp-level products and not tcgen05: with 16 rows of the state a block, one sequence
+// of 20 heads fills 140 of 148 SMs and its 64-token step is as short as it gets.  A tcgen05 product has 128 rows of
+// K and Q against N = 16 here and is bound by its A operand's shared memory reads (128 rows x 16 x 2 bytes at
+// 128 B/clk: 32 clk an instruction, as long as the 16 warp products that it replaces), and pays a
+// round trip through tensor memory for each of three dependent products of a step.
+#include <cuda_bf16.h>
+
+#include "gates.cuh"
+#include "seq_internal.h"
+#include "seq_mma.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace mma;
+using sm100::cp_async16;
+
+constexpr int C = kSeqChunk;
+constexpr int NV = 16;       // rows of S (columns of d_v) that a block holds
+constexpr int PC = C + 8;    // pitch of a [16][64] plane: 9 x 16 bytes, odd, so ldmatrix rows spread over the banks
+constexpr int PV = NV + 8;
+
+// T and P lie in the order of the B operand's fragments: unit (t, b) is the n-tile of 8 tokens
+// from 8t against the 16 tokens from 16b, 3 terms, a lane's two words of each.  Below the
+// diagonal b <= t / 2 (20 units), above it (the transposes) b >= t / 2.
+__host__ __device__ constexpr int low_unit(int t) { return (t / 2) * (t / 2 + 1) + (t & 1) * (t / 2 + 1); }
+__host__ __device__ constexpr int up_unit(int t) { return 20 - low_unit(8 - t) ; }
+constexpr int kUnits = 20;
+
+struct ChunkWork {
+    uint2 *T, *P, *Tt, *Pt;  // [chunk x H][20][3][32]; P or the transposes may be null
+    float *gates;            // [chunk x H][3][64]: e^G, e^{G_L - G}, beta
+    float *Sig, *D;          // [chunk x H][dv][dk]
+    float *U, *X, *dR;       // [chunk x H][dv][64]: X = e^G K Sig
+    float *past, *into, *db; // [chunk x H][dv / 16][64]: a slice's part of the gates' gradients
+    float *dqh, *dkh;        // as in SeqWork
+};
+
+template <int NF>
+__global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
+                                              const float floor_log) {
+    constexpr int DK = 16 * NF, PK = DK + 8;
+    // K and Q, and in their place, once they have been multiplied, A and its inverse
+    constexpr int kRows = 2 * C * PK * (int)sizeof(bf16), kMat = C * (C + 1) * (int)sizeof(float);
+    __shared__ __align__(16) unsigned char room[kRows > kMat ? kRows : kMat];
+    bf16(*const sK)[PK] = reinterpret_cast<bf16(*)[PK]>(room);
+    bf16(*const sQ)[PK] = sK + C;
+    float(*const sA)[C + 1] = reinterpret_cast<float(*)[C + 1]>(room);
+    __shared__ double sG[C];
+    __shared__ float sB[C];
+    const long long c = blockIdx.x / p.H;
+    const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const SeqChunk ch = seq_chunk(p, c);
+    if (ch.rows == 0) return;
+    for (int i = tid; i < C * (DK / 8); i += 128) {
+        const int r = i / (DK / 8), col = i % (DK / 8) * 8, on = r < ch.rows ? 16 : 0;
+        const long long row = ch.first + (on ? r : 0);
+        cp_async16(&sK[r][col], (const bf16 *)p.k + row * p.k_stride + (size_t)hk * DK + col, on);
+        cp_async16(&sQ[r][col], (const bf16 *)p.q + row * p.q_stride + (size_t)hk * DK + col, on);
+    }
+    sm100::cp_async_commit();
+    const size_t idx = (size_t)c * p.H + h;
+    if (warp == 0) {  // two tokens a lane: prefix sums of log alpha in 64 bits (decays are differences of them)
+        double g[2];
+        float b[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * lane + e;
+            const size_t at = (size_t)(ch.first + i) * p.H + h;
+            g[e] = i < ch.rows ? fmax(log_gate<double>(p.alpha[at]), (double)floor_log) : 0.0;
+            b[e] = i < ch.rows ? p.beta[at] : 0.f;
+        }
+        double run = g[0] + g[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += y;
+        }
+        const double total = __shfl_sync(0xffffffffu, run, 31);
+        const double G[2] = {run - g[1], run};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * lane + e;
+            sG[i] = G[e];
+            sB[i] = b[e];
+            w.gates[idx * 3 * C + i] = expf((float)G[e]);
+            w.gates[idx * 3 * C + C + i] = expf((float)(total - G[e]));
+            w.gates[idx * 3 * C + 2 * C + i] = b[e];
+        }
+    }
+    sm100::cp_async_wait_all();
+    __syncthreads();
+    // warp: rows 16 warp .. + 15; columns up to the diagonal
+    float kk[8][4] = {}, qk[8][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < NF; ++ks) {
+        uint32_t a[4], q[4];
+        ldsm4(a, a_row(&sK[0][0], PK, 16 * warp, 16 * ks, lane));
+        ldsm4(q, a_row(&sQ[0][0], PK, 16 * warp, 16 * ks, lane));
+#pragma unroll
+        for (int t = 0; t < 8; t += 2) {
+            if (t > 2 * warp) continue;
+            uint32_t b[4];
+            ldsm4(b, b_row(&sK[0][0], PK, 8 * t, 8 * t + 8, 16 * ks, lane));
+            mma::mma(kk[t], a, b[0], b[1]);
+            mma::mma(kk[t + 1], a, b[2], b[3]);
+            mma::mma(qk[t], q, b[0], b[1]);
+            mma::mma(qk[t + 1], q, b[2], b[3]);
+        }
+    }
+    // the decays; A to shared memory; P's terms to memory (Pt's pairs lie along the rows: it goes through shared memory)
+    __syncthreads();
+    const int i0 = 16 * warp + lane / 4, j0 = 2 * (lane & 3);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + (e >> 1) * 8, j = 8 * t + j0 + (e & 1);
+            if (t / 2 > warp) {
+                sA[i][j] = 0.f;
+                continue;
+            }
+            const float gam = j <= i ? expf((float)(sG[i] - sG[j])) : 0.f;
+            qk[t][e] *= gam;
+            sA[i][j] = j < i ? sB[i] * gam * kk[t][e] : 0.f;
+        }
+    }
+    auto put_unit = [&](uint2 *dst, int unit, float x0, float x1, float y0, float y1) {
+        uint32_t a[3], b[3];
+        split(x0, x1, a);
+        split(y0, y1, b);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) dst[((idx * kUnits + unit) * 3 + e) * 32 + lane] = make_uint2(a[e], b[e]);
+    };
+    if (w.P) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (b > warp) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                put_unit(w.P, low_unit(2 * warp + half) + b, qk[2 * b][2 * half], qk[2 * b][2 * half + 1], qk[2 * b + 1][2 * half],
+                         qk[2 * b + 1][2 * half + 1]);
+        }
+    }
+    __syncthreads();
+    // (I + A)^-1 in place, by halves: the four 16 x 16 diagonal blocks first, a column a thread
+    if (tid < C) {
+        const int o = tid & ~15, col = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == col ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) s = fmaf(-sA[o + i][o + j], x[j], s);
+            x[i] = s;  // rows above the diagonal come out as zeros
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sA[o + i][o + col] = x[i];
+    }
+    // T21 = -T22 (A21 T11), blocks of 16 then of 32.  A thread has 4 x W columns-rows of the product
+    __syncthreads();
+    {
+        const int pair = tid >> 6, e = tid & 63, o = 32 * pair, r = e / 16 * 4, col = e % 16;
+        float m[4] = {};
+        for (int k = 0; k < 16; ++k) {
+            const float b = sA[o + k][o + col];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = fmaf(sA[o + 16 + r + i][o + k], b, m[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sA[o + 16 + r + i][o + col] = m[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = 0.f;
+        for (int k = 0; k < 16; ++k) {
+            const float b = sA[o + 16 + k][o + col];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = fmaf(-sA[o + 16 + r + i][o + 16 + k], b, m[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sA[o + 16 + r + i][o + col] = m[i];
+    }
+    __syncthreads();
+    {
+        const int r = tid / 16 * 4, col = tid % 16 * 2;
+        float m[4][2] = {};
+        for (int k = 0; k < 32; ++k) {
+            const float b0 = sA[k][col], b1 = sA[k][col + 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = sA[32 + r + i][k];
+                m[i][0] = fmaf(a, b0, m[i][0]);
+                m[i][1] = fmaf(a, b1, m[i][1]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sA[32 + r + i][col] = m[i][0], sA[32 + r + i][col + 1] = m[i][1];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i][0] = m[i][1] = 0.f;
+        for (int k = 0; k < 32; ++k) {
+            const float b0 = sA[32 + k][col], b1 = sA[32 + k][col + 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = -sA[32 + r + i][32 + k];
+                m[i][0] = fmaf(a, b0, m[i][0]);
+                m[i][1] = fmaf(a, b1, m[i][1]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sA[32 + r + i][col] = m[i][0], sA[32 + r + i][col + 1] = m[i][1];
+    }
+    __syncthreads();
+    const int n = lane / 4, k2 = 2 * (lane & 3);
+    for (int t = 2 * warp; t < 2 * warp + 2; ++t) {
+        for (int b = 0; b <= t / 2; ++b) {
+            const float *x = &sA[8 * t + n][16 * b + k2];
+            put_unit(w.T, low_unit(t) + b, x[0], x[1], x[8], x[9]);
+        }
+        if (w.Tt)
+            for (int b = t / 2; b < 4; ++b) {
+                const int i = 16 * b + k2, j = 8 * t + n;
+                put_unit(w.Tt, up_unit(t) + b - t / 2, sA[i][j], sA[i + 1][j], sA[i + 8][j], sA[i + 9][j]);
+            }
+    }
+    if (w.Pt) {
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            if (t / 2 > warp) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sA[i0 + (e >> 1) * 8][8 * t + j0 + (e & 1)] = qk[t][e];
+        }
+        __syncthreads();
+        for (int t = 2 * warp; t < 2 * warp + 2; ++t)
+            for (int b = t / 2; b < 4; ++b) {
+                const int i = 16 * b + k2, j = 8 * t + n;
+                put_unit(w.Pt, up_unit(t) + b - t / 2, sA[i][j], sA[i + 1][j], sA[i + 8][j], sA[i + 9][j]);
+            }
+    }
+}
+
+template <int NF> struct ChainSmem {
+    static constexpr int PK = 16 * NF + 8;
+    bf16 K[2][C][PK], Q[2][C][PK];
+    bf16 V[2][C][PV];          // v, or do
+    float gates[2][3][C];
+    bf16 S[3][NV][PK];         // the state's terms
+    bf16 R[3][NV][PC];
+    bf16 U[6][NV][PC];
+};
+
+// A chunk's rows into buffer b: K, Q (where wanted), 16 columns of v (or do), the gates.
+template <int NF>
+__device__ __forceinline__ void chain_fetch(ChainSmem<NF> &sm, int b, const SeqProblem &p, const ChunkWork &w, long long row,
+                                            int rows, size_t idx, int hk, bool with_q, const bf16 *v, long long v_stride) {
+    constexpr int DK = 16 * NF;
+    for (int i = threadIdx.x; i < C * (DK / 8); i += 128) {
+        const int r = i / (DK / 8), col = i % (DK / 8) * 8, on = r < rows ? 16 : 0;
+        const long long at = row + (on ? r : 0);
+        cp_async16(&sm.K[b][r][col], (const bf16 *)p.k + at * p.k_stride + (size_t)hk * DK + col, on);
+        if (with_q) cp_async16(&sm.Q[b][r][col], (const bf16 *)p.q + at * p.q_stride + (size_t)hk * DK + col, on);
+    }
+    const int r = threadIdx.x / 2, col = threadIdx.x % 2 * 8, on = r < rows ? 16 : 0;
+    cp_async16(&sm.V[b][r][col], v + (row + (on ? r : 0)) * v_stride + col, on);
+    if (threadIdx.x < 48) cp_async16(&sm.gates[b][0][0] + threadIdx.x * 4, w.gates + idx * 3 * C + threadIdx.x * 4, 16);
+    sm100::cp_async_commit();
+}
+
+// One warp's fragments of T or P (units of the n-tiles t0 = warp and t1 = 7 - warp).
+template <int TERMS> struct Frags {
+    uint2 a[2][TERMS], b[4][TERMS];  // the shorter tile has at most 2 blocks, the longer one 4
+};
+// units of a lower triangle: tile t has blocks 0 .. t / 2
+template <int TERMS>
+__device__ __forceinline__ void load_low(Frags<TERMS> &f, const uint2 *src, int warp, int lane) {
+    const int t1 = 7 - warp;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e)
+            if (b <= warp / 2) f.a[b][e] = src[((low_unit(warp) + b) * 3 + e) * 32 + lane];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e)
+            if (b <= t1 / 2) f.b[b][e] = src[((low_unit(t1) + b) * 3 + e) * 32 + lane];
+}
+// units of an upper triangle, from the last block down: f.b is tile warp's, f.a tile (7 - warp)'s
+template <int TERMS>
+__device__ __forceinline__ void load_up(Frags<TERMS> &f, const uint2 *src, int warp, int lane) {
+    const int t1 = 7 - warp;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e)
+            if (3 - b >= t1 / 2) f.a[b][e] = src[((up_unit(t1) + 3 - b - t1 / 2) * 3 + e) * 32 + lane];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e)
+            if (3 - b >= warp / 2) f.b[b][e] = src[((up_unit(warp) + 3 - b - warp / 2) * 3 + e) * 32 + lane];
+}
+
+// hi += a0 b0; lo += the other products of AT terms of a with BT of b that are above 2^-24
+template <int AT, int BT>
+__device__ __forceinline__ void mma_split(float (&hi)[4], float (&lo)[4], const uint32_t (&a)[AT][4], const uint2 (&b)[BT]) {
+    mma::mma(hi, a[0], b[0].x, b[0].y);
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int j = 0; j < BT; ++j)
+            if (i + j > 0 && i + j < (AT > BT ? AT : BT)) mma::mma(lo, a[i], b[j].x, b[j].y);
+}
+
+// Sum over the lanes that hold the other rows of the same columns.
+__device__ __forceinline__ float rows_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// The S (or D^T) rows of a block: warp w has the column pairs (16 columns) w and w + 4.
+template <int NF> struct StateRows {
+    float x[2][2][4];
+    template <typename F> __device__ __forceinline__ void each(int warp, int lane, F &&f) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (warp + 4 * m >= NF) continue;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    f(lane / 4 + 8 * half, 16 * (warp + 4 * m) + 8 * t + 2 * (lane & 3), x[m][t][2 * half], x[m][t][2 * half + 1]);
+        }
+    }
+};
+template <int NF> __device__ __forceinline__ void put_state(ChainSmem<NF> &sm, StateRows<NF> &st, int warp, int lane) {
+    st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+        uint32_t t[3];
+        split(x, y, t);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t *>(&sm.S[e][n][col]) = t[e];
+    });
+}
+
+// st = decay st + sum over the planes pl: (plane's 3 terms [16][64 tokens]) x (rows [64 tokens][dk])
+template <int NF, int SETS>
+__device__ __forceinline__ void update_state(StateRows<NF> &st, float decay, const bf16 (*const (&planes)[SETS])[NV][PC],
+                                             const bf16 *const (&rows)[SETS], int warp, int lane) {
+    constexpr int PK = 16 * NF + 8;
+    float hi[2][2][4] = {}, lo[2][2][4] = {};
+#pragma unroll
+    for (int s = 0; s < SETS; ++s)
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+            uint32_t a[3][4];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&planes[s][e][0][0], PC, 0, 16 * kb, lane));
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (warp + 4 * m >= NF) continue;
+                uint32_t b[4];
+                ldsm4_t(b, bt_row(rows[s], PK, 16 * kb, 16 * (warp + 4 * m), lane));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    mma::mma(hi[m][t], a[0], b[2 * t], b[2 * t + 1]);
+                    mma::mma(lo[m][t], a[1], b[2 * t], b[2 * t + 1]);
+                    mma::mma(lo[m][t], a[2], b[2 * t], b[2 * t + 1]);
+                }
+            }
+        }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.x[m][t][e] = fmaf(decay, st.x[m][t][e], hi[m][t][e] + lo[m][t][e]);
+}
+
+// SAVE: the pass that gdn_bwd makes (no O; Sig, U and X of every chunk are kept).
+template <int NF, bool SAVE>
+__global__ void __launch_bounds__(128, 2) k_chunk_fwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w) {
+    constexpr int DK = 16 * NF, PK = DK + 8;
+    extern __shared__ __align__(16) unsigned char raw[];
+    ChainSmem<NF> &sm = *reinterpret_cast<ChainSmem<NF> *>(raw);
+    const int groups = p.dv / NV, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
+    const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const SeqRange r = seq_range(p, s);
+    seq_report(p, r, blockIdx.x % (p.H * groups) == 0 && threadIdx.x == 0);
+    if (r.slot < 0) return;
+    const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);
+    const size_t soff = (((size_t)r.slot * p.H + h) * p.dv + c0) * DK;
+    const bf16 *v = (const bf16 *)p.v + (size_t)h * p.dv + c0;
+    auto fetch = [&](long long c, int b) {
+        chain_fetch(sm, b, p, w, r.first + c * C, (int)min((long long)C, r.len - c * C), (size_t)(base + c) * p.H + h, hk, !SAVE, v,
+                    p.v_stride);
+    };
+    if (n_chunks > 0) fetch(0, 0);
+    StateRows<NF> st = {};
+    if (!seq_starts_zero(p, s))
+        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+            const float2 t = *reinterpret_cast<const float2 *>(p.S_in + soff + (size_t)n * DK + col);
+            x = t.x;
+            y = t.y;
+        });
+    put_state(sm, st, warp, lane);
+    const int t0 = warp, t1 = 7 - warp;  // this warp's token tiles (8 tokens each)
+    for (long long c = 0; c < n_chunks; ++c) {
+        const int b = (int)(c & 1);
+        const size_t idx = (size_t)(base + c) * p.H + h;
+        const long long row = r.first + c * C;
+        const int rows = (int)min((long long)C, r.len - c * C);
+        sm100::cp_async_wait_all();
+        __syncthreads();  // this chunk's rows and the state's terms are there; the other buffer has been read
+        if (c + 1 < n_chunks) fetch(c + 1, b ^ 1);
+        Frags<3> T;
+        load_low(T, w.T + idx * kUnits * 96, warp, lane);
+        Frags<2> P;
+        if (!SAVE) load_low(P, w.P + idx * kUnits * 96, warp, lane);
+        if (SAVE)
+            st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+                *reinterpret_cast<float2 *>(w.Sig + (idx * p.dv + c0 + n) * DK + col) = make_float2(x, y);
+            });
+        // X^T = S [K; Q]^T
+        float kh[2][4] = {}, kl[2][4] = {}, qh[2][4] = {}, ql[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < NF; ++ks) {
+            uint32_t a[3][4], k[4];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.S[e][0][0], PK, 0, 16 * ks, lane));
+            ldsm4(k, b_row(&sm.K[b][0][0], PK, 8 * t0, 8 * t1, 16 * ks, lane));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                mma::mma(kh[t], a[0], k[2 * t], k[2 * t + 1]);
+                mma::mma(kl[t], a[1], k[2 * t], k[2 * t + 1]);
+                mma::mma(kl[t], a[2], k[2 * t], k[2 * t + 1]);
+            }
+            if (!SAVE) {
+                uint32_t q[4];
+                ldsm4(q, b_row(&sm.Q[b][0][0], PK, 8 * t0, 8 * t1, 16 * ks, lane));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    mma::mma(qh[t], a[0], q[2 * t], q[2 * t + 1]);
+                    mma::mma(ql[t], a[1], q[2 * t], q[2 * t + 1]);
+                }
+            }
+        }
+        // beta Y's terms
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
+            const float2 eg = *reinterpret_cast<const float2 *>(&sm.gates[b][0][tok]);
+            const float2 be = *reinterpret_cast<const float2 *>(&sm.gates[b][2][tok]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int n = lane / 4 + 8 * half;
+                const float x = eg.x * (kh[t][2 * half] + kl[t][2 * half]), y = eg.y * (kh[t][2 * half + 1] + kl[t][2 * half + 1]);
+                if (SAVE) *reinterpret_cast<float2 *>(w.X + (idx * p.dv + c0 + n) * C + tok) = make_float2(x, y);
+                uint32_t e[3];
+                split(be.x * (__bfloat162float(sm.V[b][tok][n]) - x), be.y * (__bfloat162float(sm.V[b][tok + 1][n]) - y), e);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.R[i][n][tok]) = e[i];
+            }
+        }
+        __syncthreads();
+        // U^T = (beta Y)^T T^T
+        float uh[2][4] = {}, ul[2][4] = {};
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+            if (kb > t1 / 2) continue;
+            uint32_t a[3][4];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.R[e][0][0], PC, 0, 16 * kb, lane));
+            if (kb < 2 && kb <= t0 / 2) mma_split<3, 3>(uh[0], ul[0], a, T.a[kb < 2 ? kb : 0]);
+            mma_split<3, 3>(uh[1], ul[1], a, T.b[kb]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
+            const float2 el = *reinterpret_cast<const float2 *>(&sm.gates[b][1][tok]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int n = lane / 4 + 8 * half;
+                const float x = uh[t][2 * half] + ul[t][2 * half], y = uh[t][2 * half + 1] + ul[t][2 * half + 1];
+                if (SAVE) *reinterpret_cast<float2 *>(w.U + (idx * p.dv + c0 + n) * C + tok) = make_float2(x, y);
+                uint32_t e[3];
+                split(el.x * x, el.y * y, e);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.U[i][n][tok]) = e[i];
+                if (!SAVE) {
+                    uint32_t u[2];
+                    split(x, y, u);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint32_t *>(&sm.U[3 + i][n][tok]) = u[i];
+                }
+            }
+        }
+        __syncthreads();
+        const bf16(*const planes[1])[NV][PC] = {sm.U};
+        const bf16 *const krows[1] = {&sm.K[b][0][0]};
+        update_state<NF, 1>(st, sm.gates[b][0][C - 1], planes, krows, warp, lane);
+        put_state(sm, st, warp, lane);
+        if (!SAVE) {
+            float oh[2][4] = {}, ol[2][4] = {};
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb > t1 / 2) continue;
+                uint32_t a[2][4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) ldsm4(a[e], a_row(&sm.U[3 + e][0][0], PC, 0, 16 * kb, lane));
+                if (kb < 2 && kb <= t0 / 2) mma_split<2, 2>(oh[0], ol[0], a, P.a[kb < 2 ? kb : 0]);
+                mma_split<2, 2>(oh[1], ol[1], a, P.b[kb]);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = tok + (e & 1), n = lane / 4 + 8 * (e >> 1);
+                    if (i < rows)
+                        ((bf16 *)p.o)[((row + i) * p.H + h) * p.dv + c0 + n] =
+                            __float2bfloat16_rn(fmaf(sm.gates[b][0][i], qh[t][e] + ql[t][e], oh[t][e] + ol[t][e]));
+                }
+            }
+        }
+    }
+    if (!SAVE && p.S_out)
+        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+            *reinterpret_cast<float2 *>(p.S_out + soff + (size_t)n * DK + col) = make_float2(x, y);
+        });
+}
+
+template <int NF>
+__global__ void __launch_bounds__(128, 2) k_chunk_bwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w) {
+    constexpr int DK = 16 * NF, PK = DK + 8;
+    extern __shared__ __align__(16) unsigned char raw[];
+    ChainSmem<NF> &sm = *reinterpret_cast<ChainSmem<NF> *>(raw);
+    const int groups = p.dv / NV, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
+    const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const SeqRange r = seq_rows(p, s);
+    const size_t soff = (((size_t)s * p.H + h) * p.dv + c0) * DK;
+    StateRows<NF> st = {};
+    if (r.slot >= 0 && p.dS_out)
+        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+            const float2 t = *reinterpret_cast<const float2 *>(p.dS_out + soff + (size_t)n * DK + col);
+            x = t.x;
+            y = t.y;
+        });
+    const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);  // 0 of a bad range
+    const bf16 *d_o = (const bf16 *)p.d_o + (size_t)h * p.dv + c0;
+    auto fetch = [&](long long c, int b) {
+        chain_fetch(sm, b, p, w, r.first + c * C, (int)min((long long)C, r.len - c * C), (size_t)(base + c) * p.H + h, hk, true, d_o,
+                    (long long)p.H * p.dv);
+    };
+    if (n_chunks > 0) fetch(n_chunks - 1, (int)((n_chunks - 1) & 1));
+    put_state(sm, st, warp, lane);
+    const int t0 = warp, t1 = 7 - warp;
+    for (long long c = n_chunks - 1; c >= 0; --c) {
+        const int b = (int)(c & 1);
+        const size_t idx = (size_t)(base + c) * p.H + h;
+        const long long row = r.first + c * C;
+        const int rows = (int)min((long long)C, r.len - c * C);
+        sm100::cp_async_wait_all();
+        __syncthreads();
+        if (c > 0) fetch(c - 1, b ^ 1);
+        Frags<3> P, T;  // .b: tile t0's blocks from the last one down, .a: tile t1's
+        load_up(P, w.Pt + idx * kUnits * 96, warp, lane);
+        load_up(T, w.Tt + idx * kUnits * 96, warp, lane);
+        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+            *reinterpret_cast<float2 *>(w.D + (idx * p.dv + c0 + n) * DK + col) = make_float2(x, y);
+        });
+        // D^T K^T, and dO^T P
+        float zh[2][4] = {}, zl[2][4] = {}, ph[2][4] = {}, pl[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < NF; ++ks) {
+            uint32_t a[3][4], k[4];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.S[e][0][0], PK, 0, 16 * ks, lane));
+            ldsm4(k, b_row(&sm.K[b][0][0], PK, 8 * t0, 8 * t1, 16 * ks, lane));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                mma::mma(zh[t], a[0], k[2 * t], k[2 * t + 1]);
+                mma::mma(zl[t], a[1], k[2 * t], k[2 * t + 1]);
+                mma::mma(zl[t], a[2], k[2 * t], k[2 * t + 1]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {  // blocks 3 - m
+            const int kb = 3 - m;
+            if (kb < t0 / 2) continue;
+            uint32_t a[1][4];
+            ldsm4_t(a[0], at_row(&sm.V[b][0][0], PV, 16 * kb, 0, lane));
+            mma_split<1, 3>(ph[0], pl[0], a, P.b[m]);
+            if (m < 2 && kb >= t1 / 2) mma_split<1, 3>(ph[1], pl[1], a, P.a[m < 2 ? m : 0]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
+            const float2 el = *reinterpret_cast<const float2 *>(&sm.gates[b][1][tok]);
+            const float2 eg = *reinterpret_cast<const float2 *>(&sm.gates[b][0][tok]);
+            float past0 = 0.f, past1 = 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int n = lane / 4 + 8 * half;
+                const float zx = el.x * (zh[t][2 * half] + zl[t][2 * half]), zy = el.y * (zh[t][2 * half + 1] + zl[t][2 * half + 1]);
+                const float2 u = *reinterpret_cast<const float2 *>(w.U + (idx * p.dv + c0 + n) * C + tok);
+                past0 = fmaf(u.x, zx, past0);
+                past1 = fmaf(u.y, zy, past1);
+                uint32_t e[3];
+                split(zx + (ph[t][2 * half] + pl[t][2 * half]), zy + (ph[t][2 * half + 1] + pl[t][2 * half + 1]), e);  // dU
+#pragma unroll
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.R[i][n][tok]) = e[i];
+                split(eg.x * __bfloat162float(sm.V[b][tok][n]), eg.y * __bfloat162float(sm.V[b][tok + 1][n]), e);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.U[i][n][tok]) = e[i];
+            }
+            past0 = rows_sum(past0);
+            past1 = rows_sum(past1);
+            if (lane < 4) *reinterpret_cast<float2 *>(w.past + (idx * groups + c0 / NV) * C + tok) = make_float2(past0, past1);
+        }
+        __syncthreads();
+        // dR^T = dU^T T
+        float rh[2][4] = {}, rl[2][4] = {};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int kb = 3 - m;
+            if (kb < t0 / 2) continue;
+            uint32_t a[3][4];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.R[e][0][0], PC, 0, 16 * kb, lane));
+            mma_split<3, 3>(rh[0], rl[0], a, T.b[m]);
+            if (m < 2 && kb >= t1 / 2) mma_split<3, 3>(rh[1], rl[1], a, T.a[m < 2 ? m : 0]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
+            const float2 eg = *reinterpret_cast<const float2 *>(&sm.gates[b][0][tok]);
+            const float2 be = *reinterpret_cast<const float2 *>(&sm.gates[b][2][tok]);
+            float into0 = 0.f, into1 = 0.f, db0 = 0.f, db1 = 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int n = lane / 4 + 8 * half;
+                const float x = rh[t][2 * half] + rl[t][2 * half], y = rh[t][2 * half + 1] + rl[t][2 * half + 1];
+                const size_t at = (idx * p.dv + c0 + n) * C + tok;
+                *reinterpret_cast<float2 *>(w.dR + at) = make_float2(x, y);
+                const float2 X = *reinterpret_cast<const float2 *>(w.X + at);
+                const bf16 *vp = (const bf16 *)p.v + (row + tok) * p.v_stride + (size_t)h * p.dv + c0 + n;
+                bf16 *dvp = (bf16 *)p.dv_out + ((row + tok) * p.H + h) * p.dv + c0 + n;
+                const float bx = be.x * x, by = be.y * y;
+                into0 = fmaf(-bx, X.x, into0);
+                into1 = fmaf(-by, X.y, into1);
+                if (tok < rows) {
+                    db0 = fmaf(x, __bfloat162float(vp[0]) - X.x, db0);
+                    dvp[0] = __float2bfloat16_rn(bx);
+                }
+                if (tok + 1 < rows) {
+                    db1 = fmaf(y, __bfloat162float(vp[p.v_stride]) - X.y, db1);
+                    dvp[(size_t)p.H * p.dv] = __float2bfloat16_rn(by);
+                }
+                uint32_t e[3];
+                split(-eg.x * bx, -eg.y * by, e);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.U[3 + i][n][tok]) = e[i];
+            }
+            into0 = rows_sum(into0);
+            into1 = rows_sum(into1);
+            db0 = rows_sum(db0);
+            db1 = rows_sum(db1);
+            if (lane < 4) {
+                *reinterpret_cast<float2 *>(w.into + (idx * groups + c0 / NV) * C + tok) = make_float2(into0, into1);
+                *reinterpret_cast<float2 *>(w.db + (idx * groups + c0 / NV) * C + tok) = make_float2(db0, db1);
+            }
+        }
+        __syncthreads();
+        const bf16(*const planes[2])[NV][PC] = {sm.U, sm.U + 3};
+        const bf16 *const mrows[2] = {&sm.Q[b][0][0], &sm.K[b][0][0]};
+        update_state<NF, 2>(st, sm.gates[b][0][C - 1], planes, mrows, warp, lane);
+        put_state(sm, st, warp, lane);
+    }
+    if (p.dS_in)
+        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+            *reinterpret_cast<float2 *>(p.dS_in + soff + (size_t)n * DK + col) = make_float2(x, y);
+        });
+}
+
+template <int NF> cudaError_t prep(const SeqProblem &p, const ChunkWork &w, float floor_log, cudaStream_t s) {
+    const unsigned blocks = (unsigned)(seq_max_chunks(p) * p.H);
+    if (blocks) k_prep<NF><<<blocks, 128, 0, s>>>(p, w, floor_log);
+    return cudaGetLastError();
+}
+
+template <typename K, int NF> cudaError_t chain(K kernel, const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
+    const int bytes = (int)sizeof(ChainSmem<NF>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e) return e;
+    kernel<<<(unsigned)((long long)p.n_seqs * p.H * (p.dv / NV)), 128, bytes, s>>>(p, w);
+    return cudaGetLastError();
+}
+
+template <int NF> cudaError_t fwd(const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
+    cudaError_t e = prep<NF>(p, w, kLogAlphaFloor, s);
+    return e ? e : chain<decltype(&k_chunk_fwd<NF, false>), NF>(k_chunk_fwd<NF, false>, p, w, s);
+}
+
+ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
+    const size_t n = (size_t)seq_max_chunks(p) * p.H;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char *x = (char *)base + at;
+        at += align256(bytes);
+        return x;
+    };
+    const size_t frags = n * kUnits * 3 * 32 * sizeof(uint2);
+    ChunkWork w = {};
+    w.T = (uint2 *)take(frags);
+    w.gates = (float *)take(n * 3 * C * 4);
+    if (!bwd) w.P = (uint2 *)take(frags);
+    if (total) *total = at;
+    return w;
+}
+
+}  // namespace
+
+size_t seq_chunk_workspace(const SeqProblem &p) {
+    size_t n;
+    carve(p, nullptr, false, &n);
+    return n;
+}
+
+cudaError_t launch_seq_chunk(const SeqProblem &p, void *ws, cudaStream_t s) {
+    const ChunkWork w = carve(p, ws, false, nullptr);
+    switch (p.dk / 16) {
+        case 1: return fwd<1>(p, w, s);
+        case 2: return fwd<2>(p, w, s);
+        case 3: return fwd<3>(p, w, s);
+        case 4: return fwd<4>(p, w, s);
+        case 5: return fwd<5>(p, w, s);
+        case 6: return fwd<6>(p, w, s);
+        case 7: return fwd<7>(p, w, s);
+        default: return fwd<8>(p, w, s);
+    }
+}
+
+}  // namespace gdn

@@ -141,6 +141,10 @@ cudaError_t launch_seq_zero_rows(const SeqProblem &p, float *dqh, float *dkh, cu
 // dq, dk from the heads' dqh, dkh.
 cudaError_t launch_seq_share(const SeqProblem &p, const SeqWork &w, cudaStream_t s);
 
+// gdn_packed in chunks on the tensor cores, bf16 q, k, v (seq_chunk.cu).
+size_t seq_chunk_workspace(const SeqProblem &p);
+cudaError_t launch_seq_chunk(const SeqProblem &p, void *ws, cudaStream_t s);
+
 // The recurrent form (seq_recurrent.cu).  `few`: one or a few tokens of each sequence.
 cudaError_t launch_seq_recurrent(const SeqProblem &p, bool few, cudaStream_t s);
 
