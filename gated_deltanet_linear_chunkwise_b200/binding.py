@@ -77,6 +77,7 @@ class GdnSeqArgs(ctypes.Structure):
 GDN_SEQ_BAD_SLOT = 1
 GDN_SEQ_SAME_SLOT = 2
 GDN_SEQ_BAD_ROWS = 4
+GDN_SEQ_TIMEOUT = 8
 
 GDN_MODE_TOKEN = 0
 GDN_MODE_FRAME = 1

@@ -135,7 +135,7 @@ int check(const gdn_seq_args &a, Which which, gdn::SeqProblem &p) {
 }
 
 // Which form serves a gdn_packed call: the tensor cores take bf16 operands.
-bool chunked(const gdn::SeqProblem &p) { return p.dtype == GDN_DTYPE_BF16; }
+bool chunked(const gdn::SeqProblem &p) { return p.dtype == GDN_DTYPE_BF16 && p.n_tokens > 0; }
 
 size_t workspace_for(const gdn::SeqProblem &p, Which which) {
     if (which == kBwd) return gdn::seq_bwd_workspace(p, nullptr, nullptr);

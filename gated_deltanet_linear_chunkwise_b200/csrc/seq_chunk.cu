@@ -21,6 +21,7 @@
 // K and Q against N = 16 here and is bound by its A operand's shared memory reads (128 rows x 16 x 2 bytes at
 // 128 B/clk: 32 clk an instruction, as long as the 16 warp products that it replaces), and pays a
 // round trip through tensor memory for each of three dependent products of a step.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "gates.cuh"
@@ -28,6 +29,9 @@
 #include "seq_mma.cuh"
 
 namespace gdn {
+
+bool seq_row_map(CUtensorMap *m, const void *x, long long rows, long long row_stride, int heads, int d, int cols);  // gdn_tc.cu
+
 namespace {
 
 using namespace mma;
@@ -36,45 +40,45 @@ using sm100::cp_async16;
 constexpr int C = kSeqChunk;
 constexpr int NV = 16;       // rows of S (columns of d_v) that a block holds
 constexpr int PC = C + 8;    // pitch of a [16][64] plane: 9 x 16 bytes, odd, so ldmatrix rows spread over the banks
-constexpr int PV = NV + 8;
 
-// T and P lie in the order of the B operand's fragments: unit (t, b) is the n-tile of 8 tokens
-// from 8t against the 16 tokens from 16b, 3 terms, a lane's two words of each.  Below the
-// diagonal b <= t / 2 (20 units), above it (the transposes) b >= t / 2.
+// T and P lie in the order of the B operand's fragments, a term behind the other: unit (t, b) is the n-tile of 8
+// tokens from 8t against the 16 tokens from 16b, a lane's two words of it.  Below the diagonal b <= t / 2 (20
+// units), above it (the transposes) b >= t / 2.  P reaches O only and has two terms; T and the transposes have three.
 __host__ __device__ constexpr int low_unit(int t) { return (t / 2) * (t / 2 + 1) + (t & 1) * (t / 2 + 1); }
 __host__ __device__ constexpr int up_unit(int t) { return 20 - low_unit(8 - t) ; }
 constexpr int kUnits = 20;
 
 struct ChunkWork {
-    uint2 *T, *P, *Tt, *Pt;  // [chunk x H][20][3][32]; P or the transposes may be null
+    uint2 *T, *P, *Tt, *Pt;  // [chunk x H][terms][20][32]; P or the transposes may be null
     float *gates;            // [chunk x H][3][64]: e^G, e^{G_L - G}, beta
     float *Sig, *D;          // [chunk x H][dv][dk]
     float *U, *X, *dR;       // [chunk x H][dv][64]: X = e^G K Sig
     float *past, *into, *db; // [chunk x H][dv / 16][64]: a slice's part of the gates' gradients
     float *dqh, *dkh;        // as in SeqWork
+    int *err;                // a bounded wait that gave up (k_prep clears it)
 };
 
 template <int NF>
 __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
                                               const float floor_log) {
-    constexpr int DK = 16 * NF, PK = DK + 8;
+    constexpr int DK = 16 * NF, kTile = (DK + 63) / 64 * C * 64;
     // K and Q, and in their place, once they have been multiplied, A and its inverse
-    constexpr int kRows = 2 * C * PK * (int)sizeof(bf16), kMat = C * (C + 1) * (int)sizeof(float);
+    constexpr int kRows = 2 * kTile * (int)sizeof(bf16), kMat = C * (C + 1) * (int)sizeof(float);
     __shared__ __align__(16) unsigned char room[kRows > kMat ? kRows : kMat];
-    bf16(*const sK)[PK] = reinterpret_cast<bf16(*)[PK]>(room);
-    bf16(*const sQ)[PK] = sK + C;
+    bf16 *const sK = reinterpret_cast<bf16 *>(room), *const sQ = sK + kTile;
     float(*const sA)[C + 1] = reinterpret_cast<float(*)[C + 1]>(room);
     __shared__ double sG[C];
     __shared__ float sB[C];
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0 && tid == 0) *w.err = 0;
     const SeqChunk ch = seq_chunk(p, c);
     if (ch.rows == 0) return;
     for (int i = tid; i < C * (DK / 8); i += 128) {
         const int r = i / (DK / 8), col = i % (DK / 8) * 8, on = r < ch.rows ? 16 : 0;
         const long long row = ch.first + (on ? r : 0);
-        cp_async16(&sK[r][col], (const bf16 *)p.k + row * p.k_stride + (size_t)hk * DK + col, on);
-        cp_async16(&sQ[r][col], (const bf16 *)p.q + row * p.q_stride + (size_t)hk * DK + col, on);
+        cp_async16((void *)sw_piece(sK, C, r, col), (const bf16 *)p.k + row * p.k_stride + (size_t)hk * DK + col, on);
+        cp_async16((void *)sw_piece(sQ, C, r, col), (const bf16 *)p.q + row * p.q_stride + (size_t)hk * DK + col, on);
     }
     sm100::cp_async_commit();
     const size_t idx = (size_t)c * p.H + h;
@@ -113,13 +117,13 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
 #pragma unroll
     for (int ks = 0; ks < NF; ++ks) {
         uint32_t a[4], q[4];
-        ldsm4(a, a_row(&sK[0][0], PK, 16 * warp, 16 * ks, lane));
-        ldsm4(q, a_row(&sQ[0][0], PK, 16 * warp, 16 * ks, lane));
+        ldsm4(a, sw_piece(sK, C, 16 * warp + (lane & 15), 16 * ks + (lane >> 4) * 8));
+        ldsm4(q, sw_piece(sQ, C, 16 * warp + (lane & 15), 16 * ks + (lane >> 4) * 8));
 #pragma unroll
         for (int t = 0; t < 8; t += 2) {
             if (t > 2 * warp) continue;
             uint32_t b[4];
-            ldsm4(b, b_row(&sK[0][0], PK, 8 * t, 8 * t + 8, 16 * ks, lane));
+            ldsm4(b, b_row(sK, C, 8 * t, 8 * t + 8, 16 * ks, lane));
             mma::mma(kk[t], a, b[0], b[1]);
             mma::mma(kk[t + 1], a, b[2], b[3]);
             mma::mma(qk[t], q, b[0], b[1]);
@@ -143,12 +147,13 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
             sA[i][j] = j < i ? sB[i] * gam * kk[t][e] : 0.f;
         }
     }
-    auto put_unit = [&](uint2 *dst, int unit, float x0, float x1, float y0, float y1) {
+    auto put_unit = [&](uint2 *dst, int terms, int unit, float x0, float x1, float y0, float y1) {
         uint32_t a[3], b[3];
         split(x0, x1, a);
         split(y0, y1, b);
 #pragma unroll
-        for (int e = 0; e < 3; ++e) dst[((idx * kUnits + unit) * 3 + e) * 32 + lane] = make_uint2(a[e], b[e]);
+        for (int e = 0; e < 3; ++e)
+            if (e < terms) dst[((idx * terms + e) * kUnits + unit) * 32 + lane] = make_uint2(a[e], b[e]);
     };
     if (w.P) {
 #pragma unroll
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
             if (b > warp) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                put_unit(w.P, low_unit(2 * warp + half) + b, qk[2 * b][2 * half], qk[2 * b][2 * half + 1], qk[2 * b + 1][2 * half],
+                put_unit(w.P, 2, low_unit(2 * warp + half) + b, qk[2 * b][2 * half], qk[2 * b][2 * half + 1], qk[2 * b + 1][2 * half],
                          qk[2 * b + 1][2 * half + 1]);
         }
     }
@@ -238,12 +243,12 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
     for (int t = 2 * warp; t < 2 * warp + 2; ++t) {
         for (int b = 0; b <= t / 2; ++b) {
             const float *x = &sA[8 * t + n][16 * b + k2];
-            put_unit(w.T, low_unit(t) + b, x[0], x[1], x[8], x[9]);
+            put_unit(w.T, 3, low_unit(t) + b, x[0], x[1], x[8], x[9]);
         }
         if (w.Tt)
             for (int b = t / 2; b < 4; ++b) {
                 const int i = 16 * b + k2, j = 8 * t + n;
-                put_unit(w.Tt, up_unit(t) + b - t / 2, sA[i][j], sA[i + 1][j], sA[i + 8][j], sA[i + 9][j]);
+                put_unit(w.Tt, 3, up_unit(t) + b - t / 2, sA[i][j], sA[i + 1][j], sA[i + 8][j], sA[i + 9][j]);
             }
     }
     if (w.Pt) {
@@ -258,82 +263,121 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
         for (int t = 2 * warp; t < 2 * warp + 2; ++t)
             for (int b = t / 2; b < 4; ++b) {
                 const int i = 16 * b + k2, j = 8 * t + n;
-                put_unit(w.Pt, up_unit(t) + b - t / 2, sA[i][j], sA[i + 1][j], sA[i + 8][j], sA[i + 9][j]);
+                put_unit(w.Pt, 3, up_unit(t) + b - t / 2, sA[i][j], sA[i + 1][j], sA[i + 8][j], sA[i + 9][j]);
             }
     }
 }
 
-template <int NF> struct ChainSmem {
-    static constexpr int PK = 16 * NF + 8;
-    bf16 K[2][C][PK], Q[2][C][PK];
-    bf16 V[2][C][PV];          // v, or do
+// Shared memory of a chain block, 1024-byte aligned.  Two blocks fit an SM: only K, which is read from a step's
+// first product to its last, has two buffers; the others are fetched again as soon as they have been read.
+template <int NF, bool BWD> struct ChainSmem {
+    static constexpr int PK = 16 * NF + 8, kTile = (16 * NF + 63) / 64 * C * 64;
+    static constexpr int kTermsP = BWD ? 3 : 2;
+    bf16 K[2][kTile], Q[kTile];  // as the tensor maps leave them
+    uint2 T[3][kUnits][32], P[kTermsP][kUnits][32];
+    bf16 V[C][NV];               // v, or do
     float gates[2][3][C];
-    bf16 S[3][NV][PK];         // the state's terms
-    bf16 R[3][NV][PC];
-    bf16 U[6][NV][PC];
+    bf16 S[3][NV][PK];           // the state's terms
+    bf16 U[3][NV][PC];           // e^{G_L-G} U; backwards e^G dO
+    bf16 R[3][NV][PC];           // beta Y; backwards dU, then -beta e^G dR
+    bf16 W[BWD ? 1 : 2][NV][PC]; // U for O
+    uint64_t bar[5];             // K and gates (two), Q, V, T, P
+};
+enum { kBarK = 0, kBarV = 2, kBarT = 3, kBarP = 4 };
+constexpr int kChainThreads = 160;  // four warps, and one that fetches
+
+struct ChainMaps {
+    CUtensorMap q, k, v;  // v: v, or do
 };
 
-// A chunk's rows into buffer b: K, Q (where wanted), 16 columns of v (or do), the gates.
-template <int NF>
-__device__ __forceinline__ void chain_fetch(ChainSmem<NF> &sm, int b, const SeqProblem &p, const ChunkWork &w, long long row,
-                                            int rows, size_t idx, int hk, bool with_q, const bf16 *v, long long v_stride) {
-    constexpr int DK = 16 * NF;
-    for (int i = threadIdx.x; i < C * (DK / 8); i += 128) {
-        const int r = i / (DK / 8), col = i % (DK / 8) * 8, on = r < rows ? 16 : 0;
-        const long long at = row + (on ? r : 0);
-        cp_async16(&sm.K[b][r][col], (const bf16 *)p.k + at * p.k_stride + (size_t)hk * DK + col, on);
-        if (with_q) cp_async16(&sm.Q[b][r][col], (const bf16 *)p.q + at * p.q_stride + (size_t)hk * DK + col, on);
+// One thread's fetches (a handful of copies a chunk; as 16-byte copies by the threads they were 900 address lookups a
+// chunk in ldmatrix's way, and loads of T and P to registers made every ldmatrix wait for them: 6400 clocks a step).
+template <int NF, bool BWD> struct ChainFetch {
+    ChainSmem<NF, BWD> &sm;
+    const ChainMaps &maps;
+    const ChunkWork &w;
+    int hk, h, c0;
+    __device__ __forceinline__ void tile(bf16 *dst, const CUtensorMap *map, uint64_t *bar, int row) const {
+#pragma unroll
+        for (int c = 0; c < 16 * NF; c += 64) sm100::tma_load_3d(dst + c * C, map, bar, c, hk, row);
     }
-    const int r = threadIdx.x / 2, col = threadIdx.x % 2 * 8, on = r < rows ? 16 : 0;
-    cp_async16(&sm.V[b][r][col], v + (row + (on ? r : 0)) * v_stride + col, on);
-    if (threadIdx.x < 48) cp_async16(&sm.gates[b][0][0] + threadIdx.x * 4, w.gates + idx * 3 * C + threadIdx.x * 4, 16);
-    sm100::cp_async_commit();
-}
-
-// One warp's fragments of T or P (units of the n-tiles t0 = warp and t1 = 7 - warp).
-template <int TERMS> struct Frags {
-    uint2 a[2][TERMS], b[4][TERMS];  // the shorter tile has at most 2 blocks, the longer one 4
+    static constexpr uint32_t kTileBytes = ChainSmem<NF, BWD>::kTile * 2;
+    __device__ __forceinline__ void k(int b, int row, size_t idx) const {  // and the gates
+        uint64_t *bar = &sm.bar[kBarK + b];
+        sm100::mbar_arrive_expect_tx(bar, kTileBytes + 3 * C * 4);
+        tile(sm.K[b], &maps.k, bar, row);
+        sm100::bulk_copy_g2s(&sm.gates[b][0][0], w.gates + idx * 3 * C, 3 * C * 4, bar);
+    }
+    __device__ __forceinline__ void v(int row, bool with_q) const {  // 16 columns of v (or do); forwards with Q
+        uint64_t *bar = &sm.bar[kBarV];
+        sm100::mbar_arrive_expect_tx(bar, C * NV * 2 + (with_q ? kTileBytes : 0));
+        sm100::tma_load_3d(&sm.V[0][0], &maps.v, bar, c0, h, row);
+        if (with_q) tile(sm.Q, &maps.q, bar, row);
+    }
+    __device__ __forceinline__ void t(const uint2 *src) const {
+        sm100::mbar_arrive_expect_tx(&sm.bar[kBarT], sizeof(sm.T));
+        sm100::bulk_copy_g2s(sm.T, src, sizeof(sm.T), &sm.bar[kBarT]);
+    }
+    __device__ __forceinline__ void p(const uint2 *src, int row, bool with_q) const {  // backwards with Q, read last
+        sm100::mbar_arrive_expect_tx(&sm.bar[kBarP], sizeof(sm.P) + (with_q ? kTileBytes : 0));
+        sm100::bulk_copy_g2s(sm.P, src, sizeof(sm.P), &sm.bar[kBarP]);
+        if (with_q) tile(sm.Q, &maps.q, &sm.bar[kBarP], row);
+    }
 };
-// units of a lower triangle: tile t has blocks 0 .. t / 2
-template <int TERMS>
-__device__ __forceinline__ void load_low(Frags<TERMS> &f, const uint2 *src, int warp, int lane) {
-    const int t1 = 7 - warp;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e)
-            if (b <= warp / 2) f.a[b][e] = src[((low_unit(warp) + b) * 3 + e) * 32 + lane];
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e)
-            if (b <= t1 / 2) f.b[b][e] = src[((low_unit(t1) + b) * 3 + e) * 32 + lane];
-}
-// units of an upper triangle, from the last block down: f.b is tile warp's, f.a tile (7 - warp)'s
-template <int TERMS>
-__device__ __forceinline__ void load_up(Frags<TERMS> &f, const uint2 *src, int warp, int lane) {
-    const int t1 = 7 - warp;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e)
-            if (3 - b >= t1 / 2) f.a[b][e] = src[((up_unit(t1) + 3 - b - t1 / 2) * 3 + e) * 32 + lane];
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e)
-            if (3 - b >= warp / 2) f.b[b][e] = src[((up_unit(warp) + 3 - b - warp / 2) * 3 + e) * 32 + lane];
+
+// The rows behind a sequence's end belong to the next one: zeros (what they hold may not be finite).
+__device__ __forceinline__ void zero_tail(bf16 *tile, int slabs, int pieces, int rows) {  // pieces of 16 bytes a row
+    for (int i = threadIdx.x; i < (C - rows) * slabs * pieces; i += blockDim.x)
+        reinterpret_cast<uint4 *>(tile)[i / ((C - rows) * pieces) * C * pieces + rows * pieces + i % ((C - rows) * pieces)] =
+            make_uint4(0, 0, 0, 0);
+    sm100::fence_proxy_async_smem();  // later copies land here
 }
 
-// hi += a0 b0; lo += the other products of AT terms of a with BT of b that are above 2^-24
+// Before the first fetch.
+template <int NF, bool BWD> __device__ __forceinline__ void chain_init(ChainSmem<NF, BWD> &sm) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 5; ++i) sm100::mbar_init(&sm.bar[i], 1);
+        sm100::fence_barrier_init();
+    }
+    __syncthreads();
+}
+// A block that gave up leaves no copy in flight: the last copy of every barrier is waited for once more.
+template <int NF, bool BWD>
+__device__ __forceinline__ void chain_leave(ChainSmem<NF, BWD> &sm, const SeqProblem &p, long long turn, bool with_p, int *err) {
+    const uint32_t now = (uint32_t)turn & 1;
+    sm100::mbar_wait(&sm.bar[kBarK + now], (uint32_t)(turn >> 1) & 1, err, sm100::kWaitLimitNs, true);
+    sm100::mbar_wait(&sm.bar[kBarV], now, err, sm100::kWaitLimitNs, true);
+    sm100::mbar_wait(&sm.bar[kBarT], now, err, sm100::kWaitLimitNs, true);
+    if (with_p || turn > 0) sm100::mbar_wait(&sm.bar[kBarP], with_p ? now : now ^ 1, err, sm100::kWaitLimitNs, true);
+    if (p.status && threadIdx.x == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
+}
+
+// hi += a0 b0; lo += the other products of the terms of a with those of b that are above 2^-24, for the
+// shorter tile (while it lasts) and the longer one; lo's sums are two, to keep products of one apart.
 template <int AT, int BT>
-__device__ __forceinline__ void mma_split(float (&hi)[4], float (&lo)[4], const uint32_t (&a)[AT][4], const uint2 (&b)[BT]) {
-    mma::mma(hi, a[0], b[0].x, b[0].y);
+__device__ __forceinline__ void mma_split(float (&hi)[2][4], float (&lo)[2][2][4], const uint32_t (&a)[AT][4], const uint2 (&b0)[BT],
+                                          const uint2 (&b1)[BT], bool both) {
 #pragma unroll
-    for (int i = 0; i < AT; ++i)
+    for (int k = 0; k < (AT > BT ? AT : BT); ++k)
 #pragma unroll
-        for (int j = 0; j < BT; ++j)
-            if (i + j > 0 && i + j < (AT > BT ? AT : BT)) mma::mma(lo, a[i], b[j].x, b[j].y);
+        for (int i = 0; i < AT; ++i) {
+            const int j = k - i;
+            if (j < 0 || j >= BT) continue;
+            if (both) mma::mma(k ? lo[0][k - 1 & 1] : hi[0], a[i], b0[j].x, b0[j].y);
+            mma::mma(k ? lo[1][k - 1 & 1] : hi[1], a[i], b1[j].x, b1[j].y);
+        }
+}
+// Unit (t, b) of T or P in shared memory; the blocks of a tile are counted from the diagonal's far end: block m
+// of a lower triangle is 16-token block m, of an upper one block 3 - m.
+template <int TERMS>
+__device__ __forceinline__ void low_frag(uint2 (&f)[TERMS], const uint2 (*src)[kUnits][32], int t, int m, int lane) {
+#pragma unroll
+    for (int e = 0; e < TERMS; ++e) f[e] = src[e][low_unit(t) + m][lane];
+}
+template <int TERMS>
+__device__ __forceinline__ void up_frag(uint2 (&f)[TERMS], const uint2 (*src)[kUnits][32], int t, int m, int lane) {
+#pragma unroll
+    for (int e = 0; e < TERMS; ++e) f[e] = src[e][up_unit(t) + 3 - m - t / 2][lane];
 }
 
 // Sum over the lanes that hold the other rows of the same columns.
@@ -358,7 +402,7 @@ template <int NF> struct StateRows {
         }
     }
 };
-template <int NF> __device__ __forceinline__ void put_state(ChainSmem<NF> &sm, StateRows<NF> &st, int warp, int lane) {
+template <int NF, bool BWD> __device__ __forceinline__ void put_state(ChainSmem<NF, BWD> &sm, StateRows<NF> &st, int warp, int lane) {
     st.each(warp, lane, [&](int n, int col, float &x, float &y) {
         uint32_t t[3];
         split(x, y, t);
@@ -371,7 +415,6 @@ template <int NF> __device__ __forceinline__ void put_state(ChainSmem<NF> &sm, S
 template <int NF, int SETS>
 __device__ __forceinline__ void update_state(StateRows<NF> &st, float decay, const bf16 (*const (&planes)[SETS])[NV][PC],
                                              const bf16 *const (&rows)[SETS], int warp, int lane) {
-    constexpr int PK = 16 * NF + 8;
     float hi[2][2][4] = {}, lo[2][2][4] = {};
 #pragma unroll
     for (int s = 0; s < SETS; ++s)
@@ -384,13 +427,13 @@ __device__ __forceinline__ void update_state(StateRows<NF> &st, float decay, con
             for (int m = 0; m < 2; ++m) {
                 if (warp + 4 * m >= NF) continue;
                 uint32_t b[4];
-                ldsm4_t(b, bt_row(rows[s], PK, 16 * kb, 16 * (warp + 4 * m), lane));
+                ldsm4_t(b, bt_row(rows[s], C, 16 * kb, 16 * (warp + 4 * m), lane));
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    mma::mma(hi[m][t], a[0], b[2 * t], b[2 * t + 1]);
-                    mma::mma(lo[m][t], a[1], b[2 * t], b[2 * t + 1]);
-                    mma::mma(lo[m][t], a[2], b[2 * t], b[2 * t + 1]);
-                }
+                for (int t = 0; t < 2; ++t) mma::mma(lo[m][t], a[2], b[2 * t], b[2 * t + 1]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) mma::mma(hi[m][t], a[0], b[2 * t], b[2 * t + 1]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) mma::mma(lo[m][t], a[1], b[2 * t], b[2 * t + 1]);
             }
         }
 #pragma unroll
@@ -403,10 +446,11 @@ __device__ __forceinline__ void update_state(StateRows<NF> &st, float decay, con
 
 // SAVE: the pass that gdn_bwd makes (no O; Sig, U and X of every chunk are kept).
 template <int NF, bool SAVE>
-__global__ void __launch_bounds__(128, 2) k_chunk_fwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w) {
-    constexpr int DK = 16 * NF, PK = DK + 8;
-    extern __shared__ __align__(16) unsigned char raw[];
-    ChainSmem<NF> &sm = *reinterpret_cast<ChainSmem<NF> *>(raw);
+__global__ void __launch_bounds__(kChainThreads, 2) k_chunk_fwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
+                                                                const __grid_constant__ ChainMaps maps) {
+    constexpr int DK = 16 * NF, PK = DK + 8, kSlabs = (DK + 63) / 64;
+    extern __shared__ unsigned char raw[];
+    auto &sm = *reinterpret_cast<ChainSmem<NF, false> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const int groups = p.dv / NV, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const SeqRange r = seq_range(p, s);
@@ -414,33 +458,54 @@ __global__ void __launch_bounds__(128, 2) k_chunk_fwd(const __grid_constant__ Se
     if (r.slot < 0) return;
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);
     const size_t soff = (((size_t)r.slot * p.H + h) * p.dv + c0) * DK;
-    const bf16 *v = (const bf16 *)p.v + (size_t)h * p.dv + c0;
-    auto fetch = [&](long long c, int b) {
-        chain_fetch(sm, b, p, w, r.first + c * C, (int)min((long long)C, r.len - c * C), (size_t)(base + c) * p.H + h, hk, !SAVE, v,
-                    p.v_stride);
-    };
-    if (n_chunks > 0) fetch(0, 0);
+    const ChainFetch<NF, false> fetch = {sm, maps, w, hk, h, c0};
+    const bool fetcher = threadIdx.x == 128;
+    auto index = [&](long long c) { return (size_t)(base + c) * p.H + h; };
+    auto first_row = [&](long long c) { return (int)(r.first + c * C); };
+    chain_init(sm);
+    if (fetcher && n_chunks > 0) {
+        fetch.k(0, first_row(0), index(0));
+        fetch.v(first_row(0), !SAVE);
+        fetch.t(w.T + index(0) * 3 * kUnits * 32);
+    }
     StateRows<NF> st = {};
-    if (!seq_starts_zero(p, s))
-        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
-            const float2 t = *reinterpret_cast<const float2 *>(p.S_in + soff + (size_t)n * DK + col);
-            x = t.x;
-            y = t.y;
-        });
-    put_state(sm, st, warp, lane);
-    const int t0 = warp, t1 = 7 - warp;  // this warp's token tiles (8 tokens each)
+    if (warp < 4) {
+        if (!seq_starts_zero(p, s))
+            st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+                const float2 t = *reinterpret_cast<const float2 *>(p.S_in + soff + (size_t)n * DK + col);
+                x = t.x;
+                y = t.y;
+            });
+        put_state(sm, st, warp, lane);
+    }
+    const int t0 = warp & 3, t1 = 7 - t0;  // this warp's token tiles (8 tokens each), the shorter one in T first
+    bool ok = true;
     for (long long c = 0; c < n_chunks; ++c) {
         const int b = (int)(c & 1);
-        const size_t idx = (size_t)(base + c) * p.H + h;
+        const uint32_t parity = (uint32_t)c & 1;
+        const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        sm100::cp_async_wait_all();
-        __syncthreads();  // this chunk's rows and the state's terms are there; the other buffer has been read
-        if (c + 1 < n_chunks) fetch(c + 1, b ^ 1);
-        Frags<3> T;
-        load_low(T, w.T + idx * kUnits * 96, warp, lane);
-        Frags<2> P;
-        if (!SAVE) load_low(P, w.P + idx * kUnits * 96, warp, lane);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err);
+        // behind this barrier the state's terms are there and the last step's buffers have been read
+        if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, false, w.err);
+        if (fetcher) {
+            if (c + 1 < n_chunks) fetch.k(b ^ 1, first_row(c + 1), index(c + 1));
+            if (!SAVE) fetch.p(w.P + idx * 2 * kUnits * 32, 0, false);
+        }
+        if (rows < C) {
+            zero_tail(sm.K[b], kSlabs, 8, rows);
+            if (!SAVE) zero_tail(sm.Q, kSlabs, 8, rows);
+            zero_tail(&sm.V[0][0], 1, NV / 8, rows);
+            __syncthreads();
+        }
+        if (warp == 4) {  // the fetching warp keeps the barriers' count
+            __syncthreads();
+            if (fetcher && c + 1 < n_chunks) fetch.v(first_row(c + 1), !SAVE);
+            __syncthreads();
+            if (fetcher && c + 1 < n_chunks) fetch.t(w.T + index(c + 1) * 3 * kUnits * 32);
+            continue;
+        }
         if (SAVE)
             st.each(warp, lane, [&](int n, int col, float &x, float &y) {
                 *reinterpret_cast<float2 *>(w.Sig + (idx * p.dv + c0 + n) * DK + col) = make_float2(x, y);
@@ -449,25 +514,23 @@ __global__ void __launch_bounds__(128, 2) k_chunk_fwd(const __grid_constant__ Se
         float kh[2][4] = {}, kl[2][4] = {}, qh[2][4] = {}, ql[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < NF; ++ks) {
-            uint32_t a[3][4], k[4];
+            uint32_t a[3][4], k[4], q[4];
 #pragma unroll
             for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.S[e][0][0], PK, 0, 16 * ks, lane));
-            ldsm4(k, b_row(&sm.K[b][0][0], PK, 8 * t0, 8 * t1, 16 * ks, lane));
+            ldsm4(k, b_row(sm.K[b], C, 8 * t0, 8 * t1, 16 * ks, lane));
+            if (!SAVE) ldsm4(q, b_row(sm.Q, C, 8 * t0, 8 * t1, 16 * ks, lane));
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                mma::mma(kh[t], a[0], k[2 * t], k[2 * t + 1]);
-                mma::mma(kl[t], a[1], k[2 * t], k[2 * t + 1]);
-                mma::mma(kl[t], a[2], k[2 * t], k[2 * t + 1]);
-            }
+            for (int t = 0; t < 2; ++t) mma::mma(kl[t], a[2], k[2 * t], k[2 * t + 1]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma::mma(kh[t], a[0], k[2 * t], k[2 * t + 1]);
             if (!SAVE) {
-                uint32_t q[4];
-                ldsm4(q, b_row(&sm.Q[b][0][0], PK, 8 * t0, 8 * t1, 16 * ks, lane));
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    mma::mma(qh[t], a[0], q[2 * t], q[2 * t + 1]);
-                    mma::mma(ql[t], a[1], q[2 * t], q[2 * t + 1]);
-                }
+                for (int t = 0; t < 2; ++t) mma::mma(ql[t], a[1], q[2 * t], q[2 * t + 1]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) mma::mma(qh[t], a[0], q[2 * t], q[2 * t + 1]);
             }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma::mma(kl[t], a[1], k[2 * t], k[2 * t + 1]);
         }
         // beta Y's terms
 #pragma unroll
@@ -481,22 +544,26 @@ __global__ void __launch_bounds__(128, 2) k_chunk_fwd(const __grid_constant__ Se
                 const float x = eg.x * (kh[t][2 * half] + kl[t][2 * half]), y = eg.y * (kh[t][2 * half + 1] + kl[t][2 * half + 1]);
                 if (SAVE) *reinterpret_cast<float2 *>(w.X + (idx * p.dv + c0 + n) * C + tok) = make_float2(x, y);
                 uint32_t e[3];
-                split(be.x * (__bfloat162float(sm.V[b][tok][n]) - x), be.y * (__bfloat162float(sm.V[b][tok + 1][n]) - y), e);
+                split(be.x * (__bfloat162float(sm.V[tok][n]) - x), be.y * (__bfloat162float(sm.V[tok + 1][n]) - y), e);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.R[i][n][tok]) = e[i];
             }
         }
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err);
         __syncthreads();
         // U^T = (beta Y)^T T^T
-        float uh[2][4] = {}, ul[2][4] = {};
+        float uh[2][4] = {}, ul[2][2][4] = {};
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
             if (kb > t1 / 2) continue;
             uint32_t a[3][4];
+            uint2 f0[3] = {}, f1[3];
+            const bool both = kb < 2 && kb <= t0 / 2;
 #pragma unroll
             for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.R[e][0][0], PC, 0, 16 * kb, lane));
-            if (kb < 2 && kb <= t0 / 2) mma_split<3, 3>(uh[0], ul[0], a, T.a[kb < 2 ? kb : 0]);
-            mma_split<3, 3>(uh[1], ul[1], a, T.b[kb]);
+            if (both) low_frag<3>(f0, sm.T, t0, kb, lane);
+            low_frag<3>(f1, sm.T, t1, kb, lane);
+            mma_split<3, 3>(uh, ul, a, f0, f1, both);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -504,8 +571,8 @@ __global__ void __launch_bounds__(128, 2) k_chunk_fwd(const __grid_constant__ Se
             const float2 el = *reinterpret_cast<const float2 *>(&sm.gates[b][1][tok]);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int n = lane / 4 + 8 * half;
-                const float x = uh[t][2 * half] + ul[t][2 * half], y = uh[t][2 * half + 1] + ul[t][2 * half + 1];
+                const int n = lane / 4 + 8 * half, i = 2 * half;
+                const float x = uh[t][i] + (ul[t][0][i] + ul[t][1][i]), y = uh[t][i + 1] + (ul[t][0][i + 1] + ul[t][1][i + 1]);
                 if (SAVE) *reinterpret_cast<float2 *>(w.U + (idx * p.dv + c0 + n) * C + tok) = make_float2(x, y);
                 uint32_t e[3];
                 split(el.x * x, el.y * y, e);
@@ -515,107 +582,147 @@ __global__ void __launch_bounds__(128, 2) k_chunk_fwd(const __grid_constant__ Se
                     uint32_t u[2];
                     split(x, y, u);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint32_t *>(&sm.U[3 + i][n][tok]) = u[i];
+                    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint32_t *>(&sm.W[i][n][tok]) = u[i];
                 }
             }
         }
         __syncthreads();
         const bf16(*const planes[1])[NV][PC] = {sm.U};
-        const bf16 *const krows[1] = {&sm.K[b][0][0]};
+        const bf16 *const krows[1] = {sm.K[b]};
         update_state<NF, 1>(st, sm.gates[b][0][C - 1], planes, krows, warp, lane);
         put_state(sm, st, warp, lane);
         if (!SAVE) {
-            float oh[2][4] = {}, ol[2][4] = {};
+            ok = ok && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
+            float oh[2][4] = {}, ol[2][2][4] = {};
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {
                 if (kb > t1 / 2) continue;
                 uint32_t a[2][4];
+                uint2 f0[2] = {}, f1[2];
+                const bool both = kb < 2 && kb <= t0 / 2;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) ldsm4(a[e], a_row(&sm.U[3 + e][0][0], PC, 0, 16 * kb, lane));
-                if (kb < 2 && kb <= t0 / 2) mma_split<2, 2>(oh[0], ol[0], a, P.a[kb < 2 ? kb : 0]);
-                mma_split<2, 2>(oh[1], ol[1], a, P.b[kb]);
+                for (int e = 0; e < 2; ++e) ldsm4(a[e], a_row(&sm.W[e][0][0], PC, 0, 16 * kb, lane));
+                if (both) low_frag<2>(f0, sm.P, t0, kb, lane);
+                low_frag<2>(f1, sm.P, t1, kb, lane);
+                mma_split<2, 2>(oh, ol, a, f0, f1, both);
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
+                const float2 eg = *reinterpret_cast<const float2 *>(&sm.gates[b][0][tok]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = tok + (e & 1), n = lane / 4 + 8 * (e >> 1);
+                for (int half = 0; half < 2; ++half) {
+                    // the neighbour row's lane takes the second token of both rows, this one or it the first: pairs of columns
+                    float x = fmaf(eg.x, qh[t][2 * half] + ql[t][2 * half], oh[t][2 * half] + ol[t][0][2 * half]);
+                    float y = fmaf(eg.y, qh[t][2 * half + 1] + ql[t][2 * half + 1], oh[t][2 * half + 1] + ol[t][0][2 * half + 1]);
+                    const bool odd = lane & 4;
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 4);
+                    const int i = tok + odd, n = (lane / 4 & ~1) + 8 * half;
                     if (i < rows)
-                        ((bf16 *)p.o)[((row + i) * p.H + h) * p.dv + c0 + n] =
-                            __float2bfloat16_rn(fmaf(sm.gates[b][0][i], qh[t][e] + ql[t][e], oh[t][e] + ol[t][e]));
+                        *reinterpret_cast<uint32_t *>((bf16 *)p.o + ((row + i) * p.H + h) * p.dv + c0 + n) =
+                            odd ? pack(other, y) : pack(x, other);
                 }
             }
         }
     }
-    if (!SAVE && p.S_out)
+    if (!SAVE && p.S_out && warp < 4)
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.S_out + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
+    // the last waits' answers: nobody reads buffers any more, so every thread may report for itself
+    if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
 template <int NF>
-__global__ void __launch_bounds__(128, 2) k_chunk_bwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w) {
-    constexpr int DK = 16 * NF, PK = DK + 8;
-    extern __shared__ __align__(16) unsigned char raw[];
-    ChainSmem<NF> &sm = *reinterpret_cast<ChainSmem<NF> *>(raw);
+__global__ void __launch_bounds__(kChainThreads, 2) k_chunk_bwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
+                                                                const __grid_constant__ ChainMaps maps) {
+    constexpr int DK = 16 * NF, PK = DK + 8, kSlabs = (DK + 63) / 64;
+    extern __shared__ unsigned char raw[];
+    auto &sm = *reinterpret_cast<ChainSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const int groups = p.dv / NV, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const SeqRange r = seq_rows(p, s);
     const size_t soff = (((size_t)s * p.H + h) * p.dv + c0) * DK;
-    StateRows<NF> st = {};
-    if (r.slot >= 0 && p.dS_out)
-        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
-            const float2 t = *reinterpret_cast<const float2 *>(p.dS_out + soff + (size_t)n * DK + col);
-            x = t.x;
-            y = t.y;
-        });
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);  // 0 of a bad range
-    const bf16 *d_o = (const bf16 *)p.d_o + (size_t)h * p.dv + c0;
-    auto fetch = [&](long long c, int b) {
-        chain_fetch(sm, b, p, w, r.first + c * C, (int)min((long long)C, r.len - c * C), (size_t)(base + c) * p.H + h, hk, true, d_o,
-                    (long long)p.H * p.dv);
-    };
-    if (n_chunks > 0) fetch(n_chunks - 1, (int)((n_chunks - 1) & 1));
-    put_state(sm, st, warp, lane);
-    const int t0 = warp, t1 = 7 - warp;
+    const ChainFetch<NF, true> fetch = {sm, maps, w, hk, h, c0};
+    const bool fetcher = threadIdx.x == 128;
+    auto index = [&](long long c) { return (size_t)(base + c) * p.H + h; };
+    auto first_row = [&](long long c) { return (int)(r.first + c * C); };
+    chain_init(sm);
+    if (fetcher && n_chunks > 0) {
+        const long long c = n_chunks - 1;
+        fetch.k(0, first_row(c), index(c));
+        fetch.v(first_row(c), false);
+        fetch.t(w.Tt + index(c) * 3 * kUnits * 32);
+        fetch.p(w.Pt + index(c) * 3 * kUnits * 32, first_row(c), true);
+    }
+    StateRows<NF> st = {};
+    if (warp < 4) {
+        if (r.slot >= 0 && p.dS_out)
+            st.each(warp, lane, [&](int n, int col, float &x, float &y) {
+                const float2 t = *reinterpret_cast<const float2 *>(p.dS_out + soff + (size_t)n * DK + col);
+                x = t.x;
+                y = t.y;
+            });
+        put_state(sm, st, warp, lane);
+    }
+    const int t1 = warp & 3, t0 = 7 - t1;  // the shorter tile first, as in k_chunk_fwd
+    bool ok = true;
     for (long long c = n_chunks - 1; c >= 0; --c) {
-        const int b = (int)(c & 1);
-        const size_t idx = (size_t)(base + c) * p.H + h;
+        const long long turn = n_chunks - 1 - c;
+        const int b = (int)(turn & 1);
+        const uint32_t parity = (uint32_t)turn & 1;
+        const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        sm100::cp_async_wait_all();
-        __syncthreads();
-        if (c > 0) fetch(c - 1, b ^ 1);
-        Frags<3> P, T;  // .b: tile t0's blocks from the last one down, .a: tile t1's
-        load_up(P, w.Pt + idx * kUnits * 96, warp, lane);
-        load_up(T, w.Tt + idx * kUnits * 96, warp, lane);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err) &&
+             sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
+        if (!__syncthreads_and(ok)) return chain_leave(sm, p, turn, true, w.err);
+        if (fetcher && c > 0) fetch.k(b ^ 1, first_row(c - 1), index(c - 1));
+        if (rows < C) {
+            zero_tail(sm.K[b], kSlabs, 8, rows);
+            zero_tail(sm.Q, kSlabs, 8, rows);
+            zero_tail(&sm.V[0][0], 1, NV / 8, rows);
+            __syncthreads();
+        }
+        if (warp == 4) {
+            __syncthreads();
+            if (fetcher && c > 0) fetch.v(first_row(c - 1), false);
+            __syncthreads();
+            if (fetcher && c > 0) fetch.t(w.Tt + index(c - 1) * 3 * kUnits * 32);
+            __syncthreads();
+            __syncthreads();
+            if (fetcher && c > 0) fetch.p(w.Pt + index(c - 1) * 3 * kUnits * 32, first_row(c - 1), true);
+            continue;
+        }
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(w.D + (idx * p.dv + c0 + n) * DK + col) = make_float2(x, y);
         });
         // D^T K^T, and dO^T P
-        float zh[2][4] = {}, zl[2][4] = {}, ph[2][4] = {}, pl[2][4] = {};
+        float zh[2][4] = {}, zl[2][4] = {}, ph[2][4] = {}, pl[2][2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < NF; ++ks) {
             uint32_t a[3][4], k[4];
 #pragma unroll
             for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.S[e][0][0], PK, 0, 16 * ks, lane));
-            ldsm4(k, b_row(&sm.K[b][0][0], PK, 8 * t0, 8 * t1, 16 * ks, lane));
+            ldsm4(k, b_row(sm.K[b], C, 8 * t0, 8 * t1, 16 * ks, lane));
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                mma::mma(zh[t], a[0], k[2 * t], k[2 * t + 1]);
-                mma::mma(zl[t], a[1], k[2 * t], k[2 * t + 1]);
-                mma::mma(zl[t], a[2], k[2 * t], k[2 * t + 1]);
-            }
+            for (int t = 0; t < 2; ++t) mma::mma(zl[t], a[2], k[2 * t], k[2 * t + 1]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma::mma(zh[t], a[0], k[2 * t], k[2 * t + 1]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma::mma(zl[t], a[1], k[2 * t], k[2 * t + 1]);
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {  // blocks 3 - m
-            const int kb = 3 - m;
-            if (kb < t0 / 2) continue;
+        for (int m = 0; m < 4; ++m) {  // 16-token blocks from the last one down
+            if (3 - m < t1 / 2) continue;
             uint32_t a[1][4];
-            ldsm4_t(a[0], at_row(&sm.V[b][0][0], PV, 16 * kb, 0, lane));
-            mma_split<1, 3>(ph[0], pl[0], a, P.b[m]);
-            if (m < 2 && kb >= t1 / 2) mma_split<1, 3>(ph[1], pl[1], a, P.a[m < 2 ? m : 0]);
+            uint2 f0[3] = {}, f1[3];
+            const bool both = m < 2 && 3 - m >= t0 / 2;
+            ldsm4_t(a[0], at_row(&sm.V[0][0], NV, 16 * (3 - m), 0, lane));
+            if (both) up_frag<3>(f0, sm.P, t0, m, lane);
+            up_frag<3>(f1, sm.P, t1, m, lane);
+            mma_split<1, 3>(ph, pl, a, f0, f1, both);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -625,16 +732,16 @@ __global__ void __launch_bounds__(128, 2) k_chunk_bwd(const __grid_constant__ Se
             float past0 = 0.f, past1 = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int n = lane / 4 + 8 * half;
-                const float zx = el.x * (zh[t][2 * half] + zl[t][2 * half]), zy = el.y * (zh[t][2 * half + 1] + zl[t][2 * half + 1]);
+                const int n = lane / 4 + 8 * half, i = 2 * half;
+                const float zx = el.x * (zh[t][i] + zl[t][i]), zy = el.y * (zh[t][i + 1] + zl[t][i + 1]);
                 const float2 u = *reinterpret_cast<const float2 *>(w.U + (idx * p.dv + c0 + n) * C + tok);
                 past0 = fmaf(u.x, zx, past0);
                 past1 = fmaf(u.y, zy, past1);
                 uint32_t e[3];
-                split(zx + (ph[t][2 * half] + pl[t][2 * half]), zy + (ph[t][2 * half + 1] + pl[t][2 * half + 1]), e);  // dU
+                split(zx + (ph[t][i] + (pl[t][0][i] + pl[t][1][i])), zy + (ph[t][i + 1] + (pl[t][0][i + 1] + pl[t][1][i + 1])), e);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.R[i][n][tok]) = e[i];
-                split(eg.x * __bfloat162float(sm.V[b][tok][n]), eg.y * __bfloat162float(sm.V[b][tok + 1][n]), e);
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.R[i][n][tok]) = e[i];  // dU
+                split(eg.x * __bfloat162float(sm.V[tok][n]), eg.y * __bfloat162float(sm.V[tok + 1][n]), e);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.U[i][n][tok]) = e[i];
             }
@@ -642,19 +749,23 @@ __global__ void __launch_bounds__(128, 2) k_chunk_bwd(const __grid_constant__ Se
             past1 = rows_sum(past1);
             if (lane < 4) *reinterpret_cast<float2 *>(w.past + (idx * groups + c0 / NV) * C + tok) = make_float2(past0, past1);
         }
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err);
         __syncthreads();
         // dR^T = dU^T T
-        float rh[2][4] = {}, rl[2][4] = {};
+        float rh[2][4] = {}, rl[2][2][4] = {};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const int kb = 3 - m;
-            if (kb < t0 / 2) continue;
+            if (3 - m < t1 / 2) continue;
             uint32_t a[3][4];
+            uint2 f0[3] = {}, f1[3];
+            const bool both = m < 2 && 3 - m >= t0 / 2;
 #pragma unroll
-            for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.R[e][0][0], PC, 0, 16 * kb, lane));
-            mma_split<3, 3>(rh[0], rl[0], a, T.b[m]);
-            if (m < 2 && kb >= t1 / 2) mma_split<3, 3>(rh[1], rl[1], a, T.a[m < 2 ? m : 0]);
+            for (int e = 0; e < 3; ++e) ldsm4(a[e], a_row(&sm.R[e][0][0], PC, 0, 16 * (3 - m), lane));
+            if (both) up_frag<3>(f0, sm.T, t0, m, lane);
+            up_frag<3>(f1, sm.T, t1, m, lane);
+            mma_split<3, 3>(rh, rl, a, f0, f1, both);
         }
+        __syncthreads();  // dU has been read: -beta e^G dR takes its place
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
@@ -663,8 +774,8 @@ __global__ void __launch_bounds__(128, 2) k_chunk_bwd(const __grid_constant__ Se
             float into0 = 0.f, into1 = 0.f, db0 = 0.f, db1 = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int n = lane / 4 + 8 * half;
-                const float x = rh[t][2 * half] + rl[t][2 * half], y = rh[t][2 * half + 1] + rl[t][2 * half + 1];
+                const int n = lane / 4 + 8 * half, i = 2 * half;
+                const float x = rh[t][i] + (rl[t][0][i] + rl[t][1][i]), y = rh[t][i + 1] + (rl[t][0][i + 1] + rl[t][1][i + 1]);
                 const size_t at = (idx * p.dv + c0 + n) * C + tok;
                 *reinterpret_cast<float2 *>(w.dR + at) = make_float2(x, y);
                 const float2 X = *reinterpret_cast<const float2 *>(w.X + at);
@@ -684,7 +795,7 @@ __global__ void __launch_bounds__(128, 2) k_chunk_bwd(const __grid_constant__ Se
                 uint32_t e[3];
                 split(-eg.x * bx, -eg.y * by, e);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.U[3 + i][n][tok]) = e[i];
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(&sm.R[i][n][tok]) = e[i];
             }
             into0 = rows_sum(into0);
             into1 = rows_sum(into1);
@@ -696,15 +807,17 @@ __global__ void __launch_bounds__(128, 2) k_chunk_bwd(const __grid_constant__ Se
             }
         }
         __syncthreads();
-        const bf16(*const planes[2])[NV][PC] = {sm.U, sm.U + 3};
-        const bf16 *const mrows[2] = {&sm.Q[b][0][0], &sm.K[b][0][0]};
+        const bf16(*const planes[2])[NV][PC] = {sm.U, sm.R};
+        const bf16 *const mrows[2] = {sm.Q, sm.K[b]};
         update_state<NF, 2>(st, sm.gates[b][0][C - 1], planes, mrows, warp, lane);
         put_state(sm, st, warp, lane);
+        __syncthreads();  // Q has been read
     }
-    if (p.dS_in)
+    if (p.dS_in && warp < 4)
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.dS_in + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
+    if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
 template <int NF> cudaError_t prep(const SeqProblem &p, const ChunkWork &w, float floor_log, cudaStream_t s) {
@@ -713,17 +826,25 @@ template <int NF> cudaError_t prep(const SeqProblem &p, const ChunkWork &w, floa
     return cudaGetLastError();
 }
 
-template <typename K, int NF> cudaError_t chain(K kernel, const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
-    const int bytes = (int)sizeof(ChainSmem<NF>);
+template <typename K, int NF, bool BWD> cudaError_t chain(K kernel, const SeqProblem &p, const ChunkWork &w, const ChainMaps &m, cudaStream_t s) {
+    const int bytes = (int)sizeof(ChainSmem<NF, BWD>) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e) return e;
-    kernel<<<(unsigned)((long long)p.n_seqs * p.H * (p.dv / NV)), 128, bytes, s>>>(p, w);
+    kernel<<<(unsigned)((long long)p.n_seqs * p.H * (p.dv / NV)), kChainThreads, bytes, s>>>(p, w, m);
     return cudaGetLastError();
 }
 
+bool make_maps(ChainMaps &m, const SeqProblem &p, const void *v, long long v_stride) {
+    return seq_row_map(&m.q, p.q, p.n_tokens, p.q_stride, p.Hk, p.dk, 64) &&
+           seq_row_map(&m.k, p.k, p.n_tokens, p.k_stride, p.Hk, p.dk, 64) &&
+           seq_row_map(&m.v, v, p.n_tokens, v_stride, p.H, p.dv, NV);
+}
+
 template <int NF> cudaError_t fwd(const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
+    ChainMaps m;
+    if (!make_maps(m, p, p.v, p.v_stride)) return cudaErrorInvalidValue;
     cudaError_t e = prep<NF>(p, w, kLogAlphaFloor, s);
-    return e ? e : chain<decltype(&k_chunk_fwd<NF, false>), NF>(k_chunk_fwd<NF, false>, p, w, s);
+    return e ? e : chain<decltype(&k_chunk_fwd<NF, false>), NF, false>(k_chunk_fwd<NF, false>, p, w, m, s);
 }
 
 ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
@@ -734,11 +855,12 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
         at += align256(bytes);
         return x;
     };
-    const size_t frags = n * kUnits * 3 * 32 * sizeof(uint2);
+    const size_t frag = n * kUnits * 32 * sizeof(uint2);  // a term of T or P
     ChunkWork w = {};
-    w.T = (uint2 *)take(frags);
+    w.T = (uint2 *)take(3 * frag);
     w.gates = (float *)take(n * 3 * C * 4);
-    if (!bwd) w.P = (uint2 *)take(frags);
+    w.err = (int *)take(sizeof(int));
+    if (!bwd) w.P = (uint2 *)take(2 * frag);
     if (total) *total = at;
     return w;
 }

@@ -30,9 +30,11 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], const void *row) {
                  : "memory");
 }
 
-// c[16 x 8] += a[16 x 16] b[16 x 8]
+// c[16 x 8] += a[16 x 16] b[16 x 8].  Registers only, so the compiler may move it between the
+// fragments' loads; a result is ready about 21 clocks later and an SM quarter takes one in 8, so the callers
+// put two products or more between two of one accumulator.
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -46,14 +48,19 @@ __device__ __forceinline__ const bf16 *a_row(const bf16 *base, int pitch, int ro
 __device__ __forceinline__ const bf16 *at_row(const bf16 *base, int pitch, int k0, int m0, int lane) {
     return base + (k0 + (lane >> 4) * 8 + (lane & 7)) * pitch + m0 + ((lane >> 3) & 1) * 8;
 }
-// Two n-tiles (8 rows from n0, 8 from n1) of a B operand held [n][k], k step of 16: r[0], r[1]
-// are the first tile's fragment, r[2], r[3] the second's.
-__device__ __forceinline__ const bf16 *b_row(const bf16 *base, int pitch, int n0, int n1, int k0, int lane) {
-    return base + ((lane < 16 ? n0 : n1) + (lane & 7)) * pitch + k0 + ((lane >> 3) & 1) * 8;
+// Rows of 64 columns (slabs of `rows` rows each) in the tensor maps' 128-byte swizzle: the 16-byte piece
+// of (row, col) lies at piece (col / 8 % 8) ^ (row % 8) of its 128-byte line.
+__device__ __forceinline__ const bf16 *sw_piece(const bf16 *base, int rows, int row, int col) {
+    return base + (col >> 6) * rows * 64 + row * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3);
 }
-// Two adjacent n-tiles (16 columns from n0) of a B operand held [k][n], for ldsm4_t.
-__device__ __forceinline__ const bf16 *bt_row(const bf16 *base, int pitch, int k0, int n0, int lane) {
-    return base + (k0 + ((lane >> 3) & 1) * 8 + (lane & 7)) * pitch + n0 + (lane >> 4) * 8;
+// Two n-tiles (8 rows from n0, 8 from n1) of a B operand held [n][k] in swizzled rows, k step of 16:
+// r[0], r[1] are the first tile's fragment, r[2], r[3] the second's.
+__device__ __forceinline__ const bf16 *b_row(const bf16 *base, int rows, int n0, int n1, int k0, int lane) {
+    return sw_piece(base, rows, (lane < 16 ? n0 : n1) + (lane & 7), k0 + ((lane >> 3) & 1) * 8);
+}
+// Two adjacent n-tiles (16 columns from n0) of a B operand held [k][n] in swizzled rows, for ldsm4_t.
+__device__ __forceinline__ const bf16 *bt_row(const bf16 *base, int rows, int k0, int n0, int lane) {
+    return sw_piece(base, rows, k0 + ((lane >> 3) & 1) * 8 + (lane & 7), n0 + (lane >> 4) * 8);
 }
 
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {

@@ -221,6 +221,12 @@ __device__ __forceinline__ void bulk_copy_s2g(void *gdst, const void *ssrc, uint
                  "r"(bytes)
                  : "memory");
 }
+// Global -> shared copy of `bytes` contiguous bytes (as above), counted on an mbarrier.
+__device__ __forceinline__ void bulk_copy_g2s(void *sdst, const void *gsrc, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(sdst)),
+                 "l"(gsrc), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // The issuing thread's committed bulk stores have finished reading shared memory.
 __device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }

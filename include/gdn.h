@@ -338,13 +338,14 @@ size_t gdn_workspace_bytes(int B, int H, long long T, int frame_len, int d_k, in
  * when its slot is >= n_slots (GDN_SEQ_BAD_SLOT), when an earlier sequence
  * has the same slot (GDN_SEQ_SAME_SLOT; the first one runs), or when its rows
  * are not an ordered range inside the n_tokens rows (GDN_SEQ_BAD_ROWS).  Two
- * sequences may not share rows.
+ * sequences may not share rows.  GDN_SEQ_TIMEOUT: a bounded device-side wait
+ * gave up and the outputs are not valid.
  *
  * Calls are asynchronous on `stream`, whose device must be the current one.
  * gdn_decode's and gdn_packed's results do not depend on how sequences are
  * batched, and no result depends on the order in which blocks run.
  */
-enum { GDN_SEQ_BAD_SLOT = 1, GDN_SEQ_SAME_SLOT = 2, GDN_SEQ_BAD_ROWS = 4 };
+enum { GDN_SEQ_BAD_SLOT = 1, GDN_SEQ_SAME_SLOT = 2, GDN_SEQ_BAD_ROWS = 4, GDN_SEQ_TIMEOUT = 8 };
 
 /*
  *   struct_size     sizeof(gdn_seq_args) as compiled by the caller.
