@@ -134,12 +134,13 @@ int check(const gdn_seq_args &a, Which which, gdn::SeqProblem &p) {
     return GDN_OK;
 }
 
-// Which form serves a gdn_packed call: the tensor cores take bf16 operands.
+// Which form serves a gdn_packed or gdn_bwd call: the tensor cores take bf16 operands.
 bool chunked(const gdn::SeqProblem &p) { return p.dtype == GDN_DTYPE_BF16 && p.n_tokens > 0; }
 
 size_t workspace_for(const gdn::SeqProblem &p, Which which) {
-    if (which == kBwd) return gdn::seq_bwd_workspace(p, nullptr, nullptr);
-    return which == kPacked && chunked(p) ? gdn::seq_chunk_workspace(p) : 0;
+    if (which == kDecode) return 0;
+    if (chunked(p)) return gdn::seq_chunk_workspace(p, which == kBwd);
+    return which == kBwd ? gdn::seq_bwd_workspace(p, nullptr, nullptr) : 0;
 }
 
 int run(const gdn_seq_args *a, Which which) noexcept {
@@ -170,7 +171,7 @@ int run(const gdn_seq_args *a, Which which) noexcept {
             }
         }
         cudaError_t e = cudaSuccess;
-        if (which == kBwd) e = gdn::launch_seq_bwd_simt(p, ws, s);
+        if (which == kBwd) e = chunked(p) ? gdn::launch_seq_bwd_chunk(p, ws, s) : gdn::launch_seq_bwd_simt(p, ws, s);
         else if (p.n_seqs && which == kPacked && chunked(p)) e = gdn::launch_seq_chunk(p, ws, s);
         else if (p.n_seqs) e = gdn::launch_seq_recurrent(p, which == kDecode, s);
         if (owned) {

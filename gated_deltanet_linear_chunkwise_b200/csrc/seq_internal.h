@@ -139,11 +139,12 @@ cudaError_t launch_seq_bwd_simt(const SeqProblem &p, void *ws, cudaStream_t s);
 // (also in dqh / dkh, where they are given).
 cudaError_t launch_seq_zero_rows(const SeqProblem &p, float *dqh, float *dkh, cudaStream_t s);
 // dq, dk from the heads' dqh, dkh.
-cudaError_t launch_seq_share(const SeqProblem &p, const SeqWork &w, cudaStream_t s);
+cudaError_t launch_seq_share(const SeqProblem &p, const float *dqh, const float *dkh, cudaStream_t s);
 
-// gdn_packed in chunks on the tensor cores, bf16 q, k, v (seq_chunk.cu).
-size_t seq_chunk_workspace(const SeqProblem &p);
+// gdn_packed and gdn_bwd in chunks on the tensor cores, bf16 q, k, v (seq_chunk.cu).
+size_t seq_chunk_workspace(const SeqProblem &p, bool bwd);
 cudaError_t launch_seq_chunk(const SeqProblem &p, void *ws, cudaStream_t s);
+cudaError_t launch_seq_bwd_chunk(const SeqProblem &p, void *ws, cudaStream_t s);
 
 // The recurrent form (seq_recurrent.cu).  `few`: one or a few tokens of each sequence.
 cudaError_t launch_seq_recurrent(const SeqProblem &p, bool few, cudaStream_t s);

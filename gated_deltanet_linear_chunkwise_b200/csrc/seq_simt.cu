@@ -503,12 +503,12 @@ cudaError_t launch_seq_zero_rows(const SeqProblem &p, float *dqh, float *dkh, cu
     return cudaGetLastError();
 }
 
-cudaError_t launch_seq_share(const SeqProblem &p, const SeqWork &w, cudaStream_t s) {
-    if (!w.dqh || p.n_tokens == 0) return cudaSuccess;
+cudaError_t launch_seq_share(const SeqProblem &p, const float *dqh, const float *dkh, cudaStream_t s) {
+    if (!dqh || p.n_tokens == 0) return cudaSuccess;
     const long long n = p.n_tokens * p.Hk * p.dk;
     const unsigned blocks = (unsigned)min((n + 255) / 256, 148ll * 16);
-    if (p.dtype == GDN_DTYPE_BF16) k_share<__nv_bfloat16><<<blocks, 256, 0, s>>>(p, w.dqh, w.dkh);
-    else k_share<float><<<blocks, 256, 0, s>>>(p, w.dqh, w.dkh);
+    if (p.dtype == GDN_DTYPE_BF16) k_share<__nv_bfloat16><<<blocks, 256, 0, s>>>(p, dqh, dkh);
+    else k_share<float><<<blocks, 256, 0, s>>>(p, dqh, dkh);
     return cudaGetLastError();
 }
 
@@ -517,7 +517,7 @@ cudaError_t launch_seq_bwd_simt(const SeqProblem &p, void *ws, cudaStream_t s) {
     seq_bwd_workspace(p, ws, &w);
     cudaError_t e = launch_seq_zero_rows(p, w.dqh, w.dkh, s);
     if (e == cudaSuccess && p.n_seqs) e = p.dtype == GDN_DTYPE_BF16 ? run<__nv_bfloat16>(p, w, s) : run<float>(p, w, s);
-    return e == cudaSuccess ? launch_seq_share(p, w, s) : e;
+    return e == cudaSuccess ? launch_seq_share(p, w.dqh, w.dkh, s) : e;
 }
 
 }  // namespace gdn
