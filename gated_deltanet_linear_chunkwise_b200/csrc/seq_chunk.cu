@@ -39,7 +39,7 @@ using sm100::cp_async16;
 
 constexpr int C = kSeqChunk;
 constexpr int NV = 16;       // rows of S (columns of d_v) that a block holds
-constexpr int PC = C + 8;    // pitch of a [16][64] plane: 9 x 16 bytes, odd, so ldmatrix rows spread over the banks
+constexpr int kPlane = NV * 128;  // bytes of a term's 16 rows of 64 columns, swizzled
 
 // T and P lie in the order of the B operand's fragments, a term behind the other: unit (t, b) is the n-tile of 8
 // tokens from 8t against the 16 tokens from 16b, a lane's two words of it.  Below the diagonal b <= t / 2 (20
@@ -51,10 +51,13 @@ constexpr int kUnits = 20;
 struct ChunkWork {
     uint2 *T, *P, *Tt, *Pt;  // [chunk x H][terms][20][32]; P or the transposes may be null
     float *gates;            // [chunk x H][3][64]: e^G, e^{G_L - G}, beta
-    double *G;               // [chunk x H][64], or null
-    float *Sig, *D;          // [chunk x H][dv][dk]
-    float *U, *X, *dR;       // [chunk x H][dv][64]: X = e^G K Sig
-    float *past, *into, *db; // [chunk x H][dv / 16][64]: a slice's part of the gates' gradients
+    float4 *gam;             // [chunk x H][20][32]: e^{G_i - G_j} (0 above the diagonal) in the order of a product's result, or null
+    // gdn_bwd: the chains' matrices as bf16 terms, in the swizzled 64-column lines that k_chunk_grads loads
+    bf16 *Sig;               // [chunk x H][slabs][3][dv][64]: the state entering the chunk
+    bf16 *D;                 // [chunk x H][slabs][2][dv][64]: the gradient of the one leaving it
+    bf16 *U, *dR;            // [chunk x H][3][dv][64 tokens]
+    float *X;                // [chunk x H][dv][64]: e^G K Sig
+    float *past, *into, *db, *all;  // [chunk x H][dv / 16][64] (all: [4]): a slice's part of the gates' gradients
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
 };
@@ -109,7 +112,6 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
             w.gates[idx * 3 * C + i] = expf((float)G[e]);
             w.gates[idx * 3 * C + C + i] = expf((float)(total - G[e]));
             w.gates[idx * 3 * C + 2 * C + i] = b[e];
-            if (w.G) w.G[idx * C + i] = G[e];
         }
     }
     sm100::cp_async_wait_all();
@@ -139,6 +141,7 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
     const int i0 = 16 * warp + lane / 4, j0 = 2 * (lane & 3);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
+        float gam[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int i = i0 + (e >> 1) * 8, j = 8 * t + j0 + (e & 1);
@@ -146,10 +149,11 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
                 sA[i][j] = 0.f;
                 continue;
             }
-            const float gam = j <= i ? expf((float)(sG[i] - sG[j])) : 0.f;
-            qk[t][e] *= gam;
-            sA[i][j] = j < i ? sB[i] * gam * kk[t][e] : 0.f;
+            gam[e] = j <= i ? expf((float)(sG[i] - sG[j])) : 0.f;
+            qk[t][e] *= gam[e];
+            sA[i][j] = j < i ? sB[i] * gam[e] * kk[t][e] : 0.f;
         }
+        if (w.gam && t / 2 <= warp) w.gam[(idx * kUnits + warp * (warp + 1) + t) * 32 + lane] = make_float4(gam[0], gam[1], gam[2], gam[3]);
     }
     auto put_unit = [&](uint2 *dst, int terms, int unit, float x0, float x1, float y0, float y1) {
         uint32_t a[3], b[3];
@@ -272,20 +276,20 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
     }
 }
 
-// Shared memory of a chain block, 1024-byte aligned.  Two blocks fit an SM: only K, which is read from a step's
-// first product to its last, has two buffers; the others are fetched again as soon as they have been read.
+// Shared memory of a chain block, 1024-byte aligned.  Only K, which is read from a step's first product to its
+// last, has two buffers; the others are fetched again as soon as they have been read.
 template <int NF, bool BWD> struct ChainSmem {
-    static constexpr int PK = 16 * NF + 8, kTile = (16 * NF + 63) / 64 * C * 64;
+    static constexpr int kSlabs = (NF + 3) / 4, kTile = kSlabs * C * 64;
     static constexpr int kTermsP = BWD ? 3 : 2;
-    bf16 K[2][kTile], Q[kTile];  // as the tensor maps leave them
+    bf16 K[2][kTile], Q[kTile];      // as the tensor maps leave them
+    bf16 S[kSlabs][3][NV][64];       // the state's terms, lines in the same swizzle, as all of the following
+    bf16 U[3][NV][64];               // e^{G_L-G} U; backwards e^G dO
+    bf16 R[3][NV][64];               // beta Y; backwards dU, then -beta e^G dR
+    bf16 W[3][NV][64];               // U (two terms for O, three to be kept); backwards dR
     uint2 T[3][kUnits][32], P[kTermsP][kUnits][32];
-    bf16 V[C][NV];               // v, or do
+    bf16 V[C][NV];                   // v, or do
     float gates[2][3][C];
-    bf16 S[3][NV][PK];           // the state's terms
-    bf16 U[3][NV][PC];           // e^{G_L-G} U; backwards e^G dO
-    bf16 R[3][NV][PC];           // beta Y; backwards dU, then -beta e^G dR
-    bf16 W[BWD ? 1 : 2][NV][PC]; // U for O
-    uint64_t bar[5];             // K and gates (two), Q, V, T, P
+    uint64_t bar[5];                 // K and gates (two), Q and V, T, P
 };
 enum { kBarK = 0, kBarV = 2, kBarT = 3, kBarP = 4 };
 // Four warps carry the state from chunk to chunk, four more (where O is wanted) compute it beside them, one fetches.
@@ -354,6 +358,7 @@ __device__ __forceinline__ void chain_leave(ChainSmem<NF, BWD> &sm, const SeqPro
     sm100::mbar_wait(&sm.bar[kBarV], now, err, sm100::kWaitLimitNs, true);
     sm100::mbar_wait(&sm.bar[kBarT], now, err, sm100::kWaitLimitNs, true);
     if (p_turn >= 0) sm100::mbar_wait(&sm.bar[kBarP], p_turn & 1, err, sm100::kWaitLimitNs, true);  // P's last fetch, if any
+    sm100::bulk_wait0();  // the fetching thread's copies to memory
     if (p.status && threadIdx.x == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
@@ -406,8 +411,7 @@ template <int NF> struct StateRows {
     }
 };
 template <int NF> __device__ __forceinline__ void put_state(uint32_t planes, StateRows<NF> &st, int warp, int lane) {
-    constexpr int PK = 16 * NF + 8;
-    const uint32_t at = planes + (lane / 4 * PK + 16 * warp + 2 * (lane & 3)) * 2;
+    const uint32_t at = planes + lane / 4 * 128 + 4 * (lane & 3), x0 = ((2 * warp) ^ (lane / 4)) << 4;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         if (warp + 4 * m >= NF) continue;
@@ -416,17 +420,23 @@ template <int NF> __device__ __forceinline__ void put_state(uint32_t planes, Sta
             uint32_t t[3];
             split(st.x[m][i / 2][2 * (i & 1)], st.x[m][i / 2][2 * (i & 1) + 1], t);
 #pragma unroll
-            for (int e = 0; e < 3; ++e) sts(at + (e * NV + (i & 1) * 8) * PK * 2 + 128 * m + 16 * (i / 2), t[e]);
+            for (int e = 0; e < 3; ++e) sts(at + (x0 ^ (i / 2 * 16)) + (3 * m + e) * kPlane + (i & 1) * 1024, t[e]);
         }
     }
 }
-// The address of a lane's pairs of tokens (tile t, rows n and n + 8) in a [16][64] plane.
-__device__ __forceinline__ uint32_t pair_addr(uint32_t plane, int t, int lane) { return plane + (lane / 4 * PC + 8 * t + 2 * (lane & 3)) * 2; }
+// The address of a lane's pairs of tokens (tile t, rows n and n + 8) in planes of 64 tokens.
+__device__ __forceinline__ uint32_t pair_addr(uint32_t planes, int t, int lane) {
+    return planes + lane / 4 * 128 + ((t ^ (lane / 4)) << 4) + 4 * (lane & 3);
+}
 template <int N> __device__ __forceinline__ void put_pair(uint32_t at, int half, float x, float y) {
     uint32_t t[N];
     split(x, y, t);
 #pragma unroll
-    for (int e = 0; e < N; ++e) sts(at + (e * NV + half * 8) * PC * 2, t[e]);
+    for (int e = 0; e < N; ++e) sts(at + e * kPlane + half * 1024, t[e]);
+}
+// A term's 16 lines from shared memory into a matrix of dv lines, by the copy engine.
+__device__ __forceinline__ void keep_plane(bf16 *dst, int dv, int c0, int plane, const void *src) {
+    sm100::bulk_copy_s2g(dst + ((size_t)plane * dv + c0) * 64, src, kPlane);
 }
 
 // st = decay st + sum over the planes pl: (plane's 3 terms [16][64 tokens]) x (rows [64 tokens][dk]).
@@ -437,11 +447,14 @@ __device__ __forceinline__ void update_state(StateRows<NF> &st, float decay, con
                                              int warp, int lane) {
     float hi[2][2][4], lo[2][2][4];
     uint32_t a[2][3][4], b[2][2][4];
-    const uint32_t al = a_lane(PC, lane), b0 = bt_lane(C, 16 * warp, lane), b1 = bt_lane(C, 16 * (warp + 4), lane);
+    const uint32_t b0 = bt_lane(C, 16 * warp, lane), b1 = bt_lane(C, 16 * (warp + 4), lane);
+    uint32_t al[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) al[x] = a_lane(x, lane);
     auto load = [&](int i) {
         const int s = i / 4, kb = i % 4;
 #pragma unroll
-        for (int e = 0; e < 3; ++e) ldsm4(a[i & 1][e], planes[s] + al + e * NV * PC * 2 + 32 * kb);
+        for (int e = 0; e < 3; ++e) ldsm4(a[i & 1][e], planes[s] + al[kb] + e * kPlane);
         if (warp < NF) ldsm4_t(b[i & 1][0], rows[s] + b0 + kb * 16 * 128);
         if (warp + 4 < NF) ldsm4_t(b[i & 1][1], rows[s] + b1 + kb * 16 * 128);
     };
@@ -475,14 +488,12 @@ __device__ __forceinline__ void update_state(StateRows<NF> &st, float decay, con
 // hi + lo = S rows^T for the token tiles t0, t1 of rows [64 tokens][dk], with TERMS terms of S.
 template <int NF, int TERMS>
 __device__ __forceinline__ void state_times(float (&hi)[2][4], float (&lo)[2][4], uint32_t planes, uint32_t rows, int t0, int t1, int lane) {
-    constexpr int PK = 16 * NF + 8;
-    uint32_t a[2][TERMS][4], b[2][4], bl[4];
-    planes += a_lane(PK, lane);
+    uint32_t a[2][TERMS][4], b[2][4], al[4], bl[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) bl[x] = rows + b_lane(8 * t0, 8 * t1, x, lane);
+    for (int x = 0; x < 4; ++x) al[x] = planes + a_lane(x, lane), bl[x] = rows + b_lane(8 * t0, 8 * t1, x, lane);
     auto load = [&](int ks) {
 #pragma unroll
-        for (int e = 0; e < TERMS; ++e) ldsm4(a[ks & 1][e], planes + e * NV * PK * 2 + 32 * ks);
+        for (int e = 0; e < TERMS; ++e) ldsm4(a[ks & 1][e], al[ks & 3] + (3 * (ks >> 2) + e) * kPlane);
         ldsm4(b[ks & 1], bl[ks & 3] + (ks >> 2) * C * 128);
     };
     load(0);
@@ -503,10 +514,10 @@ __device__ __forceinline__ void state_times(float (&hi)[2][4], float (&lo)[2][4]
 }
 
 // hi + lo = planes [16][64 tokens] x T (or P) for the token tiles t0 (the shorter one) and t1, from shared memory.
-// LOW: T as it is; else its transpose.  `planes`: A's address with the lane part; `step`: from 16 tokens to the next.
+// LOW: T as it is; else its transpose.  TRANS: one plane, held [64 tokens][16].
 template <bool LOW, int AT, int BT, bool TRANS = false>
-__device__ __forceinline__ void times_triangle(float (&hi)[2][4], float (&lo)[2][2][4], uint32_t planes, int term, int step, uint32_t tri,
-                                               int t0, int t1, int lane) {
+__device__ __forceinline__ void times_triangle(float (&hi)[2][4], float (&lo)[2][2][4], uint32_t planes, uint32_t tri, int t0, int t1,
+                                               int lane) {
     const int n0 = LOW ? t0 / 2 + 1 : 4 - t0 / 2, n1 = LOW ? t1 / 2 + 1 : 4 - t1 / 2;  // n0 <= 2, n1 >= 3
     uint32_t a[2][AT][4];
     uint2 f0[2][BT], f1[2][BT];
@@ -514,8 +525,9 @@ __device__ __forceinline__ void times_triangle(float (&hi)[2][4], float (&lo)[2]
     auto load = [&](int m) {
 #pragma unroll
         for (int e = 0; e < AT; ++e) {
-            const uint32_t at = planes + e * term + step * (LOW ? m : 3 - m);
-            TRANS ? ldsm4_t(a[m & 1][e], at) : ldsm4(a[m & 1][e], at);
+            const int x = LOW ? m : 3 - m;
+            if (TRANS) ldsm4_t(a[m & 1][e], planes + at_lane(NV, lane) + x * 16 * NV * 2);
+            else ldsm4(a[m & 1][e], planes + a_lane(x, lane) + e * kPlane);
         }
         if (m < 2 && m < n0) tri_frag<LOW, BT>(f0[m & 1], src0, m);
         tri_frag<LOW, BT>(f1[m & 1], src1, m);
@@ -537,7 +549,7 @@ __device__ __forceinline__ void times_triangle(float (&hi)[2][4], float (&lo)[2]
 template <int NF, bool SAVE>
 __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
                                                                 const __grid_constant__ ChainMaps maps) {
-    constexpr int DK = 16 * NF, PK = DK + 8, kSlabs = (DK + 63) / 64;
+    constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4;
     extern __shared__ unsigned char raw[];
     auto &sm = *reinterpret_cast<ChainSmem<NF, false> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const uint32_t aS = sm100::smem_u32(sm.S), aU = sm100::smem_u32(sm.U), aR = sm100::smem_u32(sm.R), aT = sm100::smem_u32(sm.T),
@@ -578,6 +590,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
+        if (SAVE) sm100::fence_proxy_async_smem();  // the state's terms go to memory by the copy engine
         ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err);
         // behind this barrier the state's terms are there and the last step's buffers have been read
         if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, SAVE ? -1 : (int)c - 1, w.err);
@@ -592,9 +605,18 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
             __syncthreads();
         }
         if (warp == kFetchWarp) {  // it keeps the barriers' count
+            if (SAVE && fetcher) {
+                for (int e = 0; e < 3 * kSlabs; ++e) keep_plane(w.Sig + idx * 3 * kSlabs * p.dv * 64, p.dv, c0, e, sm.S[e / 3][e % 3]);
+                sm100::bulk_commit();
+                sm100::bulk_wait_read0();  // these, and U's of the step before
+            }
             __syncthreads();
             if (fetcher && c + 1 < n_chunks) fetch.v(first_row(c + 1), !SAVE);
             __syncthreads();
+            if (SAVE && fetcher) {
+                for (int e = 0; e < 3; ++e) keep_plane(w.U + idx * 3 * p.dv * 64, p.dv, c0, e, sm.W[e]);
+                sm100::bulk_commit();
+            }
             if (fetcher && c + 1 < n_chunks) fetch.t(w.T + index(c + 1) * 3 * kUnits * 32);
             continue;
         }
@@ -604,7 +626,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
             ok = ok && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
             __syncthreads();
             __syncthreads();
-            times_triangle<true, 2, 2>(oh, ol, sm100::smem_u32(sm.W) + a_lane(PC, lane), NV * PC * 2, 32, aP, t0, t1, lane);
+            times_triangle<true, 2, 2>(oh, ol, sm100::smem_u32(sm.W), aP, t0, t1, lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
@@ -624,10 +646,6 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
             }
             continue;
         }
-        if (SAVE)
-            st.each(warp, lane, [&](int n, int col, float &x, float &y) {
-                *reinterpret_cast<float2 *>(w.Sig + (idx * p.dv + c0 + n) * DK + col) = make_float2(x, y);
-            });
         // X^T = S K^T
         float kh[2][4], kl[2][4];
         state_times<NF, 3>(kh, kl, aS, sm100::smem_u32(sm.K[b]), t0, t1, lane);
@@ -650,20 +668,20 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         __syncthreads();
         // U^T = (beta Y)^T T^T
         float uh[2][4], ul[2][2][4];
-        times_triangle<true, 3, 3>(uh, ul, aR + a_lane(PC, lane), NV * PC * 2, 32, aT, t0, t1, lane);
+        times_triangle<true, 3, 3>(uh, ul, aR, aT, t0, t1, lane);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
             const float2 el = *reinterpret_cast<const float2 *>(&sm.gates[b][1][tok]);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int n = lane / 4 + 8 * half, i = 2 * half;
+                const int i = 2 * half;
                 const float x = uh[t][i] + (ul[t][0][i] + ul[t][1][i]), y = uh[t][i + 1] + (ul[t][0][i + 1] + ul[t][1][i + 1]);
-                if (SAVE) *reinterpret_cast<float2 *>(w.U + (idx * p.dv + c0 + n) * C + tok) = make_float2(x, y);
                 put_pair<3>(pair_addr(aU, t ? t1 : t0, lane), half, el.x * x, el.y * y);
-                if (!SAVE) put_pair<2>(pair_addr(sm100::smem_u32(sm.W), t ? t1 : t0, lane), half, x, y);
+                put_pair<SAVE ? 3 : 2>(pair_addr(sm100::smem_u32(sm.W), t ? t1 : t0, lane), half, x, y);
             }
         }
+        if (SAVE) sm100::fence_proxy_async_smem();
         __syncthreads();
         const uint32_t planes[1] = {aU}, krows[1] = {sm100::smem_u32(sm.K[b])};
         update_state<NF, 1>(st, sm.gates[b][0][C - 1], planes, krows, warp, lane);
@@ -673,6 +691,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.S_out + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
+    if (SAVE && fetcher) sm100::bulk_wait0();
     // the last waits' answers: nobody reads buffers any more, so every thread may report for itself
     if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
@@ -680,7 +699,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
 template <int NF>
 __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
                                                                 const __grid_constant__ ChainMaps maps) {
-    constexpr int DK = 16 * NF, PK = DK + 8, kSlabs = (DK + 63) / 64;
+    constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4;
     extern __shared__ unsigned char raw[];
     auto &sm = *reinterpret_cast<ChainSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const uint32_t aS = sm100::smem_u32(sm.S), aU = sm100::smem_u32(sm.U), aR = sm100::smem_u32(sm.R), aT = sm100::smem_u32(sm.T),
@@ -721,6 +740,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
+        sm100::fence_proxy_async_smem();  // the state's terms go to memory by the copy engine
         ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err) &&
              sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
         if (!__syncthreads_and(ok)) return chain_leave(sm, p, turn, (int)turn, w.err);
@@ -732,22 +752,41 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             __syncthreads();
         }
         if (warp == 4) {
+            if (fetcher) {
+                for (int x = 0; x < kSlabs; ++x)
+                    for (int e = 0; e < 2; ++e) keep_plane(w.D + idx * 2 * kSlabs * p.dv * 64, p.dv, c0, 2 * x + e, sm.S[x][e]);
+                sm100::bulk_commit();
+                sm100::bulk_wait_read0();  // these, and dR's of the step before
+            }
             __syncthreads();
             if (fetcher && c > 0) fetch.v(first_row(c - 1), false);
             __syncthreads();
             if (fetcher && c > 0) fetch.t(w.Tt + index(c - 1) * 3 * kUnits * 32);
             __syncthreads();
+            if (fetcher) {
+                for (int e = 0; e < 3; ++e) keep_plane(w.dR + idx * 3 * p.dv * 64, p.dv, c0, e, sm.W[e]);
+                sm100::bulk_commit();
+            }
             __syncthreads();
             if (fetcher && c > 0) fetch.p(w.Pt + index(c - 1) * 3 * kUnits * 32, first_row(c - 1), true);
             continue;
         }
+        // <D, Sig>, from Sig's terms
+        float all = 0.f;
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
-            *reinterpret_cast<float2 *>(w.D + (idx * p.dv + c0 + n) * DK + col) = make_float2(x, y);
+            const char *src = (const char *)(w.Sig + idx * 3 * kSlabs * p.dv * 64) + ((size_t)(col >> 6) * 3 * p.dv + c0 + n) * 128 +
+                              sw_byte(0, 0, col & 56 ^ (n & 7) << 3) + (col & 7) * 2;
+            const uint32_t s0 = *reinterpret_cast<const uint32_t *>(src), s1 = *reinterpret_cast<const uint32_t *>(src + p.dv * 128),
+                           s2 = *reinterpret_cast<const uint32_t *>(src + p.dv * 256);
+            all = fmaf(x, low_of(s0) + (low_of(s1) + low_of(s2)), fmaf(y, high_of(s0) + (high_of(s1) + high_of(s2)), all));
         });
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        if (lane == 0) w.all[(idx * groups + c0 / NV) * 4 + warp] = all;
         // D^T K^T, and dO^T P
         float zh[2][4], zl[2][4], ph[2][4], pl[2][2][4];
         state_times<NF, 3>(zh, zl, aS, sm100::smem_u32(sm.K[b]), t0, t1, lane);
-        times_triangle<false, 1, 3, true>(ph, pl, sm100::smem_u32(sm.V) + at_lane(NV, lane), 0, 16 * NV * 2, aP, t0, t1, lane);
+        times_triangle<false, 1, 3, true>(ph, pl, sm100::smem_u32(sm.V), aP, t0, t1, lane);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
@@ -758,7 +797,10 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             for (int half = 0; half < 2; ++half) {
                 const int n = lane / 4 + 8 * half, i = 2 * half;
                 const float zx = el.x * (zh[t][i] + zl[t][i]), zy = el.y * (zh[t][i + 1] + zl[t][i + 1]);
-                const float2 u = *reinterpret_cast<const float2 *>(w.U + (idx * p.dv + c0 + n) * C + tok);
+                const char *src = (const char *)(w.U + (idx * 3 * p.dv + c0 + n) * 64) + ((tok / 8 ^ (n & 7)) << 4) + (tok & 7) * 2;
+                const uint32_t u0 = *reinterpret_cast<const uint32_t *>(src), u1 = *reinterpret_cast<const uint32_t *>(src + p.dv * 128),
+                               u2 = *reinterpret_cast<const uint32_t *>(src + p.dv * 256);
+                const float2 u = make_float2(low_of(u0) + (low_of(u1) + low_of(u2)), high_of(u0) + (high_of(u1) + high_of(u2)));
                 past0 = fmaf(u.x, zx, past0);
                 past1 = fmaf(u.y, zy, past1);
                 put_pair<3>(pair_addr(aR, t ? t1 : t0, lane), half, zx + (ph[t][i] + (pl[t][0][i] + pl[t][1][i])),
@@ -774,7 +816,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         __syncthreads();
         // dR^T = dU^T T
         float rh[2][4], rl[2][2][4];
-        times_triangle<false, 3, 3>(rh, rl, aR + a_lane(PC, lane), NV * PC * 2, 32, aT, t0, t1, lane);
+        times_triangle<false, 3, 3>(rh, rl, aR, aT, t0, t1, lane);
         __syncthreads();  // dU has been read: -beta e^G dR takes its place
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -786,9 +828,8 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             for (int half = 0; half < 2; ++half) {
                 const int n = lane / 4 + 8 * half, i = 2 * half;
                 const float x = rh[t][i] + (rl[t][0][i] + rl[t][1][i]), y = rh[t][i + 1] + (rl[t][0][i + 1] + rl[t][1][i + 1]);
-                const size_t at = (idx * p.dv + c0 + n) * C + tok;
-                *reinterpret_cast<float2 *>(w.dR + at) = make_float2(x, y);
-                const float2 X = *reinterpret_cast<const float2 *>(w.X + at);
+                put_pair<3>(pair_addr(sm100::smem_u32(sm.W), t ? t1 : t0, lane), half, x, y);
+                const float2 X = *reinterpret_cast<const float2 *>(w.X + (idx * p.dv + c0 + n) * C + tok);
                 const bf16 *vp = (const bf16 *)p.v + (row + tok) * p.v_stride + (size_t)h * p.dv + c0 + n;
                 bf16 *dvp = (bf16 *)p.dv_out + ((row + tok) * p.H + h) * p.dv + c0 + n;
                 const float bx = be.x * x, by = be.y * y;
@@ -813,6 +854,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
                 *reinterpret_cast<float2 *>(w.db + (idx * groups + c0 / NV) * C + tok) = make_float2(db0, db1);
             }
         }
+        sm100::fence_proxy_async_smem();
         __syncthreads();
         const uint32_t planes[2] = {aU, aR}, mrows[2] = {sm100::smem_u32(sm.Q), sm100::smem_u32(sm.K[b])};
         update_state<NF, 2>(st, sm.gates[b][0][C - 1], planes, mrows, warp, lane);
@@ -823,231 +865,140 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.dS_in + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
+    if (fetcher) sm100::bulk_wait0();
     if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
 // The gradients of a chunk and head from what the chains left: 8 warps, warp w has the 16 tokens from 16 (w % 4).
-// Warps 0-3 make dQ (and dK's part that sums over later tokens), warps 4-7 dK:
-//   dQ = e^G dO Sig^T + dP K,  dK = -beta e^G dR Sig^T + e^{G_L-G} U D^T + (beta dA) K + [dP; beta dA]^T [Q; K]
-// Products that reach the gates' fp32 gradients are at fp32 accuracy (dO Sig^T, dP, dA: every term); those that
-// only reach the bf16 dQ and dK take two terms of each operand.
-// Bound by the products: 6200 warp products at d = 112, 8 clocks each on a quarter of an SM.
-template <int NF> struct GradSmem {  // 1024-byte aligned
-    static constexpr int kTile = (16 * NF + 63) / 64 * C * 64;
-    bf16 K[kTile], Q[kTile], dO[2 * C * 64];  // swizzled rows
-    union {
-        bf16 SD[5][128 * 64];                 // 64 columns of Sig (3 terms) and D (2), [dv][64] swizzled
-        struct {
-            bf16 U[3][128 * 64];              // [dv][64 tokens] swizzled
-            bf16 PA[4][C][PC];                // dP and beta dA, 2 terms each
-        };
-        float kT[C][16 * NF + 4];
-    };
-    float M[C][C + 1];
-    double G[C];
-    float gates[3][C], into[C], past[C], db[C], red[8];
+// Warps 0-3 (role 0) make dQ, warps 4-7 dK, first the parts inside the chunk, then those through the states:
+//   dQ = dP K + e^G dO Sig^T,  dK = (beta dA) K + [dP; beta dA]^T [Q; K] - beta e^G dR Sig^T + e^{G_L-G} U D^T
+// Products that reach the gates' fp32 gradients are at fp32 accuracy (dP, dA, dO Sig^T: every term); those that only
+// reach the bf16 dQ and dK take two terms of each operand.  The matrices come as the terms that the chains had at
+// hand (converting fp32 here took more instructions than the products: 755 us against NNN).
+struct GradMaps {
+    CUtensorMap q, k, o;
+};
+// Shared memory, sizes from dv: K, Q, dO rows | U, dR first two terms | U, dR third terms, dP and beta dA, M; in the
+// place of the last, when they have been read, 64 columns of Sig and D.
+template <int NF> struct GradLayout {
+    static constexpr int kSlabs = (NF + 3) / 4, kTile = kSlabs * C * 128, kT = C * (16 * NF + 4) * 4, kPA = kT > 32768 ? kT : 32768;
+    int plane, K, Q, O, UR, last, PA, M, total;
+    __host__ __device__ explicit GradLayout(int dv) {
+        plane = dv * 128;
+        K = 0;
+        Q = K + kTile;
+        O = Q + kTile;
+        UR = O + 2 * C * 128;
+        last = UR + 4 * plane;
+        PA = last + 2 * plane;
+        M = PA + kPA;
+        total = M + C * (C + 1) * 4;  // 5 planes of Sig and D fit behind `last`: 3 planes are at most 48 KB
+    }
 };
 
 template <int NF>
-__global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w) {
-    constexpr int DK = 16 * NF;
+__global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
+                                                        const __grid_constant__ GradMaps maps) {
+    constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4, PM = C + 1;
     extern __shared__ unsigned char raw[];
-    auto &sm = *reinterpret_cast<GradSmem<NF> *>(raw + (-sm100::smem_u32(raw) & 1023));
+    __shared__ float gates[3][C], into[C], past[C], db[C], sums[4][C], dg[C];
+    __shared__ uint64_t bar[2];
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
     const int mt = warp & 3, role = warp >> 2, dv = p.dv, nvf = dv / 16;
     const SeqChunk ch = seq_chunk(p, c);
     if (ch.rows == 0) return;
     const size_t idx = (size_t)c * p.H + h;
-    auto rows_in = [&](bf16 *dst, const bf16 *src, long long stride, int pieces) {
-        for (int i = tid; i < C * pieces; i += 256) {
-            const int r = i / pieces, col = i % pieces * 8, on = r < ch.rows ? 16 : 0;
-            cp_async16((char *)dst + sw_byte(C, r, col), src + (ch.first + (on ? r : 0)) * stride + col, on);
+    const GradLayout<NF> at(dv);
+    unsigned char *const sm = raw + (-sm100::smem_u32(raw) & 1023);
+    const uint32_t base = sm100::smem_u32(sm), plane = at.plane;
+    if (tid == 0) {
+        sm100::mbar_init(&bar[0], 1);
+        sm100::mbar_init(&bar[1], 1);
+        sm100::fence_barrier_init();
+    }
+    __syncthreads();
+    const bf16 *Um = w.U + idx * 3 * dv * 64, *Rm = w.dR + idx * 3 * dv * 64;
+    if (tid == 0) {
+        sm100::mbar_arrive_expect_tx(&bar[0], 2 * at.kTile + (dv + 63) / 64 * C * 128 + 6 * plane);
+        for (int x = 0; x < kSlabs; ++x) {
+            sm100::tma_load_3d(sm + at.K + x * C * 128, &maps.k, &bar[0], 64 * x, hk, (int)ch.first);
+            sm100::tma_load_3d(sm + at.Q + x * C * 128, &maps.q, &bar[0], 64 * x, hk, (int)ch.first);
         }
-    };
-    rows_in(sm.dO, (const bf16 *)p.d_o + (size_t)h * dv, (long long)p.H * dv, dv / 8);
-    rows_in(sm.K, (const bf16 *)p.k + (size_t)hk * DK, p.k_stride, DK / 8);
-    rows_in(sm.Q, (const bf16 *)p.q + (size_t)hk * DK, p.q_stride, DK / 8);
-    sm100::cp_async_commit();
-    if (tid < 3 * C) sm.gates[0][tid] = w.gates[idx * 3 * C + tid];
+        for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.O + x * C * 128, &maps.o, &bar[0], 64 * x, h, (int)ch.first);
+        sm100::bulk_copy_g2s(sm + at.UR, Um, 2 * plane, &bar[0]);
+        sm100::bulk_copy_g2s(sm + at.UR + 2 * plane, Rm, 2 * plane, &bar[0]);
+        sm100::bulk_copy_g2s(sm + at.last, Um + 2 * dv * 64, plane, &bar[0]);
+        sm100::bulk_copy_g2s(sm + at.last + plane, Rm + 2 * dv * 64, plane, &bar[0]);
+    }
+    if (tid < 3 * C) gates[0][tid] = w.gates[idx * 3 * C + tid];
     if (tid < C) {
-        sm.G[tid] = w.G[idx * C + tid];
-        float past = 0.f, into = 0.f, db = 0.f;  // the slices' parts, in order
+        float x = 0.f, y = 0.f, z = 0.f;  // the slices' parts, in order
         for (int g = 0; g < nvf; ++g) {
-            past += w.past[(idx * nvf + g) * C + tid];
-            into += w.into[(idx * nvf + g) * C + tid];
-            db += w.db[(idx * nvf + g) * C + tid];
+            x += w.past[(idx * nvf + g) * C + tid];
+            y += w.into[(idx * nvf + g) * C + tid];
+            z += w.db[(idx * nvf + g) * C + tid];
         }
-        sm.past[tid] = past;
-        sm.into[tid] = into;
-        sm.db[tid] = db;
+        past[tid] = x;
+        into[tid] = y;
+        db[tid] = z;
     }
-    const float *Sig = w.Sig + idx * dv * DK, *Dm = w.D + idx * dv * DK, *Um = w.U + idx * dv * C, *Rm = w.dR + idx * dv * C;
-    const uint32_t aSD = sm100::smem_u32(sm.SD), aK = sm100::smem_u32(sm.K), aQ = sm100::smem_u32(sm.Q), aO = sm100::smem_u32(sm.dO);
-    constexpr uint32_t kPlane = 128 * 64 * 2;
     const int i0 = 16 * mt + lane / 4, j0 = 2 * (lane & 3);  // this lane's rows i0, i0 + 8; its columns 8 t + j0, + 1
-    // fragment of a fp32 [dv][64 tokens] matrix as the A operand (rows: this warp's tokens), NT terms
-    auto frag = [&](auto &a, const float *m, int ks) {
-        constexpr int NT = sizeof(a) / sizeof(a[0]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float *x = m + (size_t)(16 * ks + j0 + (e >> 1) * 8) * C + i0 + (e & 1) * 8;
-            uint32_t t[NT];
-            split(x[0], x[C], t);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) a[n][e] = t[n];
-        }
-    };
-    float acc[2 * NF][4];  // dQ's or dK's rows of this warp
-#pragma unroll
-    for (int t = 0; t < 2 * NF; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-    float all = 0.f;
-#pragma unroll
-    for (int slab = 0; slab < (NF + 3) / 4; ++slab) {
-        constexpr int kLast = DK % 64 ? DK % 64 : 64;
-        const int cols = slab + 1 < (NF + 3) / 4 ? 64 : kLast;
-        for (int i = tid; i < dv * (cols / 4); i += 256) {
-            const int n = i / (cols / 4), col = i % (cols / 4) * 4;
-            const float4 s = *reinterpret_cast<const float4 *>(Sig + (size_t)n * DK + 64 * slab + col);
-            const float4 d = *reinterpret_cast<const float4 *>(Dm + (size_t)n * DK + 64 * slab + col);
-            all += (s.x * d.x + s.y * d.y) + (s.z * d.z + s.w * d.w);
-            uint32_t a[3], b[3], e[2], f[2];
-            split(s.x, s.y, a);
-            split(s.z, s.w, b);
-            split(d.x, d.y, e);
-            split(d.z, d.w, f);
-            char *at = (char *)sm.SD + sw_byte(0, n, col) + (col & 4) * 2;
-#pragma unroll
-            for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2 *>(at + x * kPlane) = make_uint2(a[x], b[x]);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) *reinterpret_cast<uint2 *>(at + (3 + x) * kPlane) = make_uint2(e[x], f[x]);
-        }
-        sm100::cp_async_wait_all();
-        __syncthreads();
-        if (role == 0) {
-            float hi[8][4], lo[8][4];
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) hi[t][e] = lo[t][e] = 0.f;
-            for (int ks = 0; ks < nvf; ++ks) {
-                uint32_t a[4];
-                ldsm4(a, aO + sw_byte(C, 16 * mt + (lane & 15), 16 * ks + (lane >> 4) * 8));
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    if (16 * g >= cols) continue;
-                    uint32_t b[3][4];
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) ldsm4_t(b[x], aSD + x * kPlane + bt_lane(0, 16 * g, lane) + ks * 2048);
-#pragma unroll
-                    for (int x = 2; x >= 0; --x)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) mma::mma(x ? lo[2 * g + t] : hi[2 * g + t], a, b[x][2 * t], b[x][2 * t + 1]);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if (8 * slab + t >= 2 * NF) continue;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[(8 * slab + t) % (2 * NF)][e] = sm.gates[0][i0 + (e >> 1) * 8] * (hi[t][e] + lo[t][e]);
-            }
-        } else {
-            float x0[8][4], x1[8][4];
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x0[t][e] = x1[t][e] = 0.f;
-            for (int ks = 0; ks < nvf; ++ks) {
-                uint32_t r[2][4], u[2][4];
-                frag(r, Rm, ks);
-                frag(u, Um, ks);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    if (16 * g >= cols) continue;
-                    uint32_t b[2][4], d[2][4];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        ldsm4_t(b[x], aSD + x * kPlane + bt_lane(0, 16 * g, lane) + ks * 2048);
-                        ldsm4_t(d[x], aSD + (3 + x) * kPlane + bt_lane(0, 16 * g, lane) + ks * 2048);
-                    }
-#pragma unroll
-                    for (int x = 2; x >= 0; --x)  // terms (0, 1), (1, 0), (0, 0)
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            mma::mma(x0[2 * g + t], r[x == 1], b[x == 2][2 * t], b[x == 2][2 * t + 1]);
-                            mma::mma(x1[2 * g + t], u[x == 1], d[x == 2][2 * t], d[x == 2][2 * t + 1]);
-                        }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if (8 * slab + t >= 2 * NF) continue;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = i0 + (e >> 1) * 8;
-                    acc[(8 * slab + t) % (2 * NF)][e] = fmaf(-sm.gates[2][i] * sm.gates[0][i], x0[t][e], sm.gates[1][i] * x1[t][e]);
-                }
-            }
-        }
+    if (!__syncthreads_and(sm100::mbar_wait(&bar[0], 0, w.err))) {
+        sm100::mbar_wait(&bar[0], 0, w.err, sm100::kWaitLimitNs, true);
+        if (p.status && tid == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
+        return;
+    }
+    if (ch.rows < C) {
+        zero_tail((bf16 *)(sm + at.K), kSlabs, 8, ch.rows);
+        zero_tail((bf16 *)(sm + at.Q), kSlabs, 8, ch.rows);
+        zero_tail((bf16 *)(sm + at.O), (dv + 63) / 64, 8, ch.rows);
         __syncthreads();
     }
+    const uint32_t aK = base + at.K, aQ = base + at.Q, aO = base + at.O;
+    // lane parts: an A operand from token rows; from [dv][64 tokens] lines; two n-tiles of a B operand from 64-column lines
+    const uint32_t rows_at = (16 * mt + (lane & 15)) * 128;
+    auto row_a = [&](uint32_t tile, int ks) {
+        return tile + rows_at + (ks >> 2) * C * 128 + (((2 * (ks & 3) + (lane >> 4)) ^ (lane & 7)) << 4);
+    };
+    const uint32_t lines_a = ((lane >> 4) * 8 + (lane & 7)) * 128 + (((2 * mt + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+    uint32_t lines_b[4];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    if (lane == 0) sm.red[warp] = all;
-    // a pair of a row of K or Q
-    auto pair = [&](const bf16 *tile, int row, int col) {
-        return *reinterpret_cast<const uint32_t *>((const char *)tile + sw_byte(C, row, col) + (col & 7) * 2);
+    for (int g = 0; g < 4; ++g) lines_b[g] = bt_lane(0, 16 * g, lane);
+    auto pair = [&](int tile, int row, int col) {  // of a row of K or Q
+        return *reinterpret_cast<const uint32_t *>(sm + tile + sw_byte(C, row, col) + (col & 7) * 2);
     };
     auto quad = [](float x) {
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         return x + __shfl_xor_sync(0xffffffffu, x, 2);
     };
-    if (role == 0) {  // q . dq so far: the terms that come from before the chunk
-        float x[2] = {};
-#pragma unroll
-        for (int t = 0; t < 2 * NF; ++t)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t q = pair(sm.Q, i0 + 8 * half, 8 * t + j0);
-                x[half] += low_of(q) * acc[t][2 * half] + high_of(q) * acc[t][2 * half + 1];
-            }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const float y = quad(x[half]);
-            if ((lane & 3) == 0) sm.into[i0 + 8 * half] += y;
-        }
-    }
-    // dP, dA
-    for (int i = tid; i < dv * (C / 4); i += 256) {
-        const int n = i / (C / 4), col = i % (C / 4) * 4;
-        const float4 u = *reinterpret_cast<const float4 *>(Um + (size_t)n * C + col);
-        uint32_t a[3], b[3];
-        split(u.x, u.y, a);
-        split(u.z, u.w, b);
-        char *at = (char *)sm.U + sw_byte(0, n, col) + (col & 4) * 2;
-#pragma unroll
-        for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2 *>(at + x * kPlane) = make_uint2(a[x], b[x]);
-    }
-    __syncthreads();
-    uint32_t op[4][2][4];  // dP's or dA's rows as an A operand, two terms
+    float acc[2 * NF][4];  // dQ's or dK's rows of this warp
+    // ---- inside the chunk
     {
+        uint32_t op[4][2][4];  // dP's or dA's rows as an A operand, two terms
         float hi[8][4], lo[8][4], kk[8][4];
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) hi[t][e] = lo[t][e] = kk[t][e] = 0.f;
+        const uint32_t u01 = base + at.UR, u2 = base + at.last;
+#pragma unroll 1
         for (int ks = 0; ks < nvf; ++ks) {
             uint32_t a[3][4];
-            if (role == 0) ldsm4(a[0], aO + sw_byte(C, 16 * mt + (lane & 15), 16 * ks + (lane >> 4) * 8));
-            else frag(a, Rm, ks);
+            if (role == 0) {
+                ldsm4(a[0], row_a(aO, ks));
+            } else {
+                ldsm4_t(a[0], u01 + 2 * plane + lines_a + ks * 2048);
+                ldsm4_t(a[1], u01 + 3 * plane + lines_a + ks * 2048);
+                ldsm4_t(a[2], u2 + plane + lines_a + ks * 2048);
+            }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                if (g > mt) continue;
+                if (g > mt) break;
                 uint32_t b[3][4];
-#pragma unroll
-                for (int x = 0; x < 3; ++x) ldsm4_t(b[x], aSD + x * kPlane + bt_lane(0, 16 * g, lane) + ks * 2048);
+                ldsm4_t(b[0], u01 + lines_b[g] + ks * 2048);
+                ldsm4_t(b[1], u01 + plane + lines_b[g] + ks * 2048);
+                ldsm4_t(b[2], u2 + lines_b[g] + ks * 2048);
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -1061,128 +1012,116 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             }
         }
         const uint32_t left = role ? aK : aQ;
-#pragma unroll
+#pragma unroll 1
         for (int ks = 0; ks < NF; ++ks) {
             uint32_t a[4];
-            ldsm4(a, left + sw_byte(C, 16 * mt + (lane & 15), 16 * ks + (lane >> 4) * 8));
+            ldsm4(a, row_a(left, ks));
+            const uint32_t k = aK + b_lane(0, 8, ks & 3, lane) + (ks >> 2) * C * 128;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                if (g > mt) continue;
+                if (g > mt) break;
                 uint32_t b[4];
-                ldsm4(b, aK + b_lane(16 * g, 16 * g + 8, ks & 3, lane) + (ks >> 2) * C * 128);
+                ldsm4(b, k + g * 2048);
                 mma::mma(kk[2 * g], a, b[0], b[1]);
                 mma::mma(kk[2 * g + 1], a, b[2], b[3]);
             }
         }
+        float *M = reinterpret_cast<float *>(sm + at.M);
+        const uint32_t aPA = base + at.PA + role * 2 * C * 128;
+        const float4 *gam = w.gam + (idx * kUnits + mt * (mt + 1)) * 32 + lane;
+        const float be0 = role ? gates[2][i0] : 1.f, be1 = role ? gates[2][i0 + 8] : 1.f;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
+            const float4 g4 = t / 2 <= mt ? gam[t * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float gm[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int i = i0 + 8 * half, j = 8 * t + j0;
-                const float be = role ? sm.gates[2][i] : 1.f;
-                float x[2], m[2];
+                const float be = half ? be1 : be0;
+                float x[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const bool in = role ? j + e < i : j + e <= i;
-                    const float gam = in ? expf((float)(sm.G[i] - sm.G[j + e])) : 0.f;
-                    x[e] = gam * (hi[t][2 * half + e] + lo[t][2 * half + e]);
-                    if (role) x[e] = -x[e];
-                    m[e] = be * x[e] * kk[t][2 * half + e];
+                    x[e] = gm[2 * half + e] * (hi[t][2 * half + e] + lo[t][2 * half + e]);
+                    if (role) x[e] = j + e < i ? -x[e] : 0.f;
+                    if (role == 0) M[i * PM + j + e] = x[e] * kk[t][2 * half + e];  // role 1 adds its own behind the barrier
                 }
                 uint32_t s[2];
                 split(x[0], x[1], s);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) op[t / 2][n][half + 2 * (t & 1)] = s[n];
-                split(be * x[0], be * x[1], s);
+                hi[t][2 * half] = be * x[0] * kk[t][2 * half];
+                hi[t][2 * half + 1] = be * x[1] * kk[t][2 * half + 1];
+                if (role) split(be * x[0], be * x[1], s);
 #pragma unroll
-                for (int n = 0; n < 2; ++n) *reinterpret_cast<uint32_t *>(&sm.PA[2 * role + n][i][j]) = s[n];
-                hi[t][2 * half] = m[0];
-                hi[t][2 * half + 1] = m[1];
+                for (int n = 0; n < 2; ++n) sts(aPA + n * C * 128 + sw_byte(0, i, 8 * t) + j0 * 2, s[n]);
             }
         }
-        auto put_m = [&](bool add) {
+        __syncthreads();
+        if (role) {
 #pragma unroll
             for (int t = 0; t < 8; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float &m = sm.M[i0 + (e >> 1) * 8][8 * t + j0 + (e & 1)];
-                    m = add ? m + hi[t][e] : hi[t][e];
-                }
-        };
-        if (role == 0) put_m(false);
-        __syncthreads();
-        if (role) put_m(true);
-    }
-    // rows x K: dQ's or dK's part inside the chunk
-#pragma unroll
-    for (int g = 0; g < NF; ++g) {
-        float x[2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-            if (kb > mt) continue;
-            uint32_t b[4];
-            ldsm4_t(b, aK + bt_lane(C, 16 * g, lane) + kb * 2048);
-#pragma unroll
-            for (int n = 1; n >= 0; --n)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) mma::mma(x[t], op[kb][n], b[2 * t], b[2 * t + 1]);
+                for (int e = 0; e < 4; ++e) M[(i0 + (e >> 1) * 8) * PM + 8 * t + j0 + (e & 1)] += hi[t][e];
         }
-        float db[2] = {};
+        // rows x K
+        float part[2] = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int g = 0; g < NF; ++g) {
+            float x[2][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = i0 + 8 * half;
-                const float be = role ? sm.gates[2][i] : 1.f;
-                if (role) {
-                    const uint32_t k = pair(sm.K, i, 16 * g + 8 * t + j0);
-                    db[half] += low_of(k) * x[t][2 * half] + high_of(k) * x[t][2 * half + 1];
-                }
-                acc[2 * g + t][2 * half] = fmaf(be, x[t][2 * half], acc[2 * g + t][2 * half]);
-                acc[2 * g + t][2 * half + 1] = fmaf(be, x[t][2 * half + 1], acc[2 * g + t][2 * half + 1]);
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+            const uint32_t k = aK + bt_lane(C, 16 * g, lane);
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb > mt) break;
+                uint32_t b[4];
+                ldsm4_t(b, k + kb * 2048);
+#pragma unroll
+                for (int n = 1; n >= 0; --n)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) mma::mma(x[t], op[kb][n], b[2 * t], b[2 * t + 1]);
             }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (role) {
+                        const uint32_t kv = pair(at.K, i0 + 8 * half, 16 * g + 8 * t + j0);
+                        part[half] += low_of(kv) * x[t][2 * half] + high_of(kv) * x[t][2 * half + 1];
+                    }
+                    const float be = half ? be1 : be0;
+                    acc[2 * g + t][2 * half] = be * x[t][2 * half];
+                    acc[2 * g + t][2 * half + 1] = be * x[t][2 * half + 1];
+                }
+        }
         if (role)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float y = quad(db[half]);
-                if ((lane & 3) == 0) sm.db[i0 + 8 * half] += y;
+                const float y = quad(part[half]);
+                if ((lane & 3) == 0) db[i0 + 8 * half] += y;
             }
     }
-    auto store = [&](bf16 *dst, float *dst32) {
+    // rows j of [dP; beta dA]^T [Q; K]: half of the columns by each role, handed over through shared memory
+    float *const kT = reinterpret_cast<float *>(sm + at.PA);
+    {
+        constexpr int kMine = (NF + 1) / 2;  // groups of 16 columns: role 0 the first ones, role 1 the others
+        float x[2 * kMine][4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = i0 + 8 * half;
-            if (i >= ch.rows) continue;
-            const size_t at = ((size_t)(ch.first + i) * p.H + h) * DK + j0;
-#pragma unroll
-            for (int t = 0; t < 2 * NF; ++t) {
-                if (dst32) *reinterpret_cast<float2 *>(dst32 + at + 8 * t) = make_float2(acc[t][2 * half], acc[t][2 * half + 1]);
-                else *reinterpret_cast<uint32_t *>(dst + at + 8 * t) = pack(acc[t][2 * half], acc[t][2 * half + 1]);
-            }
-        }
-    };
-    __syncthreads();  // U has been read (dP, dA: before the last barrier), PA is complete; M too
-    if (role == 0) {
-        store((bf16 *)p.dq, w.dqh);
-        // rows j of [dP; beta dA]^T [Q; K]
-        float x[2 * NF][4];
-#pragma unroll
-        for (int t = 0; t < 2 * NF; ++t)
+        for (int t = 0; t < 2 * kMine; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-        const uint32_t aPA = sm100::smem_u32(sm.PA) + at_lane(PC, lane) + 32 * mt;
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-            if (kb < mt) continue;
+        const uint32_t pa = base + at.PA + lines_a;
+#pragma unroll 1
+        for (int kb = mt; kb < 4; ++kb) {
             uint32_t a[4][4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) ldsm4_t(a[n], aPA + n * C * PC * 2 + kb * 16 * PC * 2);
+            for (int n = 0; n < 4; ++n) ldsm4_t(a[n], pa + n * C * 128 + kb * 2048);
 #pragma unroll
-            for (int g = 0; g < NF; ++g) {
+            for (int y = 0; y < kMine; ++y) {
+                const int g = role ? kMine + y : y;
+                if (g >= NF) break;
                 uint32_t q[4], k[4];
                 ldsm4_t(q, aQ + bt_lane(C, 16 * g, lane) + kb * 2048);
                 ldsm4_t(k, aK + bt_lane(C, 16 * g, lane) + kb * 2048);
@@ -1190,47 +1129,181 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                 for (int n = 1; n >= 0; --n)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        mma::mma(x[2 * g + t], a[n], q[2 * t], q[2 * t + 1]);
-                        mma::mma(x[2 * g + t], a[2 + n], k[2 * t], k[2 * t + 1]);
+                        mma::mma(x[2 * y + t], a[n], q[2 * t], q[2 * t + 1]);
+                        mma::mma(x[2 * y + t], a[2 + n], k[2 * t], k[2 * t + 1]);
                     }
             }
         }
+        // sums of M's columns over the rows from each row on: a quarter of the rows a thread, then the quarters below
+        float *M = reinterpret_cast<float *>(sm + at.M);
+        __syncthreads();  // M is complete, PA has been read
+        {
+            const int j = tid & 63, q = tid >> 6;
+            float s = 0.f;
 #pragma unroll
-        for (int t = 0; t < 2 * NF; ++t)
+            for (int i = 15; i >= 0; --i) {
+                s += M[(16 * q + i) * PM + j];
+                M[(16 * q + i) * PM + j] = s;
+            }
+            sums[q][j] = s;
+        }
+        if (role == 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t][e] = x[t][e];
-    } else if (warp < 6) {
-        const int j = tid - 128;  // column sums of M over the rows from each row on
-        for (int i = C - 2; i >= 0; --i) sm.M[i][j] += sm.M[i + 1][j];
+            for (int t = 0; t < 2 * kMine; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    *reinterpret_cast<float2 *>(kT + (i0 + 8 * half) * (DK + 4) + 8 * t + j0) = make_float2(x[t][2 * half], x[t][2 * half + 1]);
+        } else {
+#pragma unroll
+            for (int t = 2 * kMine; t < 2 * NF; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][e] += x[t - 2 * kMine][e];
+        }
+        __syncthreads();
+        if (role) {
+#pragma unroll
+            for (int t = 0; t < 2 * kMine && t < 2 * NF; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float2 y = *reinterpret_cast<const float2 *>(kT + (i0 + 8 * half) * (DK + 4) + 8 * t + j0);
+                    acc[t][2 * half] += y.x;
+                    acc[t][2 * half + 1] += y.y;
+                }
+        }
+        {  // row i of the sums: the columns before it, four threads a row
+            const int i = tid >> 2;
+            float s = 0.f;
+            for (int j = tid & 3; j < i; j += 4) {
+                s += M[i * PM + j];
+                for (int q = i / 16 + 1; q < 4; ++q) s += sums[q][j];
+            }
+            s = quad(s);
+            if ((tid & 3) == 0) dg[i] = s;
+        }
+        sm100::fence_proxy_async_smem();
+        __syncthreads();  // all that the state's columns take the place of has been read
     }
-    __syncthreads();  // PA has been read: kT lies there
-    if (role == 0) {
+    // ---- through the states
+    float part[2] = {};
 #pragma unroll
-        for (int t = 0; t < 2 * NF; ++t)
+    for (int slab = 0; slab < kSlabs; ++slab) {
+        constexpr int kLast = NF % 4 ? NF % 4 : 4;
+        constexpr int kFull = 4;
+        const int groups = slab + 1 < kSlabs ? kFull : kLast;  // of 16 columns
+        if (tid == 0) {
+            sm100::mbar_arrive_expect_tx(&bar[1], 5 * plane);
+            sm100::bulk_copy_g2s(sm + at.last, w.Sig + (idx * kSlabs + slab) * 3 * dv * 64, 3 * plane, &bar[1]);
+            sm100::bulk_copy_g2s(sm + at.last + 3 * plane, w.D + (idx * kSlabs + slab) * 2 * dv * 64, 2 * plane, &bar[1]);
+        }
+        if (!__syncthreads_and(sm100::mbar_wait(&bar[1], slab, w.err))) {
+            sm100::mbar_wait(&bar[1], slab, w.err, sm100::kWaitLimitNs, true);
+            if (p.status && tid == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
+            return;
+        }
+        const uint32_t s0 = base + at.last, u01 = base + at.UR;
+        float x[8][4], y[8][4];  // role 0: leading and small products; role 1: dR Sig^T and U D^T
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-                *reinterpret_cast<float2 *>(&sm.kT[i0 + 8 * half][8 * t + j0]) = make_float2(acc[t][2 * half], acc[t][2 * half + 1]);
-    }
-    __syncthreads();
-    if (role) {
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int t = 0; t < 2 * NF; ++t)
+            for (int e = 0; e < 4; ++e) x[t][e] = y[t][e] = 0.f;
+        if (role == 0) {
+#pragma unroll 1
+            for (int ks = 0; ks < nvf; ++ks) {
+                uint32_t a[4];
+                ldsm4(a, row_a(aO, ks));
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (g >= groups) break;
+                    uint32_t b[3][4];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) ldsm4_t(b[n], s0 + n * plane + lines_b[g] + ks * 2048);
+#pragma unroll
+                    for (int n = 2; n >= 0; --n)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) mma::mma(n ? y[2 * g + t] : x[2 * g + t], a, b[n][2 * t], b[n][2 * t + 1]);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int ks = 0; ks < nvf; ++ks) {
+                uint32_t r[2][4], u[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    ldsm4_t(u[n], u01 + n * plane + lines_a + ks * 2048);
+                    ldsm4_t(r[n], u01 + (2 + n) * plane + lines_a + ks * 2048);
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (g >= groups) break;
+                    uint32_t b[2][4], d[2][4];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        ldsm4_t(b[n], s0 + n * plane + lines_b[g] + ks * 2048);
+                        ldsm4_t(d[n], s0 + (3 + n) * plane + lines_b[g] + ks * 2048);
+                    }
+#pragma unroll
+                    for (int n = 2; n >= 0; --n)  // terms (0, 1), (1, 0), (0, 0)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            mma::mma(x[2 * g + t], r[n == 1], b[n == 2][2 * t], b[n == 2][2 * t + 1]);
+                            mma::mma(y[2 * g + t], u[n == 1], d[n == 2][2 * t], d[n == 2][2 * t + 1]);
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            if (t >= 2 * groups) break;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float2 x = *reinterpret_cast<const float2 *>(&sm.kT[i0 + 8 * half][8 * t + j0]);
-                acc[t][2 * half] += x.x;
-                acc[t][2 * half + 1] += x.y;
+                const int i = i0 + 8 * half;
+                float *to = acc[(8 * slab + t) % (2 * NF)] + 2 * half;
+                if (role == 0) {
+                    const float eg = gates[0][i], z0 = eg * (x[t][2 * half] + y[t][2 * half]), z1 = eg * (x[t][2 * half + 1] + y[t][2 * half + 1]);
+                    const uint32_t q = pair(at.Q, i, 64 * slab + 8 * t + j0);
+                    part[half] += low_of(q) * z0 + high_of(q) * z1;
+                    to[0] += z0;
+                    to[1] += z1;
+                } else {
+                    const float s = -gates[2][i] * gates[0][i], el = gates[1][i];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) to[e] += fmaf(s, x[t][2 * half + e], el * y[t][2 * half + e]);
+                }
             }
-        store((bf16 *)p.dk_out, w.dkh);
-    } else if (tid < ch.rows) {
+        }
+        __syncthreads();
+    }
+    if (role == 0)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float x = quad(part[half]);
+            if ((lane & 3) == 0) into[i0 + 8 * half] += x;
+        }
+    {
+        bf16 *const dst = role ? (bf16 *)p.dk_out : (bf16 *)p.dq;
+        float *const dst32 = role ? w.dkh : w.dqh;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = i0 + 8 * half;
+            if (i >= ch.rows) continue;
+            const size_t to = ((size_t)(ch.first + i) * p.H + h) * DK + j0;
+#pragma unroll
+            for (int t = 0; t < 2 * NF; ++t) {
+                if (dst32) *reinterpret_cast<float2 *>(dst32 + to + 8 * t) = make_float2(acc[t][2 * half], acc[t][2 * half + 1]);
+                else *reinterpret_cast<uint32_t *>(dst + to + 8 * t) = pack(acc[t][2 * half], acc[t][2 * half + 1]);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < ch.rows) {
         float g = 0.f;
-        for (int i = 0; i < 8; ++i) g += sm.red[i];
-        g *= sm.gates[0][C - 1];
-        for (int j = 0; j < tid; ++j) g += sm.M[tid][j] + sm.past[j];
-        for (int i = tid; i < C; ++i) g += sm.into[i];
-        const size_t at = (size_t)(ch.first + tid) * p.H + h;
-        p.dalpha[at] = g / fmaxf(p.alpha[at], expf(kSeqBwdLogFloor));
-        p.dbeta[at] = sm.db[tid];
+        for (int i = 0; i < 4 * nvf; ++i) g += w.all[idx * 4 * nvf + i];
+        g = fmaf(g, gates[0][C - 1], dg[tid]);
+        for (int j = 0; j < tid; ++j) g += past[j];
+        for (int i = tid; i < C; ++i) g += into[i];
+        const size_t to = (size_t)(ch.first + tid) * p.H + h;
+        p.dalpha[to] = g / fmaxf(p.alpha[to], expf(kSeqBwdLogFloor));
+        p.dbeta[to] = db[tid];
     }
 }
 
@@ -1267,10 +1340,14 @@ template <int NF> cudaError_t bwd(const SeqProblem &p, const ChunkWork &w, cudaS
     cudaError_t e = prep<NF>(p, w, kSeqBwdLogFloor, s);
     if (!e) e = chain<decltype(&k_chunk_fwd<NF, true>), NF, false>(k_chunk_fwd<NF, true>, chain_threads(false), p, w, m, s);
     if (!e) e = chain<decltype(&k_chunk_bwd<NF>), NF, true>(k_chunk_bwd<NF>, chain_threads(false), p, w, mo, s);
-    const int bytes = (int)sizeof(GradSmem<NF>) + 1024;
+    GradMaps g;
+    g.q = m.q;
+    g.k = m.k;
+    if (!seq_row_map(&g.o, p.d_o, p.n_tokens, (long long)p.H * p.dv, p.H, p.dv, 64)) return cudaErrorInvalidValue;
+    const int bytes = GradLayout<NF>(p.dv).total + 1024;
     if (!e) e = cudaFuncSetAttribute(k_chunk_grads<NF>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e) return e;
-    k_chunk_grads<NF><<<(unsigned)(seq_max_chunks(p) * p.H), 256, bytes, s>>>(p, w);
+    k_chunk_grads<NF><<<(unsigned)(seq_max_chunks(p) * p.H), 256, bytes, s>>>(p, w, g);
     return cudaGetLastError();
 }
 
@@ -1292,12 +1369,14 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
     } else {
         w.Tt = (uint2 *)take(3 * frag);
         w.Pt = (uint2 *)take(3 * frag);
-        w.G = (double *)take(n * C * 8);
-        w.Sig = (float *)take(n * p.dk * p.dv * 4);
-        w.D = (float *)take(n * p.dk * p.dv * 4);
-        w.U = (float *)take(n * C * p.dv * 4);
+        const size_t lines = n * p.dv * 128, slabs = (p.dk + 63) / 64;  // bytes of a term of a 64-column slab
+        w.gam = (float4 *)take(n * kUnits * 32 * sizeof(float4));
+        w.Sig = (bf16 *)take(3 * slabs * lines);
+        w.D = (bf16 *)take(2 * slabs * lines);
+        w.U = (bf16 *)take(3 * lines);
+        w.dR = (bf16 *)take(3 * lines);
         w.X = (float *)take(n * C * p.dv * 4);
-        w.dR = (float *)take(n * C * p.dv * 4);
+        w.all = (float *)take(n * (p.dv / NV) * 4 * 4);
         w.past = (float *)take(n * (p.dv / NV) * C * 4);
         w.into = (float *)take(n * (p.dv / NV) * C * 4);
         w.db = (float *)take(n * (p.dv / NV) * C * 4);

@@ -58,9 +58,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 }
 
 // Lane parts of fragment addresses (bytes).
-// A operand held row-major (k contiguous), `pitch` elements a row: lanes 0-15 give the rows of the left 8 columns
-// of a 16 x 16 tile, 16-31 those of the right 8.
-__device__ __forceinline__ uint32_t a_lane(int pitch, int lane) { return ((lane & 15) * pitch + (lane >> 4) * 8) * 2; }
 // A operand held [k][m] (m contiguous), for ldsm4_t.
 __device__ __forceinline__ uint32_t at_lane(int pitch, int lane) {
     return (((lane >> 4) * 8 + (lane & 7)) * pitch + ((lane >> 3) & 1) * 8) * 2;
@@ -70,6 +67,9 @@ __device__ __forceinline__ uint32_t at_lane(int pitch, int lane) {
 __host__ __device__ constexpr uint32_t sw_byte(int rows, int row, int col) {
     return (col >> 6) * rows * 128 + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4);
 }
+// A operand of 16 rows held row-major in swizzled rows: lanes 0-15 give the rows of the left 8 columns of a 16 x 16
+// tile, 16-31 those of the right 8; the tile at column 16 x (of 64).
+__device__ __forceinline__ uint32_t a_lane(int x, int lane) { return sw_byte(0, lane & 15, 16 * x + (lane >> 4) * 8); }
 // Two n-tiles (8 rows from n0, 8 from n1, multiples of 8) of a B operand held [n][k] in swizzled rows: r[0], r[1]
 // are the first tile's fragment, r[2], r[3] the second's.  The lane part for a k step at column 16 x (of 64).
 __device__ __forceinline__ uint32_t b_lane(int n0, int n1, int x, int lane) {
