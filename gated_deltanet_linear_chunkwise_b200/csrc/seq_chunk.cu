@@ -23,6 +23,7 @@
 // round trip through tensor memory for each of three dependent products of a step.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cstdlib>
 
 #include "gates.cuh"
 #include "seq_internal.h"
@@ -54,10 +55,9 @@ struct ChunkWork {
     float4 *gam;             // [chunk x H][20][32]: e^{G_i - G_j} (0 above the diagonal) in the order of a product's result, or null
     // gdn_bwd: the chains' matrices as bf16 terms, in the swizzled 64-column lines that k_chunk_grads loads
     bf16 *Sig;               // [chunk x H][slabs][3][dv][64]: the state entering the chunk
-    bf16 *D;                 // [chunk x H][slabs][2][dv][64]: the gradient of the one leaving it
+    bf16 *D;                 // [chunk x H][slabs][3][dv][64]: the gradient of the one leaving it
     bf16 *U, *dR;            // [chunk x H][3][dv][64 tokens]
-    float *X;                // [chunk x H][dv][64]: e^G K Sig
-    float *past, *into, *db, *all;  // [chunk x H][dv / 16][64] (all: [4]): a slice's part of the gates' gradients
+    float *X, *Z;            // [chunk x H][dv][64]: (e^G K Sig)^T, (e^{G_L-G} K D)^T
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
 };
@@ -343,9 +343,9 @@ __device__ __forceinline__ void zero_tail(bf16 *tile, int slabs, int pieces, int
 }
 
 // Before the first fetch.
-template <int NF, bool BWD> __device__ __forceinline__ void chain_init(ChainSmem<NF, BWD> &sm) {
+__device__ __forceinline__ void chain_init(uint64_t (&bar)[5]) {
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 5; ++i) sm100::mbar_init(&sm.bar[i], 1);
+        for (int i = 0; i < 5; ++i) sm100::mbar_init(&bar[i], 1);
         sm100::fence_barrier_init();
     }
     __syncthreads();
@@ -386,13 +386,6 @@ template <bool LOW, int TERMS> __device__ __forceinline__ void tri_frag(uint2 (&
 }
 template <bool LOW> __device__ __forceinline__ uint32_t tri_addr(uint32_t src, int t, int lane) {
     return src + (LOW ? low_unit(t) : up_unit(t) + 3 - t / 2) * 256 + lane * 8;
-}
-
-// Sum over the lanes that hold the other rows of the same columns.
-__device__ __forceinline__ float rows_sum(float x) {
-    x += __shfl_xor_sync(0xffffffffu, x, 4);
-    x += __shfl_xor_sync(0xffffffffu, x, 8);
-    return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
 // The S (or D^T) rows of a block: warp w has the column pairs (16 columns) w and w + 4.
@@ -566,7 +559,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
     const bool fetcher = threadIdx.x == 32 * kFetchWarp;
     auto index = [&](long long c) { return (size_t)(base + c) * p.H + h; };
     auto first_row = [&](long long c) { return (int)(r.first + c * C); };
-    chain_init(sm);
+    chain_init(sm.bar);
     if (fetcher && n_chunks > 0) {
         fetch.k(0, first_row(0), index(0));
         fetch.v(first_row(0), !SAVE);
@@ -713,7 +706,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
     const bool fetcher = threadIdx.x == 128;
     auto index = [&](long long c) { return (size_t)(base + c) * p.H + h; };
     auto first_row = [&](long long c) { return (int)(r.first + c * C); };
-    chain_init(sm);
+    chain_init(sm.bar);
     if (fetcher && n_chunks > 0) {
         const long long c = n_chunks - 1;
         fetch.k(0, first_row(c), index(c));
@@ -754,7 +747,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         if (warp == 4) {
             if (fetcher) {
                 for (int x = 0; x < kSlabs; ++x)
-                    for (int e = 0; e < 2; ++e) keep_plane(w.D + idx * 2 * kSlabs * p.dv * 64, p.dv, c0, 2 * x + e, sm.S[x][e]);
+                    for (int e = 0; e < 3; ++e) keep_plane(w.D + idx * 3 * kSlabs * p.dv * 64, p.dv, c0, 3 * x + e, sm.S[x][e]);
                 sm100::bulk_commit();
                 sm100::bulk_wait_read0();  // these, and dR's of the step before
             }
@@ -771,18 +764,6 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             if (fetcher && c > 0) fetch.p(w.Pt + index(c - 1) * 3 * kUnits * 32, first_row(c - 1), true);
             continue;
         }
-        // <D, Sig>, from Sig's terms
-        float all = 0.f;
-        st.each(warp, lane, [&](int n, int col, float &x, float &y) {
-            const char *src = (const char *)(w.Sig + idx * 3 * kSlabs * p.dv * 64) + ((size_t)(col >> 6) * 3 * p.dv + c0 + n) * 128 +
-                              sw_byte(0, 0, col & 56 ^ (n & 7) << 3) + (col & 7) * 2;
-            const uint32_t s0 = *reinterpret_cast<const uint32_t *>(src), s1 = *reinterpret_cast<const uint32_t *>(src + p.dv * 128),
-                           s2 = *reinterpret_cast<const uint32_t *>(src + p.dv * 256);
-            all = fmaf(x, low_of(s0) + (low_of(s1) + low_of(s2)), fmaf(y, high_of(s0) + (high_of(s1) + high_of(s2)), all));
-        });
-#pragma unroll
-        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        if (lane == 0) w.all[(idx * groups + c0 / NV) * 4 + warp] = all;
         // D^T K^T, and dO^T P
         float zh[2][4], zl[2][4], ph[2][4], pl[2][2][4];
         state_times<NF, 3>(zh, zl, aS, sm100::smem_u32(sm.K[b]), t0, t1, lane);
@@ -792,25 +773,16 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
             const float2 el = *reinterpret_cast<const float2 *>(&sm.gates[b][1][tok]);
             const float2 eg = *reinterpret_cast<const float2 *>(&sm.gates[b][0][tok]);
-            float past0 = 0.f, past1 = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int n = lane / 4 + 8 * half, i = 2 * half;
                 const float zx = el.x * (zh[t][i] + zl[t][i]), zy = el.y * (zh[t][i + 1] + zl[t][i + 1]);
-                const char *src = (const char *)(w.U + (idx * 3 * p.dv + c0 + n) * 64) + ((tok / 8 ^ (n & 7)) << 4) + (tok & 7) * 2;
-                const uint32_t u0 = *reinterpret_cast<const uint32_t *>(src), u1 = *reinterpret_cast<const uint32_t *>(src + p.dv * 128),
-                               u2 = *reinterpret_cast<const uint32_t *>(src + p.dv * 256);
-                const float2 u = make_float2(low_of(u0) + (low_of(u1) + low_of(u2)), high_of(u0) + (high_of(u1) + high_of(u2)));
-                past0 = fmaf(u.x, zx, past0);
-                past1 = fmaf(u.y, zy, past1);
+                *reinterpret_cast<float2 *>(w.Z + (idx * p.dv + c0 + n) * C + tok) = make_float2(zx, zy);
                 put_pair<3>(pair_addr(aR, t ? t1 : t0, lane), half, zx + (ph[t][i] + (pl[t][0][i] + pl[t][1][i])),
                             zy + (ph[t][i + 1] + (pl[t][0][i + 1] + pl[t][1][i + 1])));  // dU
                 put_pair<3>(pair_addr(aU, t ? t1 : t0, lane), half, eg.x * __bfloat162float(sm.V[tok][n]),
                             eg.y * __bfloat162float(sm.V[tok + 1][n]));
             }
-            past0 = rows_sum(past0);
-            past1 = rows_sum(past1);
-            if (lane < 4) *reinterpret_cast<float2 *>(w.past + (idx * groups + c0 / NV) * C + tok) = make_float2(past0, past1);
         }
         ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err);
         __syncthreads();
@@ -823,35 +795,21 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             const int tok = 8 * (t ? t1 : t0) + 2 * (lane & 3);
             const float2 eg = *reinterpret_cast<const float2 *>(&sm.gates[b][0][tok]);
             const float2 be = *reinterpret_cast<const float2 *>(&sm.gates[b][2][tok]);
-            float into0 = 0.f, into1 = 0.f, db0 = 0.f, db1 = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int n = lane / 4 + 8 * half, i = 2 * half;
-                const float x = rh[t][i] + (rl[t][0][i] + rl[t][1][i]), y = rh[t][i + 1] + (rl[t][0][i + 1] + rl[t][1][i + 1]);
+                const int i = 2 * half;
+                float x = rh[t][i] + (rl[t][0][i] + rl[t][1][i]), y = rh[t][i + 1] + (rl[t][0][i + 1] + rl[t][1][i + 1]);
                 put_pair<3>(pair_addr(sm100::smem_u32(sm.W), t ? t1 : t0, lane), half, x, y);
-                const float2 X = *reinterpret_cast<const float2 *>(w.X + (idx * p.dv + c0 + n) * C + tok);
-                const bf16 *vp = (const bf16 *)p.v + (row + tok) * p.v_stride + (size_t)h * p.dv + c0 + n;
-                bf16 *dvp = (bf16 *)p.dv_out + ((row + tok) * p.H + h) * p.dv + c0 + n;
-                const float bx = be.x * x, by = be.y * y;
-                into0 = fmaf(-bx, X.x, into0);
-                into1 = fmaf(-by, X.y, into1);
-                if (tok < rows) {
-                    db0 = fmaf(x, __bfloat162float(vp[0]) - X.x, db0);
-                    dvp[0] = __float2bfloat16_rn(bx);
-                }
-                if (tok + 1 < rows) {
-                    db1 = fmaf(y, __bfloat162float(vp[p.v_stride]) - X.y, db1);
-                    dvp[(size_t)p.H * p.dv] = __float2bfloat16_rn(by);
-                }
-                put_pair<3>(pair_addr(aR, t ? t1 : t0, lane), half, -eg.x * bx, -eg.y * by);
-            }
-            into0 = rows_sum(into0);
-            into1 = rows_sum(into1);
-            db0 = rows_sum(db0);
-            db1 = rows_sum(db1);
-            if (lane < 4) {
-                *reinterpret_cast<float2 *>(w.into + (idx * groups + c0 / NV) * C + tok) = make_float2(into0, into1);
-                *reinterpret_cast<float2 *>(w.db + (idx * groups + c0 / NV) * C + tok) = make_float2(db0, db1);
+                x *= be.x;
+                y *= be.y;
+                put_pair<3>(pair_addr(aR, t ? t1 : t0, lane), half, -eg.x * x, -eg.y * y);
+                // dV: as with O, pairs of columns
+                const bool odd = lane & 4;
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 4);
+                const int at = tok + odd, n = (lane / 4 & ~1) + 8 * half;
+                if (at < rows)
+                    *reinterpret_cast<uint32_t *>((bf16 *)p.dv_out + ((row + at) * p.H + h) * p.dv + c0 + n) =
+                        odd ? pack(other, y) : pack(x, other);
             }
         }
         sm100::fence_proxy_async_smem();
@@ -869,6 +827,540 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
     if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
+// ---------------------------------------------------------------- a warp a slice
+// The same walks with a warp for each 16 columns and no exchange between warps: a product's result lies in a lane as
+// the next product's A operand does (rows n, pairs along k), so S, beta Y, U, dU and dR stay in registers from
+// product to product and shared memory holds only what all slices read: K, Q, T, P and v.  A block has up to four
+// slices of one sequence and head; one of its threads fetches.
+constexpr int kSlices = 4;
+constexpr int kWalkThreads = 32 * kSlices;  // eight warps an SM, two blocks, leave a thread its 255 registers
+
+template <int NF, bool BWD> struct WalkSmem {  // 1024-byte aligned
+    static constexpr int kSlabs = (NF + 3) / 4, kTile = kSlabs * C * 64, kTermsP = BWD ? 3 : 2;
+    bf16 K[2][kTile], Q[kTile];
+    bf16 V[C * 64];  // the block's 64 columns of v, or do
+    uint2 T[3][kUnits][32], P[kTermsP][kUnits][32];
+    float gates[2][3][C];
+    uint64_t bar[5];
+};
+
+template <int NF, bool BWD> struct WalkFetch {
+    WalkSmem<NF, BWD> &sm;
+    const ChainMaps &maps;  // v, or do, in boxes of 64 columns
+    const ChunkWork &w;
+    int hk, h, c0;
+    static constexpr uint32_t kTileBytes = WalkSmem<NF, BWD>::kTile * 2;
+    __device__ __forceinline__ void tile(bf16 *dst, const CUtensorMap *map, uint64_t *bar, int row) const {
+#pragma unroll
+        for (int c = 0; c < 16 * NF; c += 64) sm100::tma_load_3d(dst + c * C, map, bar, c, hk, row);
+    }
+    __device__ __forceinline__ void k(int b, int row, size_t idx) const {  // and the gates
+        uint64_t *bar = &sm.bar[kBarK + b];
+        sm100::mbar_arrive_expect_tx(bar, kTileBytes + 3 * C * 4);
+        tile(sm.K[b], &maps.k, bar, row);
+        sm100::bulk_copy_g2s(&sm.gates[b][0][0], w.gates + idx * 3 * C, 3 * C * 4, bar);
+    }
+    __device__ __forceinline__ void t(const uint2 *src) const {
+        sm100::mbar_arrive_expect_tx(&sm.bar[kBarT], sizeof(sm.T));
+        sm100::bulk_copy_g2s(sm.T, src, sizeof(sm.T), &sm.bar[kBarT]);
+    }
+    // forwards (not SAVE): Q and P, read at a step's end.  Backwards Q alone.
+    __device__ __forceinline__ void qp(const uint2 *src, int row) const {
+        sm100::mbar_arrive_expect_tx(&sm.bar[kBarP], kTileBytes + (BWD ? 0 : sizeof(sm.P)));
+        tile(sm.Q, &maps.q, &sm.bar[kBarP], row);
+        if (!BWD) sm100::bulk_copy_g2s(sm.P, src, sizeof(sm.P), &sm.bar[kBarP]);
+    }
+    // v; backwards do and P
+    __device__ __forceinline__ void v(const uint2 *src, int row) const {
+        uint64_t *bar = &sm.bar[kBarV];
+        sm100::mbar_arrive_expect_tx(bar, C * 128 + (BWD ? sizeof(sm.P) : 0));
+        sm100::tma_load_3d(sm.V, &maps.v, bar, c0, h, row);
+        if (BWD) sm100::bulk_copy_g2s(sm.P, src, sizeof(sm.P), bar);
+    }
+};
+
+// Two tiles of a result (16 columns along k) as an A operand's terms.
+template <int N> __device__ __forceinline__ void as_operand(uint32_t (&a)[N][4], const float (&x)[4], const float (&y)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float *s = (e & 2) ? y : x;
+        uint32_t t[N];
+        split(s[2 * (e & 1)], s[2 * (e & 1) + 1], t);
+#pragma unroll
+        for (int n = 0; n < N; ++n) a[n][e] = t[n];
+    }
+}
+
+// hi (+ lo) = S rows^T, all eight token tiles; TERMS terms of S.  MERGE: one sum (what only reaches a bf16 output).
+template <int NF, int TERMS, bool MERGE>
+__device__ __forceinline__ void walk_state_times(float (&hi)[8][4], float (&lo)[MERGE ? 1 : 8][4], const float (&S)[2 * NF][4], uint32_t rows,
+                                                 const uint32_t (&bl)[4]) {
+#pragma unroll
+    for (int ks = 0; ks < NF; ++ks) {
+        uint32_t a[TERMS][4];
+        as_operand<TERMS>(a, S[2 * ks], S[2 * ks + 1]);
+#pragma unroll
+        for (int t = 0; t < 8; t += 4) {
+            uint32_t b[2][4];
+            ldsm4(b[0], rows + bl[ks & 3] + (ks >> 2) * C * 128 + t * 1024);
+            ldsm4(b[1], rows + bl[ks & 3] + (ks >> 2) * C * 128 + t * 1024 + 2048);
+#pragma unroll
+            for (int n = TERMS - 1; n >= 0; --n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float(&d)[4] = MERGE || n == 0 ? hi[t + i] : lo[MERGE ? 0 : t + i];
+                    const bool first = ks == 0 && (MERGE ? n == TERMS - 1 : n == 0 || n == TERMS - 1);
+                    mma::mma(d, a[n], b[i / 2][2 * (i & 1)], b[i / 2][2 * (i & 1) + 1], first);
+                }
+        }
+    }
+}
+
+// hi, lo += a T for the 16-token block kb of the rows: the units of the tiles that hold it.  MERGE as above.
+template <bool LOW, int AT, int BT, bool MERGE>
+__device__ __forceinline__ void walk_triangle(float (&hi)[8][4], float (&lo)[MERGE ? 1 : 8][4], const uint32_t (&a)[AT][4], uint32_t tri, int kb) {
+#pragma unroll
+    for (int t2 = 0; t2 < 8; t2 += 2) {
+        if (LOW ? t2 / 2 < kb : t2 / 2 > kb) continue;
+        uint2 f[2][BT];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < BT; ++e) f[i][e] = lds2(tri + (e * kUnits + (LOW ? low_unit(t2 + i) + kb : up_unit(t2 + i) + kb - t2 / 2)) * 256);
+#pragma unroll
+        for (int k = (AT > BT ? AT : BT) - 1; k >= 0; --k)
+#pragma unroll
+            for (int x = 0; x < AT; ++x) {
+                const int y = k - x;
+                if (y < 0 || y >= BT) continue;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mma::mma(MERGE || k == 0 ? hi[t2 + i] : lo[MERGE ? 0 : t2 + i], a[x], f[i][y].x, f[i][y].y);
+            }
+    }
+}
+
+// S += a rows, a: four 16-token blocks' terms, rows [64 tokens][dk].
+template <int NF>
+__device__ __forceinline__ void walk_update(float (&S)[2 * NF][4], const uint32_t (&a)[4][3][4], uint32_t rows, int lane) {
+#pragma unroll
+    for (int g = 0; g < NF; ++g) {
+        float hi[2][4], lo[2][4];
+        const uint32_t at = rows + bt_lane(C, 16 * g, lane);
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+            uint32_t b[4];
+            ldsm4_t(b, at + kb * 2048);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma::mma(lo[t], a[kb][2], b[2 * t], b[2 * t + 1], kb == 0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma::mma(hi[t], a[kb][0], b[2 * t], b[2 * t + 1], kb == 0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) mma::mma(lo[t], a[kb][1], b[2 * t], b[2 * t + 1]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[2 * g + t][e] += hi[t][e] + lo[t][e];
+    }
+}
+
+// A warp's columns of v or do [64 tokens][64]: x[t][half] is a pair of tokens of tile t, row n or n + 8.
+__device__ __forceinline__ void walk_columns(uint32_t (&x)[8][2], uint32_t tile, int slice, int lane) {
+    // blocks (tile t, n 0-7), (t, n 8-15), (t + 1, n 0-7), (t + 1, n 8-15)
+    const uint32_t at = tile + ((lane >> 4) * 8 + (lane & 7)) * 128 + (((2 * slice + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) {
+        uint32_t r[4];
+        ldsm4_t(r, at + t * 1024);
+        x[t][0] = r[0];
+        x[t][1] = r[1];
+        x[t + 1][0] = r[2];
+        x[t + 1][1] = r[3];
+    }
+}
+
+// bf16 rows of [tokens][H][dv] from x[t]: lanes of neighbouring rows swap, so that each writes a pair of columns.
+__device__ __forceinline__ void walk_store(bf16 *dst, long long row_elems, const float (&x)[8][4], int rows, int lane) {
+    const bool odd = lane & 4;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float mine = odd ? x[t][2 * half + 1] : x[t][2 * half];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? x[t][2 * half] : x[t][2 * half + 1], 4);
+            const int i = 8 * t + 2 * (lane & 3) + odd, n = (lane / 4 & ~1) + 8 * half;
+            if (i < rows) *reinterpret_cast<uint32_t *>(dst + i * row_elems + n) = odd ? pack(other, mine) : pack(mine, other);
+        }
+}
+
+// A pair's terms into lines [dv][64] at (line, column pair): dst is the first term's line 0.
+template <int N> __device__ __forceinline__ void keep_pair(bf16 *dst, int dv, int line, int col, float x, float y) {
+    uint32_t t[N];
+    split(x, y, t);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        *reinterpret_cast<uint32_t *>((char *)dst + ((size_t)e * dv + line) * 128 + (((col >> 3 & 7) ^ (line & 7)) << 4) + (col & 7) * 2) = t[e];
+}
+// Which slice a thread's warp walks.
+struct WalkPlace {
+    int s, h, hk, c0, slice, slices;  // c0: the block's first column; slices: how many the block has
+};
+__device__ __forceinline__ WalkPlace walk_place(const SeqProblem &p) {
+    const int groups = (p.dv + 16 * kSlices - 1) / (16 * kSlices);
+    WalkPlace x;
+    x.s = blockIdx.x / (p.H * groups);
+    x.h = blockIdx.x / groups % p.H;
+    x.hk = x.h / (p.H / p.Hk);
+    x.c0 = blockIdx.x % groups * 16 * kSlices;
+    x.slice = warp_number();
+    x.slices = min(kSlices, (p.dv - x.c0) / 16);
+    return x;
+}
+template <typename Smem> __device__ __forceinline__ void walk_leave(Smem &sm, const SeqProblem &p, const int (&last)[5], int *err) {
+    for (int i = 0; i < 5; ++i)  // the last fetch of each barrier, if it had one
+        if (last[i] >= 0) sm100::mbar_wait(&sm.bar[i], last[i] & 1, err, sm100::kWaitLimitNs, true);
+    if (p.status && threadIdx.x == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
+}
+
+template <int NF, bool SAVE>
+__global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
+                                                              const __grid_constant__ ChainMaps maps) {
+    constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4;
+    extern __shared__ unsigned char raw[];
+    auto &sm = *reinterpret_cast<WalkSmem<NF, false> *>(raw + (-sm100::smem_u32(raw) & 1023));
+    const WalkPlace at = walk_place(p);
+    const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
+    const SeqRange r = seq_range(p, at.s);
+    seq_report(p, r, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
+    if (r.slot < 0) return;
+    const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, at.s, r.first);
+    const WalkFetch<NF, false> fetch = {sm, maps, w, at.hk, at.h, at.c0};
+    const bool fetcher = threadIdx.x == 0, walks = at.slice < at.slices;
+    auto index = [&](long long c) { return (size_t)(base + c) * p.H + at.h; };
+    auto first_row = [&](long long c) { return (int)(r.first + c * C); };
+    chain_init(sm.bar);
+    if (fetcher && n_chunks > 0) {
+        fetch.k(0, first_row(0), index(0));
+        fetch.v(nullptr, first_row(0));
+        fetch.t(w.T + index(0) * 3 * kUnits * 32);
+        if (!SAVE) fetch.qp(w.P + index(0) * 2 * kUnits * 32, first_row(0));
+    }
+    float S[2 * NF][4] = {};
+    float *const s_out = p.S_out + (((size_t)r.slot * p.H + at.h) * p.dv + col + n0) * DK + j0;
+    if (walks && !seq_starts_zero(p, at.s)) {
+        const float *s_in = p.S_in + (((size_t)r.slot * p.H + at.h) * p.dv + col + n0) * DK + j0;
+#pragma unroll
+        for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float2 x = *reinterpret_cast<const float2 *>(s_in + half * 8 * DK + 8 * t);
+                S[t][2 * half] = x.x;
+                S[t][2 * half + 1] = x.y;
+            }
+    }
+    uint32_t bl[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) bl[x] = b_lane(0, 8, x, lane);
+    const uint32_t aT = sm100::smem_u32(sm.T) + lane * 8, aP = sm100::smem_u32(sm.P) + lane * 8;
+    bool ok = true;
+#pragma unroll 1
+    for (long long c = 0; c < n_chunks; ++c) {
+        const int b = (int)(c & 1);
+        const uint32_t parity = (uint32_t)c & 1;
+        const size_t idx = index(c);
+        const long long row = r.first + c * C;
+        const int rows = (int)min((long long)C, r.len - c * C);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) &&
+             sm100::mbar_wait(&sm.bar[kBarT], parity, w.err) && (SAVE || sm100::mbar_wait(&sm.bar[kBarP], parity, w.err));
+        if (!__syncthreads_and(ok)) {
+            const int last[5] = {(int)((c + (c & 1)) >> 1), c ? (int)((c - !(c & 1)) >> 1) : -1, (int)c, (int)c, SAVE ? -1 : (int)c};
+            return walk_leave(sm, p, last, w.err);
+        }
+        if (fetcher && c + 1 < n_chunks) fetch.k(b ^ 1, first_row(c + 1), index(c + 1));
+        if (rows < C) {
+            zero_tail(sm.K[b], kSlabs, 8, rows);
+            if (!SAVE) zero_tail(sm.Q, kSlabs, 8, rows);
+            zero_tail(sm.V, 1, 8, rows);
+            __syncthreads();
+        }
+        if (!walks) {  // it keeps the barriers' count
+            __syncthreads();
+            __syncthreads();
+            continue;
+        }
+        const uint32_t aK = sm100::smem_u32(sm.K[b]);
+        const float *eg = sm.gates[b][0] + j0, *el = sm.gates[b][1] + j0, *be = sm.gates[b][2] + j0;
+        if (SAVE) {
+#pragma unroll
+            for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    keep_pair<3>(w.Sig + (idx * kSlabs + t / 8) * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * (t & 7) + j0, S[t][2 * half],
+                                 S[t][2 * half + 1]);
+        }
+        float R[8][4];
+        {
+            float lo[8][4];
+            uint32_t v[8][2];
+            walk_state_times<NF, 3, false>(R, lo, S, aK, bl);
+            walk_columns(v, sm100::smem_u32(sm.V), at.slice, lane);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 g = *reinterpret_cast<const float2 *>(eg + 8 * t), h = *reinterpret_cast<const float2 *>(be + 8 * t);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float x = g.x * (R[t][2 * half] + lo[t][2 * half]), y = g.y * (R[t][2 * half + 1] + lo[t][2 * half + 1]);
+                    if (SAVE) *reinterpret_cast<float2 *>(w.X + (idx * p.dv + col + n0 + 8 * half) * C + 8 * t + j0) = make_float2(x, y);
+                    R[t][2 * half] = h.x * (low_of(v[t][half]) - x);
+                    R[t][2 * half + 1] = h.y * (high_of(v[t][half]) - y);
+                }
+            }
+        }
+        float U[8][4];
+        {
+            float lo[8][4];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) U[t][e] = lo[t][e] = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                uint32_t a[3][4];
+                as_operand<3>(a, R[2 * kb], R[2 * kb + 1]);
+                walk_triangle<true, 3, 3, false>(U, lo, a, aT, kb);
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) U[t][e] += lo[t][e];
+        }
+        __syncthreads();  // v and T have been read
+        if (fetcher && c + 1 < n_chunks) {
+            fetch.v(nullptr, first_row(c + 1));
+            fetch.t(w.T + index(c + 1) * 3 * kUnits * 32);
+        }
+        if (SAVE) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    keep_pair<3>(w.U + idx * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * t + j0, U[t][2 * half], U[t][2 * half + 1]);
+        } else {
+            float O[8][4], none[1][4];
+            walk_state_times<NF, 2, true>(O, none, S, sm100::smem_u32(sm.Q), bl);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 g = *reinterpret_cast<const float2 *>(eg + 8 * t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) O[t][e] *= e & 1 ? g.y : g.x;
+            }
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                uint32_t a[2][4];
+                as_operand<2>(a, U[2 * kb], U[2 * kb + 1]);
+                walk_triangle<true, 2, 2, true>(O, none, a, aP, kb);
+            }
+            walk_store((bf16 *)p.o + (row * p.H + at.h) * p.dv + col, (long long)p.H * p.dv, O, rows, lane);
+        }
+        __syncthreads();  // Q and P have been read
+        if (!SAVE && fetcher && c + 1 < n_chunks) fetch.qp(w.P + index(c + 1) * 2 * kUnits * 32, first_row(c + 1));
+        uint32_t a[4][3][4];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const float2 g = *reinterpret_cast<const float2 *>(el + 8 * t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) U[t][e] *= e & 1 ? g.y : g.x;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) as_operand<3>(a[kb], U[2 * kb], U[2 * kb + 1]);
+        const float decay = sm.gates[b][0][C - 1];
+#pragma unroll
+        for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][e] *= decay;
+        walk_update<NF>(S, a, aK, lane);
+    }
+    if (!SAVE && p.S_out && walks) {
+#pragma unroll
+        for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                *reinterpret_cast<float2 *>(s_out + half * 8 * DK + 8 * t) = make_float2(S[t][2 * half], S[t][2 * half + 1]);
+    }
+}
+
+template <int NF>
+__global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
+                                                              const __grid_constant__ ChainMaps maps) {
+    constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4;
+    extern __shared__ unsigned char raw[];
+    auto &sm = *reinterpret_cast<WalkSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
+    const WalkPlace at = walk_place(p);
+    const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice, groups = p.dv / NV;
+    const SeqRange r = seq_rows(p, at.s);
+    const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, at.s, r.first);  // 0 of a bad range
+    const WalkFetch<NF, true> fetch = {sm, maps, w, at.hk, at.h, at.c0};
+    const bool fetcher = threadIdx.x == 0, walks = at.slice < at.slices;
+    auto index = [&](long long c) { return (size_t)(base + c) * p.H + at.h; };
+    auto first_row = [&](long long c) { return (int)(r.first + c * C); };
+    chain_init(sm.bar);
+    if (fetcher && n_chunks > 0) {
+        const long long c = n_chunks - 1;
+        fetch.k(0, first_row(c), index(c));
+        fetch.v(w.Pt + index(c) * 3 * kUnits * 32, first_row(c));
+        fetch.t(w.Tt + index(c) * 3 * kUnits * 32);
+        fetch.qp(nullptr, first_row(c));
+    }
+    float D[2 * NF][4] = {};
+    const size_t soff = (((size_t)at.s * p.H + at.h) * p.dv + col + n0) * DK + j0;
+    if (walks && r.slot >= 0 && p.dS_out) {
+#pragma unroll
+        for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float2 x = *reinterpret_cast<const float2 *>(p.dS_out + soff + half * 8 * DK + 8 * t);
+                D[t][2 * half] = x.x;
+                D[t][2 * half + 1] = x.y;
+            }
+    }
+    uint32_t bl[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) bl[x] = b_lane(0, 8, x, lane);
+    const uint32_t aT = sm100::smem_u32(sm.T) + lane * 8, aP = sm100::smem_u32(sm.P) + lane * 8;
+    bool ok = true;
+#pragma unroll 1
+    for (long long turn = 0; turn < n_chunks; ++turn) {
+        const long long c = n_chunks - 1 - turn;
+        const int b = (int)(turn & 1);
+        const uint32_t parity = (uint32_t)turn & 1;
+        const size_t idx = index(c);
+        const long long row = r.first + c * C;
+        const int rows = (int)min((long long)C, r.len - c * C);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) &&
+             sm100::mbar_wait(&sm.bar[kBarT], parity, w.err) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
+        if (!__syncthreads_and(ok)) {
+            const int i = (int)turn, last[5] = {(i + (i & 1)) >> 1, i ? (i - !(i & 1)) >> 1 : -1, i, i, i};
+            return walk_leave(sm, p, last, w.err);
+        }
+        if (fetcher && c > 0) fetch.k(b ^ 1, first_row(c - 1), index(c - 1));
+        if (rows < C) {
+            zero_tail(sm.K[b], kSlabs, 8, rows);
+            zero_tail(sm.Q, kSlabs, 8, rows);
+            zero_tail(sm.V, 1, 8, rows);
+            __syncthreads();
+        }
+        if (!walks) {
+            __syncthreads();
+            __syncthreads();
+            continue;
+        }
+        const uint32_t aK = sm100::smem_u32(sm.K[b]), aO = sm100::smem_u32(sm.V);
+        const float *eg = sm.gates[b][0] + j0, *el = sm.gates[b][1] + j0, *be = sm.gates[b][2] + j0;
+#pragma unroll
+        for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                keep_pair<3>(w.D + (idx * kSlabs + t / 8) * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * (t & 7) + j0, D[t][2 * half],
+                             D[t][2 * half + 1]);
+        float X[8][4];  // dU, then dR
+        {
+            float Z[8][4], lo[8][4];
+            walk_state_times<NF, 3, false>(Z, lo, D, aK, bl);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 l = *reinterpret_cast<const float2 *>(el + 8 * t);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    Z[t][2 * half] = l.x * (Z[t][2 * half] + lo[t][2 * half]);
+                    Z[t][2 * half + 1] = l.y * (Z[t][2 * half + 1] + lo[t][2 * half + 1]);
+                    *reinterpret_cast<float2 *>(w.Z + (idx * p.dv + col + n0 + 8 * half) * C + 8 * t + j0) =
+                        make_float2(Z[t][2 * half], Z[t][2 * half + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[t][e] = lo[t][e] = 0.f;
+            }
+            const uint32_t o_at = aO + ((lane >> 4) * 8 + (lane & 7)) * 128 + (((2 * at.slice + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                uint32_t a[1][4];
+                ldsm4_t(a[0], o_at + kb * 2048);
+                walk_triangle<false, 1, 3, false>(X, lo, a, aP, kb);
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Z[t][e] += X[t][e] + lo[t][e], X[t][e] = lo[t][e] = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                uint32_t a[3][4];
+                as_operand<3>(a, Z[2 * kb], Z[2 * kb + 1]);
+                walk_triangle<false, 3, 3, false>(X, lo, a, aT, kb);
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[t][e] += lo[t][e];
+        }
+        __syncthreads();  // T has been read
+        if (fetcher && c > 0) fetch.t(w.Tt + index(c - 1) * 3 * kUnits * 32);
+        uint32_t a[4][3][4];
+        {  // (e^G dO)^T Q
+            uint32_t v[8][2];
+            walk_columns(v, aO, at.slice, lane);
+            float x[8][4];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const float2 g = *reinterpret_cast<const float2 *>(eg + 8 * t);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    x[t][2 * half] = g.x * low_of(v[t][half]);
+                    x[t][2 * half + 1] = g.y * high_of(v[t][half]);
+                }
+            }
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) as_operand<3>(a[kb], x[2 * kb], x[2 * kb + 1]);
+            const float decay = sm.gates[b][0][C - 1];
+#pragma unroll
+            for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) D[t][e] *= decay;
+            walk_update<NF>(D, a, sm100::smem_u32(sm.Q), lane);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const float2 h = *reinterpret_cast<const float2 *>(be + 8 * t);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                keep_pair<3>(w.dR + idx * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * t + j0, X[t][2 * half], X[t][2 * half + 1]);
+                X[t][2 * half] *= h.x;
+                X[t][2 * half + 1] *= h.y;
+            }
+        }
+        __syncthreads();  // do, P and Q have been read
+        if (fetcher && c > 0) {
+            fetch.v(w.Pt + index(c - 1) * 3 * kUnits * 32, first_row(c - 1));
+            fetch.qp(nullptr, first_row(c - 1));
+        }
+        walk_store((bf16 *)p.dv_out + (row * p.H + at.h) * p.dv + col, (long long)p.H * p.dv, X, rows, lane);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const float2 g = *reinterpret_cast<const float2 *>(eg + 8 * t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[t][e] *= e & 1 ? -g.y : -g.x;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) as_operand<3>(a[kb], X[2 * kb], X[2 * kb + 1]);
+        walk_update<NF>(D, a, aK, lane);
+    }
+    if (p.dS_in && walks) {
+#pragma unroll
+        for (int t = 0; t < 2 * NF; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                *reinterpret_cast<float2 *>(p.dS_in + soff + half * 8 * DK + 8 * t) = make_float2(D[t][2 * half], D[t][2 * half + 1]);
+    }
+}
+
 // The gradients of a chunk and head from what the chains left: 8 warps, warp w has the 16 tokens from 16 (w % 4).
 // Warps 0-3 (role 0) make dQ, warps 4-7 dK, first the parts inside the chunk, then those through the states:
 //   dQ = dP K + e^G dO Sig^T,  dK = (beta dA) K + [dP; beta dA]^T [Q; K] - beta e^G dR Sig^T + e^{G_L-G} U D^T
@@ -876,10 +1368,10 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
 // reach the bf16 dQ and dK take two terms of each operand.  The matrices come as the terms that the chains had at
 // hand (converting fp32 here took more instructions than the products: 755 us against NNN).
 struct GradMaps {
-    CUtensorMap q, k, o;
+    CUtensorMap q, k, v, o;
 };
-// Shared memory, sizes from dv: K, Q, dO rows | U, dR first two terms | U, dR third terms, dP and beta dA, M; in the
-// place of the last, when they have been read, 64 columns of Sig and D.
+// Shared memory, sizes from dv: K, Q, dO rows | U, dR first two terms | U, dR third terms, dP and beta dA (before them
+// v's rows), M; in the place of the last, when they have been read, 64 columns of Sig and D.
 template <int NF> struct GradLayout {
     static constexpr int kSlabs = (NF + 3) / 4, kTile = kSlabs * C * 128, kT = C * (16 * NF + 4) * 4, kPA = kT > 32768 ? kT : 32768;
     int plane, K, Q, O, UR, last, PA, M, total;
@@ -901,7 +1393,8 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                                                         const __grid_constant__ GradMaps maps) {
     constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4, PM = C + 1;
     extern __shared__ unsigned char raw[];
-    __shared__ float gates[3][C], into[C], past[C], db[C], sums[4][C], dg[C];
+    __shared__ __align__(16) float gates[3][C], part_sums[8][3][C];  // read and written in pairs
+    __shared__ float into[C], past[C], db[C], sums[4][C], dg[C], red[8];
     __shared__ uint64_t bar[2];
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
@@ -920,29 +1413,19 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     __syncthreads();
     const bf16 *Um = w.U + idx * 3 * dv * 64, *Rm = w.dR + idx * 3 * dv * 64;
     if (tid == 0) {
-        sm100::mbar_arrive_expect_tx(&bar[0], 2 * at.kTile + (dv + 63) / 64 * C * 128 + 6 * plane);
+        sm100::mbar_arrive_expect_tx(&bar[0], 2 * at.kTile + (dv + 63) / 64 * 2 * C * 128 + 6 * plane);
         for (int x = 0; x < kSlabs; ++x) {
             sm100::tma_load_3d(sm + at.K + x * C * 128, &maps.k, &bar[0], 64 * x, hk, (int)ch.first);
             sm100::tma_load_3d(sm + at.Q + x * C * 128, &maps.q, &bar[0], 64 * x, hk, (int)ch.first);
         }
         for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.O + x * C * 128, &maps.o, &bar[0], 64 * x, h, (int)ch.first);
+        for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.PA + x * C * 128, &maps.v, &bar[0], 64 * x, h, (int)ch.first);
         sm100::bulk_copy_g2s(sm + at.UR, Um, 2 * plane, &bar[0]);
         sm100::bulk_copy_g2s(sm + at.UR + 2 * plane, Rm, 2 * plane, &bar[0]);
         sm100::bulk_copy_g2s(sm + at.last, Um + 2 * dv * 64, plane, &bar[0]);
         sm100::bulk_copy_g2s(sm + at.last + plane, Rm + 2 * dv * 64, plane, &bar[0]);
     }
     if (tid < 3 * C) gates[0][tid] = w.gates[idx * 3 * C + tid];
-    if (tid < C) {
-        float x = 0.f, y = 0.f, z = 0.f;  // the slices' parts, in order
-        for (int g = 0; g < nvf; ++g) {
-            x += w.past[(idx * nvf + g) * C + tid];
-            y += w.into[(idx * nvf + g) * C + tid];
-            z += w.db[(idx * nvf + g) * C + tid];
-        }
-        past[tid] = x;
-        into[tid] = y;
-        db[tid] = z;
-    }
     const int i0 = 16 * mt + lane / 4, j0 = 2 * (lane & 3);  // this lane's rows i0, i0 + 8; its columns 8 t + j0, + 1
     if (!__syncthreads_and(sm100::mbar_wait(&bar[0], 0, w.err))) {
         sm100::mbar_wait(&bar[0], 0, w.err, sm100::kWaitLimitNs, true);
@@ -953,7 +1436,43 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         zero_tail((bf16 *)(sm + at.K), kSlabs, 8, ch.rows);
         zero_tail((bf16 *)(sm + at.Q), kSlabs, 8, ch.rows);
         zero_tail((bf16 *)(sm + at.O), (dv + 63) / 64, 8, ch.rows);
+        zero_tail((bf16 *)(sm + at.PA), (dv + 63) / 64, 8, ch.rows);
         __syncthreads();
+    }
+    {  // sums over dv: past = U . Z, into = -beta dR . X (k's part), db = dR . (V - X).  A pair of tokens a lane, dv over the warps
+        const float *X = w.X + idx * dv * C + 2 * lane, *Z = w.Z + idx * dv * C + 2 * lane;
+        const float2 be = *reinterpret_cast<const float2 *>(&gates[2][2 * lane]);
+        float s[3][2] = {};
+#pragma unroll 4
+        for (int n = warp; n < dv; n += 8) {
+            const float2 x = *reinterpret_cast<const float2 *>(X + n * C), z = *reinterpret_cast<const float2 *>(Z + n * C);
+            const int line = n * 128 + ((lane >> 2 ^ (n & 7)) << 4) + (lane & 3) * 4;
+            auto sum3 = [&](int first, int third) {
+                const uint32_t a = *reinterpret_cast<const uint32_t *>(sm + first + line), b = *reinterpret_cast<const uint32_t *>(sm + first + plane + line),
+                               c = *reinterpret_cast<const uint32_t *>(sm + third + line);
+                return make_float2(low_of(a) + (low_of(b) + low_of(c)), high_of(a) + (high_of(b) + high_of(c)));
+            };
+            const float2 u = sum3(at.UR, at.last), r = sum3(at.UR + 2 * plane, at.last + plane);
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                v[e] = __bfloat162float(*reinterpret_cast<const bf16 *>(sm + at.PA + sw_byte(C, 2 * lane + e, n) + (n & 7) * 2));
+            s[0][0] = fmaf(u.x, z.x, s[0][0]);
+            s[0][1] = fmaf(u.y, z.y, s[0][1]);
+            s[1][0] = fmaf(-be.x * r.x, x.x, s[1][0]);
+            s[1][1] = fmaf(-be.y * r.y, x.y, s[1][1]);
+            s[2][0] = fmaf(r.x, v[0] - x.x, s[2][0]);
+            s[2][1] = fmaf(r.y, v[1] - x.y, s[2][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<float2 *>(&part_sums[warp][i][2 * lane]) = make_float2(s[i][0], s[i][1]);
+        __syncthreads();  // and v has been read
+        if (tid < 3 * C) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x += part_sums[i][tid / C][tid % C];
+            (tid < C ? past : tid < 2 * C ? into : db)[tid % C] = x;
+        }
     }
     const uint32_t aK = base + at.K, aQ = base + at.Q, aO = base + at.O;
     // lane parts: an A operand from token rows; from [dv][64 tokens] lines; two n-tiles of a B operand from 64-column lines
@@ -1184,7 +1703,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         __syncthreads();  // all that the state's columns take the place of has been read
     }
     // ---- through the states
-    float part[2] = {};
+    float part[2] = {}, all = 0.f;
 #pragma unroll
     for (int slab = 0; slab < kSlabs; ++slab) {
         constexpr int kLast = NF % 4 ? NF % 4 : 4;
@@ -1193,12 +1712,30 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         if (tid == 0) {
             sm100::mbar_arrive_expect_tx(&bar[1], 5 * plane);
             sm100::bulk_copy_g2s(sm + at.last, w.Sig + (idx * kSlabs + slab) * 3 * dv * 64, 3 * plane, &bar[1]);
-            sm100::bulk_copy_g2s(sm + at.last + 3 * plane, w.D + (idx * kSlabs + slab) * 2 * dv * 64, 2 * plane, &bar[1]);
+            sm100::bulk_copy_g2s(sm + at.last + 3 * plane, w.D + (idx * kSlabs + slab) * 3 * dv * 64, 2 * plane, &bar[1]);
         }
         if (!__syncthreads_and(sm100::mbar_wait(&bar[1], slab, w.err))) {
             sm100::mbar_wait(&bar[1], slab, w.err, sm100::kWaitLimitNs, true);
             if (p.status && tid == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
             return;
+        }
+        {  // <D, Sig> over the slab; D's third term from memory
+            const bf16 *third = w.D + ((idx * kSlabs + slab) * 3 + 2) * dv * 64;
+            const int pieces = 4 * groups;  // of 8 bytes a line
+#pragma unroll 4
+            for (int i = tid; i < dv * pieces; i += 256) {
+                const int n = i / pieces, c4 = i % pieces, line = n * 128 + ((c4 >> 1 ^ (n & 7)) << 4) + (c4 & 1) * 8;
+                const uint2 d2 = *reinterpret_cast<const uint2 *>((const char *)third + line);
+                uint2 m[5];
+#pragma unroll
+                for (int x = 0; x < 5; ++x) m[x] = *reinterpret_cast<const uint2 *>(sm + at.last + x * plane + line);
+                auto dot = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f) {
+                    all = fmaf(low_of(a) + (low_of(b) + low_of(c)), low_of(d) + (low_of(e) + low_of(f)), all);
+                    all = fmaf(high_of(a) + (high_of(b) + high_of(c)), high_of(d) + (high_of(e) + high_of(f)), all);
+                };
+                dot(m[0].x, m[1].x, m[2].x, m[3].x, m[4].x, d2.x);
+                dot(m[0].y, m[1].y, m[2].y, m[3].y, m[4].y, d2.y);
+            }
         }
         const uint32_t s0 = base + at.last, u01 = base + at.UR;
         float x[8][4], y[8][4];  // role 0: leading and small products; role 1: dR Sig^T and U D^T
@@ -1273,6 +1810,9 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         }
         __syncthreads();
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) red[warp] = all;
     if (role == 0)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -1295,15 +1835,32 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         }
     }
     __syncthreads();
-    if (tid < ch.rows) {
-        float g = 0.f;
-        for (int i = 0; i < 4 * nvf; ++i) g += w.all[idx * 4 * nvf + i];
-        g = fmaf(g, gates[0][C - 1], dg[tid]);
-        for (int j = 0; j < tid; ++j) g += past[j];
-        for (int i = tid; i < C; ++i) g += into[i];
-        const size_t to = (size_t)(ch.first + tid) * p.H + h;
-        p.dalpha[to] = g / fmaxf(p.alpha[to], expf(kSeqBwdLogFloor));
-        p.dbeta[to] = db[tid];
+    if (warp < 2) {  // token tid: the terms from before the chunk to it or later ones, those from earlier ones past its end
+        float in = into[tid], out = tid ? past[tid - 1] : 0.f, g = 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_down_sync(0xffffffffu, in, o), y = __shfl_up_sync(0xffffffffu, out, o);
+            in += lane + o < 32 ? x : 0.f;
+            out += lane >= o ? y : 0.f;
+        }
+        if (warp == 0) {
+            float later = into[32 + lane];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) later += __shfl_xor_sync(0xffffffffu, later, o);
+            in += later;
+        } else {
+            float before = lane < 31 ? past[lane] : 0.f;  // past[31] is in `out` already
+#pragma unroll
+            for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+            out += before;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g += red[i];
+        if (tid < ch.rows) {
+            const size_t to = (size_t)(ch.first + tid) * p.H + h;
+            p.dalpha[to] = (fmaf(g, gates[0][C - 1], dg[tid]) + (in + out)) / fmaxf(p.alpha[to], expf(kSeqBwdLogFloor));
+            p.dbeta[to] = db[tid];
+        }
     }
 }
 
@@ -1321,29 +1878,59 @@ template <typename K, int NF, bool BWD> cudaError_t chain(K kernel, int threads,
     return cudaGetLastError();
 }
 
-bool make_maps(ChainMaps &m, const SeqProblem &p, const void *v, long long v_stride) {
+bool make_maps(ChainMaps &m, const SeqProblem &p, const void *v, long long v_stride, int v_cols) {
     return seq_row_map(&m.q, p.q, p.n_tokens, p.q_stride, p.Hk, p.dk, 64) &&
            seq_row_map(&m.k, p.k, p.n_tokens, p.k_stride, p.Hk, p.dk, 64) &&
-           seq_row_map(&m.v, v, p.n_tokens, v_stride, p.H, p.dv, NV);
+           seq_row_map(&m.v, v, p.n_tokens, v_stride, p.H, p.dv, v_cols);
+}
+
+bool walk(const SeqProblem &p) { return getenv("GDN_COOP") == nullptr; }
+unsigned walk_blocks(const SeqProblem &p) {
+    return (unsigned)((long long)p.n_seqs * p.H * ((p.dv + 16 * kSlices - 1) / (16 * kSlices)));
+}
+
+template <int NF, bool SAVE> cudaError_t walk_fwd(const SeqProblem &p, const ChunkWork &w, const ChainMaps &m, cudaStream_t s) {
+    const int bytes = (int)sizeof(WalkSmem<NF, false>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_walk_fwd<NF, SAVE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e) return e;
+    k_walk_fwd<NF, SAVE><<<walk_blocks(p), kWalkThreads, bytes, s>>>(p, w, m);
+    return cudaGetLastError();
 }
 
 template <int NF> cudaError_t fwd(const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
     ChainMaps m;
-    if (!make_maps(m, p, p.v, p.v_stride)) return cudaErrorInvalidValue;
+    if (walk(p)) {
+        if (!make_maps(m, p, p.v, p.v_stride, 64)) return cudaErrorInvalidValue;
+        cudaError_t e = prep<NF>(p, w, kLogAlphaFloor, s);
+        return e ? e : walk_fwd<NF, false>(p, w, m, s);
+    }
+    if (!make_maps(m, p, p.v, p.v_stride, NV)) return cudaErrorInvalidValue;
     cudaError_t e = prep<NF>(p, w, kLogAlphaFloor, s);
     return e ? e : chain<decltype(&k_chunk_fwd<NF, false>), NF, false>(k_chunk_fwd<NF, false>, chain_threads(true), p, w, m, s);
 }
 
 template <int NF> cudaError_t bwd(const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
+    const int cols = walk(p) ? 64 : NV;
     ChainMaps m, mo;
-    if (!make_maps(m, p, p.v, p.v_stride) || !make_maps(mo, p, p.d_o, (long long)p.H * p.dv)) return cudaErrorInvalidValue;
+    if (!make_maps(m, p, p.v, p.v_stride, cols) || !make_maps(mo, p, p.d_o, (long long)p.H * p.dv, cols)) return cudaErrorInvalidValue;
     cudaError_t e = prep<NF>(p, w, kSeqBwdLogFloor, s);
-    if (!e) e = chain<decltype(&k_chunk_fwd<NF, true>), NF, false>(k_chunk_fwd<NF, true>, chain_threads(false), p, w, m, s);
-    if (!e) e = chain<decltype(&k_chunk_bwd<NF>), NF, true>(k_chunk_bwd<NF>, chain_threads(false), p, w, mo, s);
+    if (walk(p)) {
+        if (!e) e = walk_fwd<NF, true>(p, w, m, s);
+        const int bytes = (int)sizeof(WalkSmem<NF, true>) + 1024;
+        if (!e) e = cudaFuncSetAttribute(k_walk_bwd<NF>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e) return e;
+        k_walk_bwd<NF><<<walk_blocks(p), kWalkThreads, bytes, s>>>(p, w, mo);
+        e = cudaGetLastError();
+    } else {
+        if (!e) e = chain<decltype(&k_chunk_fwd<NF, true>), NF, false>(k_chunk_fwd<NF, true>, chain_threads(false), p, w, m, s);
+        if (!e) e = chain<decltype(&k_chunk_bwd<NF>), NF, true>(k_chunk_bwd<NF>, chain_threads(false), p, w, mo, s);
+    }
     GradMaps g;
     g.q = m.q;
     g.k = m.k;
-    if (!seq_row_map(&g.o, p.d_o, p.n_tokens, (long long)p.H * p.dv, p.H, p.dv, 64)) return cudaErrorInvalidValue;
+    if (!seq_row_map(&g.v, p.v, p.n_tokens, p.v_stride, p.H, p.dv, 64) ||
+        !seq_row_map(&g.o, p.d_o, p.n_tokens, (long long)p.H * p.dv, p.H, p.dv, 64))
+        return cudaErrorInvalidValue;
     const int bytes = GradLayout<NF>(p.dv).total + 1024;
     if (!e) e = cudaFuncSetAttribute(k_chunk_grads<NF>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e) return e;
@@ -1372,14 +1959,11 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
         const size_t lines = n * p.dv * 128, slabs = (p.dk + 63) / 64;  // bytes of a term of a 64-column slab
         w.gam = (float4 *)take(n * kUnits * 32 * sizeof(float4));
         w.Sig = (bf16 *)take(3 * slabs * lines);
-        w.D = (bf16 *)take(2 * slabs * lines);
+        w.D = (bf16 *)take(3 * slabs * lines);
         w.U = (bf16 *)take(3 * lines);
         w.dR = (bf16 *)take(3 * lines);
         w.X = (float *)take(n * C * p.dv * 4);
-        w.all = (float *)take(n * (p.dv / NV) * 4 * 4);
-        w.past = (float *)take(n * (p.dv / NV) * C * 4);
-        w.into = (float *)take(n * (p.dv / NV) * C * 4);
-        w.db = (float *)take(n * (p.dv / NV) * C * 4);
+        w.Z = (float *)take(n * C * p.dv * 4);
         w.dqh = p.H > p.Hk ? (float *)take(rows * p.dk * 4) : nullptr;
         w.dkh = p.H > p.Hk ? (float *)take(rows * p.dk * 4) : nullptr;
     }
