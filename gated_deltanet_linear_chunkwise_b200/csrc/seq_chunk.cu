@@ -53,11 +53,9 @@ struct ChunkWork {
     uint2 *T, *P, *Tt, *Pt;  // [chunk x H][terms][20][32]; P or the transposes may be null
     float *gates;            // [chunk x H][3][64]: e^G, e^{G_L - G}, beta
     float4 *gam;             // [chunk x H][20][32]: e^{G_i - G_j} (0 above the diagonal) in the order of a product's result, or null
-    // gdn_bwd: the chains' matrices as bf16 terms, in the swizzled 64-column lines that k_chunk_grads loads
-    bf16 *Sig;               // [chunk x H][slabs][3][dv][64]: the state entering the chunk
-    bf16 *D;                 // [chunk x H][slabs][3][dv][64]: the gradient of the one leaving it
-    bf16 *U, *dR;            // [chunk x H][3][dv][64 tokens]
-    float *X, *Z;            // [chunk x H][dv][64]: (e^G K Sig)^T, (e^{G_L-G} K D)^T
+    // gdn_bwd: the chains' matrices, fp32
+    float *Sig, *D;          // [chunk x H][dv][dk]: the state entering the chunk; the gradient of the one leaving it
+    float *U, *dR, *X, *Z;   // [chunk x H][dv][64]; X = e^G K Sig, Z = e^{G_L-G} K D
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
 };
@@ -285,7 +283,7 @@ template <int NF, bool BWD> struct ChainSmem {
     bf16 S[kSlabs][3][NV][64];       // the state's terms, lines in the same swizzle, as all of the following
     bf16 U[3][NV][64];               // e^{G_L-G} U; backwards e^G dO
     bf16 R[3][NV][64];               // beta Y; backwards dU, then -beta e^G dR
-    bf16 W[3][NV][64];               // U (two terms for O, three to be kept); backwards dR
+    bf16 W[2][NV][64];               // U, for O
     uint2 T[3][kUnits][32], P[kTermsP][kUnits][32];
     bf16 V[C][NV];                   // v, or do
     float gates[2][3][C];
@@ -358,7 +356,6 @@ __device__ __forceinline__ void chain_leave(ChainSmem<NF, BWD> &sm, const SeqPro
     sm100::mbar_wait(&sm.bar[kBarV], now, err, sm100::kWaitLimitNs, true);
     sm100::mbar_wait(&sm.bar[kBarT], now, err, sm100::kWaitLimitNs, true);
     if (p_turn >= 0) sm100::mbar_wait(&sm.bar[kBarP], p_turn & 1, err, sm100::kWaitLimitNs, true);  // P's last fetch, if any
-    sm100::bulk_wait0();  // the fetching thread's copies to memory
     if (p.status && threadIdx.x == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
@@ -427,11 +424,6 @@ template <int N> __device__ __forceinline__ void put_pair(uint32_t at, int half,
 #pragma unroll
     for (int e = 0; e < N; ++e) sts(at + e * kPlane + half * 1024, t[e]);
 }
-// A term's 16 lines from shared memory into a matrix of dv lines, by the copy engine.
-__device__ __forceinline__ void keep_plane(bf16 *dst, int dv, int c0, int plane, const void *src) {
-    sm100::bulk_copy_s2g(dst + ((size_t)plane * dv + c0) * 64, src, kPlane);
-}
-
 // st = decay st + sum over the planes pl: (plane's 3 terms [16][64 tokens]) x (rows [64 tokens][dk]).
 // Here and below the next step's fragments are loaded before a step's products: left to the compiler, each
 // step waited for its own loads (840 clocks for 48 products a warp).
@@ -583,7 +575,6 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        if (SAVE) sm100::fence_proxy_async_smem();  // the state's terms go to memory by the copy engine
         ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err);
         // behind this barrier the state's terms are there and the last step's buffers have been read
         if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, SAVE ? -1 : (int)c - 1, w.err);
@@ -598,18 +589,9 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
             __syncthreads();
         }
         if (warp == kFetchWarp) {  // it keeps the barriers' count
-            if (SAVE && fetcher) {
-                for (int e = 0; e < 3 * kSlabs; ++e) keep_plane(w.Sig + idx * 3 * kSlabs * p.dv * 64, p.dv, c0, e, sm.S[e / 3][e % 3]);
-                sm100::bulk_commit();
-                sm100::bulk_wait_read0();  // these, and U's of the step before
-            }
             __syncthreads();
             if (fetcher && c + 1 < n_chunks) fetch.v(first_row(c + 1), !SAVE);
             __syncthreads();
-            if (SAVE && fetcher) {
-                for (int e = 0; e < 3; ++e) keep_plane(w.U + idx * 3 * p.dv * 64, p.dv, c0, e, sm.W[e]);
-                sm100::bulk_commit();
-            }
             if (fetcher && c + 1 < n_chunks) fetch.t(w.T + index(c + 1) * 3 * kUnits * 32);
             continue;
         }
@@ -639,6 +621,10 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
             }
             continue;
         }
+        if (SAVE)
+            st.each(warp, lane, [&](int n, int k, float &x, float &y) {
+                *reinterpret_cast<float2 *>(w.Sig + (idx * p.dv + c0 + n) * DK + k) = make_float2(x, y);
+            });
         // X^T = S K^T
         float kh[2][4], kl[2][4];
         state_times<NF, 3>(kh, kl, aS, sm100::smem_u32(sm.K[b]), t0, t1, lane);
@@ -668,13 +654,13 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
             const float2 el = *reinterpret_cast<const float2 *>(&sm.gates[b][1][tok]);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int i = 2 * half;
+                const int n = lane / 4 + 8 * half, i = 2 * half;
                 const float x = uh[t][i] + (ul[t][0][i] + ul[t][1][i]), y = uh[t][i + 1] + (ul[t][0][i + 1] + ul[t][1][i + 1]);
                 put_pair<3>(pair_addr(aU, t ? t1 : t0, lane), half, el.x * x, el.y * y);
-                put_pair<SAVE ? 3 : 2>(pair_addr(sm100::smem_u32(sm.W), t ? t1 : t0, lane), half, x, y);
+                if (SAVE) *reinterpret_cast<float2 *>(w.U + (idx * p.dv + c0 + n) * C + tok) = make_float2(x, y);
+                else put_pair<2>(pair_addr(sm100::smem_u32(sm.W), t ? t1 : t0, lane), half, x, y);
             }
         }
-        if (SAVE) sm100::fence_proxy_async_smem();
         __syncthreads();
         const uint32_t planes[1] = {aU}, krows[1] = {sm100::smem_u32(sm.K[b])};
         update_state<NF, 1>(st, sm.gates[b][0][C - 1], planes, krows, warp, lane);
@@ -684,7 +670,6 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.S_out + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
-    if (SAVE && fetcher) sm100::bulk_wait0();
     // the last waits' answers: nobody reads buffers any more, so every thread may report for itself
     if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
@@ -733,7 +718,6 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        sm100::fence_proxy_async_smem();  // the state's terms go to memory by the copy engine
         ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err) &&
              sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
         if (!__syncthreads_and(ok)) return chain_leave(sm, p, turn, (int)turn, w.err);
@@ -745,25 +729,18 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             __syncthreads();
         }
         if (warp == 4) {
-            if (fetcher) {
-                for (int x = 0; x < kSlabs; ++x)
-                    for (int e = 0; e < 3; ++e) keep_plane(w.D + idx * 3 * kSlabs * p.dv * 64, p.dv, c0, 3 * x + e, sm.S[x][e]);
-                sm100::bulk_commit();
-                sm100::bulk_wait_read0();  // these, and dR's of the step before
-            }
             __syncthreads();
             if (fetcher && c > 0) fetch.v(first_row(c - 1), false);
             __syncthreads();
             if (fetcher && c > 0) fetch.t(w.Tt + index(c - 1) * 3 * kUnits * 32);
             __syncthreads();
-            if (fetcher) {
-                for (int e = 0; e < 3; ++e) keep_plane(w.dR + idx * 3 * p.dv * 64, p.dv, c0, e, sm.W[e]);
-                sm100::bulk_commit();
-            }
             __syncthreads();
             if (fetcher && c > 0) fetch.p(w.Pt + index(c - 1) * 3 * kUnits * 32, first_row(c - 1), true);
             continue;
         }
+        st.each(warp, lane, [&](int n, int k, float &x, float &y) {
+            *reinterpret_cast<float2 *>(w.D + (idx * p.dv + c0 + n) * DK + k) = make_float2(x, y);
+        });
         // D^T K^T, and dO^T P
         float zh[2][4], zl[2][4], ph[2][4], pl[2][2][4];
         state_times<NF, 3>(zh, zl, aS, sm100::smem_u32(sm.K[b]), t0, t1, lane);
@@ -799,7 +776,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             for (int half = 0; half < 2; ++half) {
                 const int i = 2 * half;
                 float x = rh[t][i] + (rl[t][0][i] + rl[t][1][i]), y = rh[t][i + 1] + (rl[t][0][i + 1] + rl[t][1][i + 1]);
-                put_pair<3>(pair_addr(sm100::smem_u32(sm.W), t ? t1 : t0, lane), half, x, y);
+                *reinterpret_cast<float2 *>(w.dR + (idx * p.dv + c0 + lane / 4 + 8 * half) * C + tok) = make_float2(x, y);
                 x *= be.x;
                 y *= be.y;
                 put_pair<3>(pair_addr(aR, t ? t1 : t0, lane), half, -eg.x * x, -eg.y * y);
@@ -812,7 +789,6 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
                         odd ? pack(other, y) : pack(x, other);
             }
         }
-        sm100::fence_proxy_async_smem();
         __syncthreads();
         const uint32_t planes[2] = {aU, aR}, mrows[2] = {sm100::smem_u32(sm.Q), sm100::smem_u32(sm.K[b])};
         update_state<NF, 2>(st, sm.gates[b][0][C - 1], planes, mrows, warp, lane);
@@ -823,7 +799,6 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.dS_in + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
-    if (fetcher) sm100::bulk_wait0();
     if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
@@ -993,14 +968,6 @@ __device__ __forceinline__ void walk_store(bf16 *dst, long long row_elems, const
         }
 }
 
-// A pair's terms into lines [dv][64] at (line, column pair): dst is the first term's line 0.
-template <int N> __device__ __forceinline__ void keep_pair(bf16 *dst, int dv, int line, int col, float x, float y) {
-    uint32_t t[N];
-    split(x, y, t);
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        *reinterpret_cast<uint32_t *>((char *)dst + ((size_t)e * dv + line) * 128 + (((col >> 3 & 7) ^ (line & 7)) << 4) + (col & 7) * 2) = t[e];
-}
 // Which slice a thread's warp walks.
 struct WalkPlace {
     int s, h, hk, c0, slice, slices;  // c0: the block's first column; slices: how many the block has
@@ -1095,8 +1062,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_const
             for (int t = 0; t < 2 * NF; ++t)
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
-                    keep_pair<3>(w.Sig + (idx * kSlabs + t / 8) * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * (t & 7) + j0, S[t][2 * half],
-                                 S[t][2 * half + 1]);
+                    *reinterpret_cast<float2 *>(w.Sig + (idx * p.dv + col + n0 + 8 * half) * DK + 8 * t + j0) =
+                        make_float2(S[t][2 * half], S[t][2 * half + 1]);
         }
         float R[8][4];
         {
@@ -1144,7 +1111,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_const
             for (int t = 0; t < 8; ++t)
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
-                    keep_pair<3>(w.U + idx * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * t + j0, U[t][2 * half], U[t][2 * half + 1]);
+                    *reinterpret_cast<float2 *>(w.U + (idx * p.dv + col + n0 + 8 * half) * C + 8 * t + j0) =
+                        make_float2(U[t][2 * half], U[t][2 * half + 1]);
         } else {
             float O[8][4], none[1][4];
             walk_state_times<NF, 2, true>(O, none, S, sm100::smem_u32(sm.Q), bl);
@@ -1260,8 +1228,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
         for (int t = 0; t < 2 * NF; ++t)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                keep_pair<3>(w.D + (idx * kSlabs + t / 8) * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * (t & 7) + j0, D[t][2 * half],
-                             D[t][2 * half + 1]);
+                *reinterpret_cast<float2 *>(w.D + (idx * p.dv + col + n0 + 8 * half) * DK + 8 * t + j0) =
+                    make_float2(D[t][2 * half], D[t][2 * half + 1]);
         float X[8][4];  // dU, then dR
         {
             float Z[8][4], lo[8][4];
@@ -1331,7 +1299,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
             const float2 h = *reinterpret_cast<const float2 *>(be + 8 * t);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                keep_pair<3>(w.dR + idx * 3 * p.dv * 64, p.dv, col + n0 + 8 * half, 8 * t + j0, X[t][2 * half], X[t][2 * half + 1]);
+                *reinterpret_cast<float2 *>(w.dR + (idx * p.dv + col + n0 + 8 * half) * C + 8 * t + j0) =
+                    make_float2(X[t][2 * half], X[t][2 * half + 1]);
                 X[t][2 * half] *= h.x;
                 X[t][2 * half + 1] *= h.y;
             }
@@ -1365,8 +1334,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
 // Warps 0-3 (role 0) make dQ, warps 4-7 dK, first the parts inside the chunk, then those through the states:
 //   dQ = dP K + e^G dO Sig^T,  dK = (beta dA) K + [dP; beta dA]^T [Q; K] - beta e^G dR Sig^T + e^{G_L-G} U D^T
 // Products that reach the gates' fp32 gradients are at fp32 accuracy (dP, dA, dO Sig^T: every term); those that only
-// reach the bf16 dQ and dK take two terms of each operand.  The matrices come as the terms that the chains had at
-// hand (converting fp32 here took more instructions than the products: 755 us against NNN).
+// reach the bf16 dQ and dK take two terms of each operand.
 struct GradMaps {
     CUtensorMap q, k, v, o;
 };
@@ -1395,7 +1363,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     extern __shared__ unsigned char raw[];
     __shared__ __align__(16) float gates[3][C], part_sums[8][3][C];  // read and written in pairs
     __shared__ float into[C], past[C], db[C], sums[4][C], dg[C], red[8];
-    __shared__ uint64_t bar[2];
+    __shared__ uint64_t bar[1];
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
     const int mt = warp & 3, role = warp >> 2, dv = p.dv, nvf = dv / 16;
@@ -1407,23 +1375,23 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     const uint32_t base = sm100::smem_u32(sm), plane = at.plane;
     if (tid == 0) {
         sm100::mbar_init(&bar[0], 1);
-        sm100::mbar_init(&bar[1], 1);
         sm100::fence_barrier_init();
     }
     __syncthreads();
-    const bf16 *Um = w.U + idx * 3 * dv * 64, *Rm = w.dR + idx * 3 * dv * 64;
+    const float *Um = w.U + idx * dv * C, *Rm = w.dR + idx * dv * C, *Sm = w.Sig + idx * dv * DK, *Dm = w.D + idx * dv * DK;
+    if (tid == 32) {  // into L2 for later
+        sm100::bulk_prefetch_l2(Sm, dv * DK * 4);
+        sm100::bulk_prefetch_l2(Dm, dv * DK * 4);
+        sm100::bulk_prefetch_l2(w.gam + idx * kUnits * 32, kUnits * 32 * 16);
+    }
     if (tid == 0) {
-        sm100::mbar_arrive_expect_tx(&bar[0], 2 * at.kTile + (dv + 63) / 64 * 2 * C * 128 + 6 * plane);
+        sm100::mbar_arrive_expect_tx(&bar[0], 2 * at.kTile + (dv + 63) / 64 * 2 * C * 128);
         for (int x = 0; x < kSlabs; ++x) {
             sm100::tma_load_3d(sm + at.K + x * C * 128, &maps.k, &bar[0], 64 * x, hk, (int)ch.first);
             sm100::tma_load_3d(sm + at.Q + x * C * 128, &maps.q, &bar[0], 64 * x, hk, (int)ch.first);
         }
         for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.O + x * C * 128, &maps.o, &bar[0], 64 * x, h, (int)ch.first);
         for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.PA + x * C * 128, &maps.v, &bar[0], 64 * x, h, (int)ch.first);
-        sm100::bulk_copy_g2s(sm + at.UR, Um, 2 * plane, &bar[0]);
-        sm100::bulk_copy_g2s(sm + at.UR + 2 * plane, Rm, 2 * plane, &bar[0]);
-        sm100::bulk_copy_g2s(sm + at.last, Um + 2 * dv * 64, plane, &bar[0]);
-        sm100::bulk_copy_g2s(sm + at.last + plane, Rm + 2 * dv * 64, plane, &bar[0]);
     }
     if (tid < 3 * C) gates[0][tid] = w.gates[idx * 3 * C + tid];
     const int i0 = 16 * mt + lane / 4, j0 = 2 * (lane & 3);  // this lane's rows i0, i0 + 8; its columns 8 t + j0, + 1
@@ -1439,20 +1407,27 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         zero_tail((bf16 *)(sm + at.PA), (dv + 63) / 64, 8, ch.rows);
         __syncthreads();
     }
-    {  // sums over dv: past = U . Z, into = -beta dR . X (k's part), db = dR . (V - X).  A pair of tokens a lane, dv over the warps
-        const float *X = w.X + idx * dv * C + 2 * lane, *Z = w.Z + idx * dv * C + 2 * lane;
+    {  // U and dR as terms, and the sums over dv: past = U . Z, into = -beta dR . X (k's part), db = dR . (V - X).  A pair of
+       // tokens a lane, dv over the warps
         const float2 be = *reinterpret_cast<const float2 *>(&gates[2][2 * lane]);
         float s[3][2] = {};
 #pragma unroll 4
         for (int n = warp; n < dv; n += 8) {
-            const float2 x = *reinterpret_cast<const float2 *>(X + n * C), z = *reinterpret_cast<const float2 *>(Z + n * C);
-            const int line = n * 128 + ((lane >> 2 ^ (n & 7)) << 4) + (lane & 3) * 4;
-            auto sum3 = [&](int first, int third) {
-                const uint32_t a = *reinterpret_cast<const uint32_t *>(sm + first + line), b = *reinterpret_cast<const uint32_t *>(sm + first + plane + line),
-                               c = *reinterpret_cast<const uint32_t *>(sm + third + line);
-                return make_float2(low_of(a) + (low_of(b) + low_of(c)), high_of(a) + (high_of(b) + high_of(c)));
-            };
-            const float2 u = sum3(at.UR, at.last), r = sum3(at.UR + 2 * plane, at.last + plane);
+            const size_t from = (size_t)n * C + 2 * lane;
+            const float2 u = *reinterpret_cast<const float2 *>(Um + from), r = *reinterpret_cast<const float2 *>(Rm + from),
+                         x = *reinterpret_cast<const float2 *>(w.X + idx * dv * C + from),
+                         z = *reinterpret_cast<const float2 *>(w.Z + idx * dv * C + from);
+            const uint32_t line = base + n * 128 + ((lane >> 2 ^ (n & 7)) << 4) + (lane & 3) * 4;
+            uint32_t a[3], b[3];
+            split(u.x, u.y, a);
+            split(r.x, r.y, b);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sts(line + at.UR + i * plane, a[i]);
+                sts(line + at.UR + (2 + i) * plane, b[i]);
+            }
+            sts(line + at.last, a[2]);
+            sts(line + at.last + plane, b[2]);
             float v[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -1466,7 +1441,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i) *reinterpret_cast<float2 *>(&part_sums[warp][i][2 * lane]) = make_float2(s[i][0], s[i][1]);
-        __syncthreads();  // and v has been read
+        __syncthreads();  // the terms are there, v has been read
         if (tid < 3 * C) {
             float x = 0.f;
 #pragma unroll
@@ -1699,7 +1674,6 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             s = quad(s);
             if ((tid & 3) == 0) dg[i] = s;
         }
-        sm100::fence_proxy_async_smem();
         __syncthreads();  // all that the state's columns take the place of has been read
     }
     // ---- through the states
@@ -1709,34 +1683,26 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         constexpr int kLast = NF % 4 ? NF % 4 : 4;
         constexpr int kFull = 4;
         const int groups = slab + 1 < kSlabs ? kFull : kLast;  // of 16 columns
-        if (tid == 0) {
-            sm100::mbar_arrive_expect_tx(&bar[1], 5 * plane);
-            sm100::bulk_copy_g2s(sm + at.last, w.Sig + (idx * kSlabs + slab) * 3 * dv * 64, 3 * plane, &bar[1]);
-            sm100::bulk_copy_g2s(sm + at.last + 3 * plane, w.D + (idx * kSlabs + slab) * 3 * dv * 64, 2 * plane, &bar[1]);
-        }
-        if (!__syncthreads_and(sm100::mbar_wait(&bar[1], slab, w.err))) {
-            sm100::mbar_wait(&bar[1], slab, w.err, sm100::kWaitLimitNs, true);
-            if (p.status && tid == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
-            return;
-        }
-        {  // <D, Sig> over the slab; D's third term from memory
-            const bf16 *third = w.D + ((idx * kSlabs + slab) * 3 + 2) * dv * 64;
-            const int pieces = 4 * groups;  // of 8 bytes a line
+        // Sig's and D's columns as terms, and <D, Sig> over them
+        const int pieces = 4 * groups;  // of four columns a line
 #pragma unroll 4
-            for (int i = tid; i < dv * pieces; i += 256) {
-                const int n = i / pieces, c4 = i % pieces, line = n * 128 + ((c4 >> 1 ^ (n & 7)) << 4) + (c4 & 1) * 8;
-                const uint2 d2 = *reinterpret_cast<const uint2 *>((const char *)third + line);
-                uint2 m[5];
+        for (int i = tid; i < dv * pieces; i += 256) {
+            const int n = i / pieces, c4 = i % pieces;
+            const float4 s = *reinterpret_cast<const float4 *>(Sm + (size_t)n * DK + 64 * slab + 4 * c4);
+            const float4 d = *reinterpret_cast<const float4 *>(Dm + (size_t)n * DK + 64 * slab + 4 * c4);
+            all = fmaf(s.x, d.x, fmaf(s.y, d.y, fmaf(s.z, d.z, fmaf(s.w, d.w, all))));
+            uint32_t a[3], b[3], e[2], f[2];
+            split(s.x, s.y, a);
+            split(s.z, s.w, b);
+            split(d.x, d.y, e);
+            split(d.z, d.w, f);
+            unsigned char *line = sm + at.last + n * 128 + ((c4 >> 1 ^ (n & 7)) << 4) + (c4 & 1) * 8;
 #pragma unroll
-                for (int x = 0; x < 5; ++x) m[x] = *reinterpret_cast<const uint2 *>(sm + at.last + x * plane + line);
-                auto dot = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f) {
-                    all = fmaf(low_of(a) + (low_of(b) + low_of(c)), low_of(d) + (low_of(e) + low_of(f)), all);
-                    all = fmaf(high_of(a) + (high_of(b) + high_of(c)), high_of(d) + (high_of(e) + high_of(f)), all);
-                };
-                dot(m[0].x, m[1].x, m[2].x, m[3].x, m[4].x, d2.x);
-                dot(m[0].y, m[1].y, m[2].y, m[3].y, m[4].y, d2.y);
-            }
+            for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2 *>(line + x * plane) = make_uint2(a[x], b[x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) *reinterpret_cast<uint2 *>(line + (3 + x) * plane) = make_uint2(e[x], f[x]);
         }
+        __syncthreads();
         const uint32_t s0 = base + at.last, u01 = base + at.UR;
         float x[8][4], y[8][4];  // role 0: leading and small products; role 1: dR Sig^T and U D^T
 #pragma unroll
@@ -1884,6 +1850,12 @@ bool make_maps(ChainMaps &m, const SeqProblem &p, const void *v, long long v_str
            seq_row_map(&m.v, v, p.n_tokens, v_stride, p.H, p.dv, v_cols);
 }
 
+unsigned num_sms() {
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return (unsigned)n;
+}
+
 bool walk(const SeqProblem &p) { return getenv("GDN_COOP") == nullptr; }
 unsigned walk_blocks(const SeqProblem &p) {
     return (unsigned)((long long)p.n_seqs * p.H * ((p.dv + 16 * kSlices - 1) / (16 * kSlices)));
@@ -1956,12 +1928,11 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
     } else {
         w.Tt = (uint2 *)take(3 * frag);
         w.Pt = (uint2 *)take(3 * frag);
-        const size_t lines = n * p.dv * 128, slabs = (p.dk + 63) / 64;  // bytes of a term of a 64-column slab
         w.gam = (float4 *)take(n * kUnits * 32 * sizeof(float4));
-        w.Sig = (bf16 *)take(3 * slabs * lines);
-        w.D = (bf16 *)take(3 * slabs * lines);
-        w.U = (bf16 *)take(3 * lines);
-        w.dR = (bf16 *)take(3 * lines);
+        w.Sig = (float *)take(n * p.dk * p.dv * 4);
+        w.D = (float *)take(n * p.dk * p.dv * 4);
+        w.U = (float *)take(n * C * p.dv * 4);
+        w.dR = (float *)take(n * C * p.dv * 4);
         w.X = (float *)take(n * C * p.dv * 4);
         w.Z = (float *)take(n * C * p.dv * 4);
         w.dqh = p.H > p.Hk ? (float *)take(rows * p.dk * 4) : nullptr;
