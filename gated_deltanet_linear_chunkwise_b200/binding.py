@@ -74,6 +74,8 @@ class GdnSeqArgs(ctypes.Structure):
     ]
 
 
+_SEQ_ARGS_BYTES = ctypes.sizeof(GdnSeqArgs)
+
 GDN_SEQ_BAD_SLOT = 1
 GDN_SEQ_SAME_SLOT = 2
 GDN_SEQ_BAD_ROWS = 4
@@ -324,10 +326,10 @@ def _need(ok, status, text):
         raise GdnError(status, text)
 
 
-def _tokens(name, t, q, lead, heads, d):
+def _tokens(name, t, dtype, device, lead, heads, d):
     """A q/k/v-like tensor [*lead, heads, d]: checked; returns the elements between its token rows."""
-    if t.device != q.device or t.dtype != q.dtype:
-        raise GdnError(1, "%s must have q's device and dtype (%s, %s)" % (name, q.device, q.dtype))
+    if t.dtype is not dtype or t.device != device:
+        raise GdnError(1, "%s must have q's device and dtype (%s, %s)" % (name, device, dtype))
     if t.shape != (*lead, heads, d):
         raise GdnError(2, "%s must have shape %s, got %s" % (name, (*lead, heads, d), tuple(t.shape)))
     if t.is_contiguous():
@@ -340,47 +342,44 @@ def _tokens(name, t, q, lead, heads, d):
 
 
 def _plain(name, t, dtype, shape, device):
-    """A contiguous tensor of one type and shape (None in a shape: any size), or None."""
+    """The address of a contiguous tensor of one type and shape, or None of None."""
     if t is None:
         return None
-    if t.device != device or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise GdnError(1, "%s must be a contiguous %s tensor on %s" % (name, str(dtype).replace("torch.", ""), device))
-    if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise GdnError(2, "%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.shape != shape:
+        raise GdnError(2, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t.data_ptr()
 
 
 def _seq_args(q, k, v, alpha, beta, lead):
-    """The arguments that the sequence entries share; `lead` is the tokens' leading shape."""
+    """The arguments that the sequence entries share; `lead` is the tokens' leading shape.  A serving loop pays
+    for this at every token, so each attribute is asked for once."""
     import torch
-    for name, t in (("q", q), ("k", k), ("v", v), ("alpha", alpha), ("beta", beta)):
-        if t is None:
-            raise GdnError(1, "%s is required" % name)
+    if q is None or k is None or v is None or alpha is None or beta is None:
+        raise GdnError(1, "q, k, v, alpha and beta are required (one is None)")
     if not q.is_cuda:
         raise GdnError(1, "q is not a CUDA tensor")
-    if q.dtype is not torch.bfloat16 and q.dtype is not torch.float32:
+    dtype, dev, n = q.dtype, q.device, len(lead)
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise GdnError(1, "q/k/v must share one dtype, bf16 or fp32")
-    n = len(lead)
-    if q.dim() != n + 2 or v.dim() != n + 2:
-        raise GdnError(2, "q and v must have %d dimensions, got %s and %s" % (n + 2, tuple(q.shape), tuple(v.shape)))
-    Hk, d_k = q.shape[n:]
-    H, d_v = v.shape[n:]
-    a = GdnSeqArgs()
-    a.struct_size = ctypes.sizeof(GdnSeqArgs)
-    a.dtype = GDN_DTYPE_BF16 if q.dtype is torch.bfloat16 else GDN_DTYPE_F32
-    a.q_stride = _tokens("q", q, q, lead, Hk, d_k)
-    a.k_stride = _tokens("k", k, q, lead, Hk, d_k)
-    a.v_stride = _tokens("v", v, q, lead, H, d_v)
-    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    a.alpha = _plain("alpha", alpha, torch.float32, (*lead, H), q.device)
-    a.beta = _plain("beta", beta, torch.float32, (*lead, H), q.device)
+    qs, vs = q.shape, v.shape
+    if len(qs) != n + 2 or len(vs) != n + 2:
+        raise GdnError(2, "q and v must have %d dimensions, got %s and %s" % (n + 2, tuple(qs), tuple(vs)))
+    Hk, d_k = qs[n], qs[n + 1]
+    H, d_v = vs[n], vs[n + 1]
+    a = GdnSeqArgs(_SEQ_ARGS_BYTES, GDN_DTYPE_BF16 if dtype is torch.bfloat16 else GDN_DTYPE_F32,
+                   q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                   _plain("alpha", alpha, torch.float32, (*lead, H), dev),
+                   _plain("beta", beta, torch.float32, (*lead, H), dev),
+                   _tokens("q", q, dtype, dev, lead, Hk, d_k), _tokens("k", k, dtype, dev, lead, Hk, d_k),
+                   _tokens("v", v, dtype, dev, lead, H, d_v))
     a.H, a.Hk, a.d_k, a.d_v = H, Hk, d_k, d_v
-    return a
+    return a, dtype, dev, H, d_k, d_v
 
 
 def _lead(q, cu_seqlens):
     """Leading shape of the tokens, and (n_seqs, seq_len, n_tokens)."""
-    import torch
     if cu_seqlens is None:
         if q.dim() != 4:
             raise GdnError(2, "without cu_seqlens q is [B, T, Hk, d_k], got %s" % (tuple(q.shape),))
@@ -399,26 +398,25 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
-        self.outer = []
+        self.outer = None
         if stream is not None:
-            self.outer.append(torch.cuda.stream(stream))
-        elif device.index != torch.cuda.current_device():
-            self.outer.append(torch.cuda.device(device))
-        self.handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+            if stream.device != device:
+                raise GdnError(1, "stream is on %s, the tensors on %s" % (stream.device, device))
+            self.outer = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+        else:
+            if device.index != torch._C._cuda_getDevice():
+                self.outer = torch.cuda.device(device)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
 
     def __enter__(self):
-        for c in self.outer:
-            c.__enter__()
+        if self.outer is not None:
+            self.outer.__enter__()
         return self.handle
 
     def __exit__(self, *e):
-        for c in reversed(self.outer):
-            c.__exit__(*e)
-
-
-def _stream_device(stream, device):
-    if stream is not None and stream.device != device:
-        raise GdnError(1, "stream is on %s, the tensors on %s" % (stream.device, device))
+        if self.outer is not None:
+            self.outer.__exit__(*e)
 
 
 def gdn_decode(q, k, v, alpha, beta, S, slots=None, *, o=None, status=None, stream=None):
@@ -435,23 +433,27 @@ def gdn_decode(q, k, v, alpha, beta, S, slots=None, *, o=None, status=None, stre
     Returns (o, S).
     """
     import torch
-    lead = q.shape[:-2]
-    _need(len(lead) in (1, 2), 2, "q is [B, n, Hk, d_k] or [B, Hk, d_k], got %s" % (tuple(q.shape),))
-    a = _seq_args(q, k, v, alpha, beta, tuple(lead))
-    dev = q.device
-    _need(S is not None, 1, "S is required")
-    a.n_seqs, a.seq_len = lead[0], lead[1] if len(lead) == 2 else 1
-    a.n_tokens = a.n_seqs * a.seq_len
-    a.S_in = a.S_out = _plain("S", S, torch.float32, (None, a.H, a.d_v, a.d_k), dev)
-    a.n_slots = S.shape[0]
-    a.slots = _plain("slots", slots, torch.int32, (lead[0],), dev)
-    a.status_dev = _plain("status", status, torch.int32, (1,), dev)
-    _stream_device(stream, dev)
+    if q is None or S is None:
+        raise GdnError(1, "q and S are required")
+    lead = tuple(q.shape[:-2])
+    if len(lead) != 1 and len(lead) != 2:
+        raise GdnError(2, "q is [B, n, Hk, d_k] or [B, Hk, d_k], got %s" % (tuple(q.shape),))
+    a, dtype, dev, H, d_k, d_v = _seq_args(q, k, v, alpha, beta, lead)
+    B, n = lead[0], lead[1] if len(lead) == 2 else 1
+    n_slots = S.shape[0] if S.dim() else 0
+    a.S_in = a.S_out = _plain("S", S, torch.float32, (n_slots, H, d_v, d_k), dev)
+    a.n_seqs, a.seq_len, a.n_tokens, a.n_slots = B, n, B * n, n_slots
+    if slots is not None:
+        a.slots = _plain("slots", slots, torch.int32, (B,), dev)
+    if status is not None:
+        a.status_dev = _plain("status", status, torch.int32, (1,), dev)
     with _On(dev, stream) as a.stream:
         if o is None:
-            o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-        a.o = _plain("o", o, v.dtype, v.shape, dev)
-        check(load_library().gdn_decode(ctypes.byref(a)))
+            o = torch.empty(v.shape, dtype=dtype, device=dev)
+            a.o = o.data_ptr()
+        else:
+            a.o = _plain("o", o, dtype, v.shape, dev)
+        check((_lib or load_library()).gdn_decode(ctypes.byref(a)))
     return o, S
 
 
@@ -471,8 +473,7 @@ def gdn_packed(q, k, v, alpha, beta, cu_seqlens=None, S_in=None, *, S_out=None, 
     """
     import torch
     lead, n, T, N = _lead(q, cu_seqlens)
-    a = _seq_args(q, k, v, alpha, beta, lead)
-    dev = q.device
+    a, dtype, dev, H, d_k, d_v = _seq_args(q, k, v, alpha, beta, lead)
     a.n_seqs, a.seq_len, a.n_tokens = n, T, N
     a.cu_seqlens = _plain("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
     a.slots = _plain("slots", slots, torch.int32, (n,), dev)
@@ -480,18 +481,17 @@ def gdn_packed(q, k, v, alpha, beta, cu_seqlens=None, S_in=None, *, S_out=None, 
         fresh = fresh.view(torch.uint8)
     a.fresh = _plain("fresh", fresh, torch.uint8, (n,), dev)
     a.status_dev = _plain("status", status, torch.int32, (1,), dev)
-    _stream_device(stream, dev)
     with _On(dev, stream) as a.stream:
         if o is None:
-            o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+            o = torch.empty(v.shape, dtype=dtype, device=dev)
         if S_out is None and return_state:
             _need(slots is None, 1, "return_state makes one state a sequence: with slots pass S_out")
-            S_out = torch.empty((n, a.H, a.d_v, a.d_k), dtype=torch.float32, device=dev)
-        a.o = _plain("o", o, v.dtype, v.shape, dev)
-        pools = [t for t in (S_in, S_out) if t is not None]
-        a.n_slots = pools[0].shape[0] if pools else n
-        a.S_in = _plain("S_in", S_in, torch.float32, (a.n_slots, a.H, a.d_v, a.d_k), dev)
-        a.S_out = _plain("S_out", S_out, torch.float32, (a.n_slots, a.H, a.d_v, a.d_k), dev)
+            S_out = torch.empty((n, H, d_v, d_k), dtype=torch.float32, device=dev)
+        a.o = _plain("o", o, dtype, v.shape, dev)
+        pool = S_in if S_in is not None else S_out
+        a.n_slots = n if pool is None else pool.shape[0] if pool.dim() else 0
+        a.S_in = _plain("S_in", S_in, torch.float32, (a.n_slots, H, d_v, d_k), dev)
+        a.S_out = _plain("S_out", S_out, torch.float32, (a.n_slots, H, d_v, d_k), dev)
         _seq_workspace(a, workspace, dev, 0)
         check(load_library().gdn_packed(ctypes.byref(a)))
     return o, S_out
@@ -524,18 +524,16 @@ def gdn_bwd(q, k, v, alpha, beta, do, cu_seqlens=None, S_in=None, *, dS_out=None
     """
     import torch
     lead, n, T, N = _lead(q, cu_seqlens)
-    a = _seq_args(q, k, v, alpha, beta, lead)
-    dev = q.device
+    a, dtype, dev, H, d_k, d_v = _seq_args(q, k, v, alpha, beta, lead)
     a.n_seqs, a.seq_len, a.n_tokens = n, T, N
     a.cu_seqlens = _plain("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
-    state = (n, a.H, a.d_v, a.d_k)
+    state = (n, H, d_v, d_k)
     a.n_slots = n
     a.S_in = _plain("S_in", S_in, torch.float32, state, dev)
     a.dS_out = _plain("dS_out", dS_out, torch.float32, state, dev)
     _need(do is not None, 1, "do is required")
-    a.d_o = _plain("do", do, v.dtype, v.shape, dev)
+    a.d_o = _plain("do", do, dtype, v.shape, dev)
     a.status_dev = _plain("status", status, torch.int32, (1,), dev)
-    _stream_device(stream, dev)
     with _On(dev, stream) as a.stream:
         dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k))
         dv = torch.empty(v.shape, dtype=v.dtype, device=dev)

@@ -23,7 +23,6 @@
 // round trip through tensor memory for each of three dependent products of a step.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cstdlib>
 
 #include "gates.cuh"
 #include "seq_internal.h"
@@ -1856,7 +1855,11 @@ unsigned num_sms() {
     return (unsigned)n;
 }
 
-bool walk(const SeqProblem &p) { return getenv("GDN_COOP") == nullptr; }
+// A warp a slice, or four warps on each?  With few slices a step's length counts, and four warps halve it; with many
+// the SMs are full either way and a warp a slice moves less through shared memory.  Measured (20 heads, d = 112, us, a warp / four
+// warps): packed 140 slices 360 / 178, 560 455 / 347, 840 275 / 268, 1120 269 / 360, 5600 123 / 255; bwd 140 1066 / 682, 840
+// 1024 / 1025, 1120 1113 / 1340.
+bool walk(const SeqProblem &p) { return (long long)p.n_seqs * p.H * (p.dv / NV) >= 6ll * num_sms(); }
 unsigned walk_blocks(const SeqProblem &p) {
     return (unsigned)((long long)p.n_seqs * p.H * ((p.dv + 16 * kSlices - 1) / (16 * kSlices)));
 }
