@@ -1163,7 +1163,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
     extern __shared__ unsigned char raw[];
     auto &sm = *reinterpret_cast<WalkSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const WalkPlace at = walk_place(p);
-    const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice, groups = p.dv / NV;
+    const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
     const SeqRange r = seq_rows(p, at.s);
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, at.s, r.first);  // 0 of a bad range
     const WalkFetch<NF, true> fetch = {sm, maps, w, at.hk, at.h, at.c0};

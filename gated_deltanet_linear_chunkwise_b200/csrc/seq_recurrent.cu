@@ -12,6 +12,7 @@
 // tokens' rows staged in shared memory a block ahead.  Its bound is the fp32 pipe: 4 d_k d_v
 // instructions' lanes a token and head.
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "seq_internal.h"
 
@@ -35,66 +36,106 @@ __device__ __forceinline__ float quad_sum(float x) {
     return x;
 }
 
-// One token on a lane's piece of a row; k and q are this lane's pieces of the token's rows.
-// Returns u's row value's output sum (already over the row).
-template <int NF>
-__device__ __forceinline__ float token_step(float4 (&S)[NF], const float4 (&k)[NF], const float4 (&q)[NF], float alpha,
-                                            float beta, float v) {
+__device__ __forceinline__ float4 floats(float4 x) { return x; }
+__device__ __forceinline__ float4 floats(uint2 r) {  // four bf16
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
+}
+
+// One token on a lane's piece of a row; k and q are this lane's pieces of the token's rows (as they lie in memory:
+// widened where they are used, they take half the registers).  Returns o's value, summed over the row's lanes.
+template <int NF, typename Piece>
+__device__ __forceinline__ float token_step(float4 (&S)[NF], const Piece (&k)[NF], const Piece (&q)[NF], float alpha, float beta, float v) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
+        const float4 x = floats(k[j]);
         S[j].x *= alpha; S[j].y *= alpha; S[j].z *= alpha; S[j].w *= alpha;
-        a.x = fmaf(S[j].x, k[j].x, a.x); a.y = fmaf(S[j].y, k[j].y, a.y);
-        a.z = fmaf(S[j].z, k[j].z, a.z); a.w = fmaf(S[j].w, k[j].w, a.w);
+        a.x = fmaf(S[j].x, x.x, a.x); a.y = fmaf(S[j].y, x.y, a.y);
+        a.z = fmaf(S[j].z, x.z, a.z); a.w = fmaf(S[j].w, x.w, a.w);
     }
     const float u = beta * (v - quad_sum((a.x + a.y) + (a.z + a.w)));
     a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NF; ++j) {
-        S[j].x = fmaf(u, k[j].x, S[j].x); S[j].y = fmaf(u, k[j].y, S[j].y);
-        S[j].z = fmaf(u, k[j].z, S[j].z); S[j].w = fmaf(u, k[j].w, S[j].w);
-        a.x = fmaf(S[j].x, q[j].x, a.x); a.y = fmaf(S[j].y, q[j].y, a.y);
-        a.z = fmaf(S[j].z, q[j].z, a.z); a.w = fmaf(S[j].w, q[j].w, a.w);
+        const float4 x = floats(k[j]), y = floats(q[j]);
+        S[j].x = fmaf(u, x.x, S[j].x); S[j].y = fmaf(u, x.y, S[j].y);
+        S[j].z = fmaf(u, x.z, S[j].z); S[j].w = fmaf(u, x.w, S[j].w);
+        a.x = fmaf(S[j].x, y.x, a.x); a.y = fmaf(S[j].y, y.y, a.y);
+        a.z = fmaf(S[j].z, y.z, a.z); a.w = fmaf(S[j].w, y.w, a.w);
     }
     return quad_sum((a.x + a.y) + (a.z + a.w));
 }
 
+constexpr long long kManyHeads = 1480;
 constexpr int kFewThreads = 64;  // 16 rows: d_v is a multiple of 16, so a block stays in one head
 
-template <typename T, int NF>
-__global__ void __launch_bounds__(kFewThreads) k_few(const __grid_constant__ SeqProblem p) {
-    const int per_seq = p.H * (p.dv / 16);
-    const int s = blockIdx.x / per_seq, rb = blockIdx.x % per_seq;
-    const int row = rb * 16 + threadIdx.x / 4, part = threadIdx.x & 3;
-    const int h = rb / (p.dv / 16), r = row - h * p.dv, hk = h / (p.H / p.Hk);
-    const int slot = p.slots ? p.slots[s] : s;
-    const bool inside = slot >= 0 && (!p.slots || slot < p.n_slots);
-    // the state's loads start before the slots are compared: they need only an index in range
-    float4 S[NF];
-    const size_t soff = ((size_t)(inside ? slot : 0) * p.H * p.dv + row) * p.dk + part * 4;
-    if (inside) {
+// A lane's pieces of a token's k and q rows as they lie in memory, and its row's v and gates.
+template <typename T, int NF> struct Token {
+    using Piece = typename std::conditional<sizeof(T) == 2, uint2, float4>::type;
+    Piece k[NF], q[NF];
+    float v, alpha, beta;
+    __device__ __forceinline__ void load(const SeqProblem &p, long long tok, int h, int hk, int r, int part) {
+        const T *kp = (const T *)p.k + tok * p.k_stride + (size_t)hk * p.dk + part * 4;
+        const T *qp = (const T *)p.q + tok * p.q_stride + (size_t)hk * p.dk + part * 4;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) S[j] = ld4(p.S_in + soff + 16 * j);
+        for (int j = 0; j < NF; ++j) k[j] = *reinterpret_cast<const Piece *>(kp + 16 * j);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) q[j] = *reinterpret_cast<const Piece *>(qp + 16 * j);
+        v = to_f(((const T *)p.v)[tok * p.v_stride + (size_t)h * p.dv + r]);
+        alpha = p.alpha[tok * p.H + h];
+        beta = p.beta[tok * p.H + h];
     }
+};
+// The state is read once and written once: it goes through L2 as a stream.
+template <int NF> __device__ __forceinline__ void load_state(float4 (&S)[NF], const float *from) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) S[j] = __ldcs(reinterpret_cast<const float4 *>(from + 16 * j));
+}
+template <int NF> __device__ __forceinline__ void store_state(float *to, const float4 (&S)[NF]) {
+#pragma unroll
+    for (int j = 0; j < NF; ++j) __stcs(reinterpret_cast<float4 *>(to + 16 * j), S[j]);
+}
+
+// HEAD: a block has all rows of a head, 16 at a time, and loads the next 16 while it works on these; else it has 16.
+template <typename T, int NF, bool HEAD>
+__global__ void __launch_bounds__(kFewThreads) k_few(const __grid_constant__ SeqProblem p) {
+    const int per_head = HEAD ? 1 : p.dv / 16, per_seq = p.H * per_head;
+    const int s = blockIdx.x / per_seq, rb = blockIdx.x % per_seq;
+    const int h = rb / per_head, hk = h / (p.H / p.Hk), part = threadIdx.x & 3;
+    int r = rb % per_head * 16 + threadIdx.x / 4;
+    const int slot = p.slots ? p.slots[s] : s;
+    // The first token's loads wait for nothing, and the state's only for an index in range: both are on their way
+    // while the slots are compared.
+    Token<T, NF> now;
+    if (p.seq_len > 0) now.load(p, (long long)s * p.seq_len, h, hk, r, part);
+    const bool inside = slot >= 0 && (!p.slots || slot < p.n_slots);
+    float4 S[NF], next[NF];
+    size_t soff = (((size_t)(inside ? slot : 0) * p.H + h) * p.dv + r) * p.dk + part * 4;
+    if (inside) load_state(S, p.S_in + soff);
     const SeqRange range = seq_range(p, s);
     seq_report(p, range, rb == 0 && threadIdx.x == 0);
     if (range.slot < 0) return;
-    for (long long t = 0; t < range.len; ++t) {
-        const long long tok = range.first + t;
-        const T *kp = (const T *)p.k + tok * p.k_stride + (size_t)hk * p.dk + part * 4;
-        const T *qp = (const T *)p.q + tok * p.q_stride + (size_t)hk * p.dk + part * 4;
-        const float v = to_f(((const T *)p.v)[tok * p.v_stride + (size_t)h * p.dv + r]);
-        const float alpha = p.alpha[tok * p.H + h], beta = p.beta[tok * p.H + h];
-        float4 k[NF], q[NF];
+    const int last = HEAD ? p.dv - 16 : 0;
+    for (int r0 = 0;; r0 += 16) {
+        const size_t ahead = soff + (size_t)16 * p.dk;
+        if (HEAD && r0 < last) load_state(next, p.S_in + ahead);
+        float v_next = 0.f;
+        if (HEAD && r0 < last && range.len > 0) v_next = to_f(((const T *)p.v)[range.first * p.v_stride + (size_t)h * p.dv + r + 16]);
+        for (long long t = 0; t < range.len; ++t) {
+            if (t) now.load(p, range.first + t, h, hk, r, part);
+            const float o = token_step<NF>(S, now.k, now.q, now.alpha, now.beta, now.v);
+            if (part == 0) put((T *)p.o + ((range.first + t) * p.H + h) * p.dv + r, o);
+        }
+        store_state(p.S_out + soff, S);
+        if (r0 >= last) break;
+        r += 16;
+        soff = ahead;
+        if (range.len > 1) now.load(p, range.first, h, hk, r, part);
+        now.v = v_next;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) k[j] = ld4(kp + 16 * j);
-#pragma unroll
-        for (int j = 0; j < NF; ++j) q[j] = ld4(qp + 16 * j);
-        const float o = token_step<NF>(S, k, q, alpha, beta, v);
-        if (part == 0) put((T *)p.o + (tok * p.H + h) * p.dv + r, o);
+        for (int j = 0; j < NF; ++j) S[j] = next[j];
     }
-#pragma unroll
-    for (int j = 0; j < NF; ++j) *reinterpret_cast<float4 *>(p.S_out + soff + 16 * j) = S[j];
 }
 
 // 16 tokens' k and q rows (fp32), v values of the block's 16 rows and gates, one stage.
@@ -186,8 +227,11 @@ __global__ void __launch_bounds__(kManyThreads) k_many(const __grid_constant__ S
 }
 
 template <typename T, int NF> cudaError_t launch(const SeqProblem &p, bool few, cudaStream_t s) {
-    const long long blocks = (long long)p.n_seqs * p.H * (p.dv / 16);
-    if (few) k_few<T, NF><<<(unsigned)blocks, kFewThreads, 0, s>>>(p);
+    const long long heads = (long long)p.n_seqs * p.H, blocks = heads * (p.dv / 16);
+    // A block a head once ten of them are on every SM: 256 sequences x 20 heads, d = 112: 92 us against 100 us with 16 rows a
+    // block (5.6 TB/s; an in-place product of the same bytes takes 78 us).  Below that the blocks are too few.
+    if (few && heads >= kManyHeads) k_few<T, NF, true><<<(unsigned)heads, kFewThreads, 0, s>>>(p);
+    else if (few) k_few<T, NF, false><<<(unsigned)blocks, kFewThreads, 0, s>>>(p);
     else k_many<T, NF><<<(unsigned)blocks, kManyThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
