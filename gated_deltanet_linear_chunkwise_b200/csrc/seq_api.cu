@@ -53,7 +53,7 @@ int check_sizes(const gdn_seq_args &a) {
         return fail(GDN_ERR_SHAPE, "n_tokens (%lld) is not n_seqs (%d) x seq_len (%lld)", a.n_tokens, a.n_seqs, a.seq_len);
     // one block for 16 rows of a state, one for a chunk of a head: both counts stay in a grid
     const long double blocks = (long double)a.n_seqs * a.H * (a.d_v / 16);
-    const long double chunks = ((long double)a.n_tokens / gdn::kSeqChunk + a.n_seqs + 1) * a.H;
+    const long double chunks = ((long double)a.n_tokens / gdn::kSeqChunk + a.n_seqs + 1) * a.H + 1;
     if (blocks >= 2147483648.0L || chunks >= 2147483648.0L)
         return fail(GDN_ERR_SHAPE, "n_seqs x H x d_v / 16 or chunks x H exceeds 2^31");
     return GDN_OK;

@@ -57,22 +57,44 @@ struct ChunkWork {
     float *U, *dR, *X, *Z;   // [chunk x H][dv][64]; X = e^G K Sig, Z = e^{G_L-G} K D
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
+    int *order;              // [n_seqs]: the sequences, the longest first
 };
+
+// The chains' blocks start with the longest sequences: a long one that starts last runs alone (16384 tokens in 24
+// sequences of 44 to 1971: NNN us against NNN in their order).  A sequence's place is the number of longer ones, ties by index.
+__device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order, int *len) {  // len: room for 2048
+    const bool sort = p.cu && p.n_seqs <= 2048;
+    if (sort)
+        for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) len[s] = (int)seq_rows(p, s).len;
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {
+        int place = s;
+        if (sort) {
+            place = 0;
+            for (int j = 0; j < p.n_seqs; ++j) place += len[j] > len[s] || (len[j] == len[s] && j < s);
+        }
+        order[place] = s;
+    }
+}
 
 template <int NF>
 __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
                                               const float floor_log) {
     constexpr int DK = 16 * NF, kTile = (DK + 63) / 64 * C * 64;
     // K and Q, and in their place, once they have been multiplied, A and its inverse
-    constexpr int kRows = 2 * kTile * (int)sizeof(bf16), kMat = C * (C + 1) * (int)sizeof(float);
+    constexpr int kRows = 2 * kTile * (int)sizeof(bf16), PA = C + 4, kMat = C * PA * (int)sizeof(float);
     __shared__ __align__(16) unsigned char room[kRows > kMat ? kRows : kMat];
     bf16 *const sK = reinterpret_cast<bf16 *>(room), *const sQ = sK + kTile;
-    float(*const sA)[C + 1] = reinterpret_cast<float(*)[C + 1]>(room);
+    float(*const sA)[PA] = reinterpret_cast<float(*)[PA]>(room);
     __shared__ double sG[C];
     __shared__ float sB[C];
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
-    if (blockIdx.x == 0 && tid == 0) *w.err = 0;
+    if (blockIdx.x == gridDim.x - 1) {  // one block more than chunks
+        if (tid == 0) *w.err = 0;
+        order_sequences(p, w.order, reinterpret_cast<int *>(room));
+        return;
+    }
     const SeqChunk ch = seq_chunk(p, c);
     if (ch.rows == 0) return;
     for (int i = tid; i < C * (DK / 8); i += 128) {
@@ -186,64 +208,55 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
 #pragma unroll
         for (int i = 0; i < 16; ++i) sA[o + i][o + col] = x[i];
     }
-    // T21 = -T22 (A21 T11), blocks of 16 then of 32.  A thread has 4 x W columns-rows of the product
+    // T21 = -T22 (A21 T11), blocks of 16 then of 32, four rows a thread
+    auto four = [&](int row, int col) { return *reinterpret_cast<const float4 *>(&sA[row][col]); };
     __syncthreads();
     {
-        const int pair = tid >> 6, e = tid & 63, o = 32 * pair, r = e / 16 * 4, col = e % 16;
-        float m[4] = {};
-        for (int k = 0; k < 16; ++k) {
-            const float b = sA[o + k][o + col];
+        const int pair = tid >> 6, e = tid & 63, o = 32 * pair, r = o + 16 + e / 16 * 4, col = o + e % 16;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = fmaf(sA[o + 16 + r + i][o + k], b, m[i]);
+        for (int pass = 0; pass < 2; ++pass) {  // A21 T11, then T22 times that
+            float m[4] = {};
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                const int from = o + 16 * pass + k;
+                const float b[4] = {sA[from][col], sA[from + 1][col], sA[from + 2][col], sA[from + 3][col]};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 a = four(r + i, from);
+                    m[i] = fmaf(a.x, b[0], fmaf(a.y, b[1], fmaf(a.z, b[2], fmaf(a.w, b[3], m[i]))));
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sA[r + i][col] = pass ? -m[i] : m[i];
+            __syncthreads();
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sA[o + 16 + r + i][o + col] = m[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = 0.f;
-        for (int k = 0; k < 16; ++k) {
-            const float b = sA[o + 16 + k][o + col];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = fmaf(-sA[o + 16 + r + i][o + 16 + k], b, m[i]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sA[o + 16 + r + i][o + col] = m[i];
     }
-    __syncthreads();
     {
-        const int r = tid / 16 * 4, col = tid % 16 * 2;
-        float m[4][2] = {};
-        for (int k = 0; k < 32; ++k) {
-            const float b0 = sA[k][col], b1 = sA[k][col + 1];
+        const int r = 32 + tid / 16 * 4, col = tid % 16 * 2;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = sA[32 + r + i][k];
-                m[i][0] = fmaf(a, b0, m[i][0]);
-                m[i][1] = fmaf(a, b1, m[i][1]);
+        for (int pass = 0; pass < 2; ++pass) {
+            float m[4][2] = {};
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                const int from = 32 * pass + k;
+                float2 b[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) b[x] = *reinterpret_cast<const float2 *>(&sA[from + x][col]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 a = four(r + i, from);
+                    m[i][0] = fmaf(a.x, b[0].x, fmaf(a.y, b[1].x, fmaf(a.z, b[2].x, fmaf(a.w, b[3].x, m[i][0]))));
+                    m[i][1] = fmaf(a.x, b[0].y, fmaf(a.y, b[1].y, fmaf(a.z, b[2].y, fmaf(a.w, b[3].y, m[i][1]))));
+                }
             }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float2 *>(&sA[r + i][col]) = pass ? make_float2(-m[i][0], -m[i][1]) : make_float2(m[i][0], m[i][1]);
+            __syncthreads();
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sA[32 + r + i][col] = m[i][0], sA[32 + r + i][col + 1] = m[i][1];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i][0] = m[i][1] = 0.f;
-        for (int k = 0; k < 32; ++k) {
-            const float b0 = sA[32 + k][col], b1 = sA[32 + k][col + 1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = -sA[32 + r + i][32 + k];
-                m[i][0] = fmaf(a, b0, m[i][0]);
-                m[i][1] = fmaf(a, b1, m[i][1]);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sA[32 + r + i][col] = m[i][0], sA[32 + r + i][col + 1] = m[i][1];
     }
-    __syncthreads();
     const int n = lane / 4, k2 = 2 * (lane & 3);
     for (int t = 2 * warp; t < 2 * warp + 2; ++t) {
         for (int b = 0; b <= t / 2; ++b) {
@@ -538,10 +551,10 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
     auto &sm = *reinterpret_cast<ChainSmem<NF, false> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const uint32_t aS = sm100::smem_u32(sm.S), aU = sm100::smem_u32(sm.U), aR = sm100::smem_u32(sm.R), aT = sm100::smem_u32(sm.T),
                    aP = sm100::smem_u32(sm.P);
-    const int groups = p.dv / NV, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
+    const int groups = p.dv / NV, s = w.order[blockIdx.x / (p.H * groups)], h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = warp_number();
     const SeqRange r = seq_range(p, s);
-    seq_report(p, r, blockIdx.x % (p.H * groups) == 0 && threadIdx.x == 0);
+    seq_report(p, r, h == 0 && c0 == 0 && threadIdx.x == 0);
     if (r.slot < 0) return;
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);
     const size_t soff = (((size_t)r.slot * p.H + h) * p.dv + c0) * DK;
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
     auto &sm = *reinterpret_cast<ChainSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const uint32_t aS = sm100::smem_u32(sm.S), aU = sm100::smem_u32(sm.U), aR = sm100::smem_u32(sm.R), aT = sm100::smem_u32(sm.T),
                    aP = sm100::smem_u32(sm.P);
-    const int groups = p.dv / NV, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
+    const int groups = p.dv / NV, s = w.order[blockIdx.x / (p.H * groups)], h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = warp_number();
     const SeqRange r = seq_rows(p, s);
     const size_t soff = (((size_t)s * p.H + h) * p.dv + c0) * DK;
@@ -971,10 +984,10 @@ __device__ __forceinline__ void walk_store(bf16 *dst, long long row_elems, const
 struct WalkPlace {
     int s, h, hk, c0, slice, slices;  // c0: the block's first column; slices: how many the block has
 };
-__device__ __forceinline__ WalkPlace walk_place(const SeqProblem &p) {
+__device__ __forceinline__ WalkPlace walk_place(const SeqProblem &p, const int *order) {
     const int groups = (p.dv + 16 * kSlices - 1) / (16 * kSlices);
     WalkPlace x;
-    x.s = blockIdx.x / (p.H * groups);
+    x.s = order[blockIdx.x / (p.H * groups)];
     x.h = blockIdx.x / groups % p.H;
     x.hk = x.h / (p.H / p.Hk);
     x.c0 = blockIdx.x % groups * 16 * kSlices;
@@ -994,7 +1007,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_const
     constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4;
     extern __shared__ unsigned char raw[];
     auto &sm = *reinterpret_cast<WalkSmem<NF, false> *>(raw + (-sm100::smem_u32(raw) & 1023));
-    const WalkPlace at = walk_place(p);
+    const WalkPlace at = walk_place(p, w.order);
     const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
     const SeqRange r = seq_range(p, at.s);
     seq_report(p, r, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
@@ -1162,7 +1175,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
     constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4;
     extern __shared__ unsigned char raw[];
     auto &sm = *reinterpret_cast<WalkSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
-    const WalkPlace at = walk_place(p);
+    const WalkPlace at = walk_place(p, w.order);
     const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
     const SeqRange r = seq_rows(p, at.s);
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, at.s, r.first);  // 0 of a bad range
@@ -1830,8 +1843,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
 }
 
 template <int NF> cudaError_t prep(const SeqProblem &p, const ChunkWork &w, float floor_log, cudaStream_t s) {
-    const unsigned blocks = (unsigned)(seq_max_chunks(p) * p.H);
-    if (blocks) k_prep<NF><<<blocks, 128, 0, s>>>(p, w, floor_log);
+    k_prep<NF><<<(unsigned)(seq_max_chunks(p) * p.H) + 1, 128, 0, s>>>(p, w, floor_log);
     return cudaGetLastError();
 }
 
@@ -1926,6 +1938,7 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
     w.T = (uint2 *)take(3 * frag);
     w.gates = (float *)take(n * 3 * C * 4);
     w.err = (int *)take(sizeof(int));
+    w.order = (int *)take((size_t)p.n_seqs * sizeof(int));
     if (!bwd) {
         w.P = (uint2 *)take(2 * frag);
     } else {
