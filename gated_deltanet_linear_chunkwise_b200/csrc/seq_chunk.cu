@@ -30,7 +30,8 @@
 
 namespace gdn {
 
-bool seq_row_map(CUtensorMap *m, const void *x, long long rows, long long row_stride, int heads, int d, int cols);  // gdn_tc.cu
+bool seq_row_map(CUtensorMap *m, const void *x, long long rows, long long row_stride, int heads, int d, int cols);
+bool seq_matrix_map(CUtensorMap *m, const float *x, long long rows, int cols, int box_rows);  // both gdn_tc.cu
 
 namespace {
 
@@ -1347,14 +1348,17 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
 //   dQ = dP K + e^G dO Sig^T,  dK = (beta dA) K + [dP; beta dA]^T [Q; K] - beta e^G dR Sig^T + e^{G_L-G} U D^T
 // Products that reach the gates' fp32 gradients are at fp32 accuracy (dP, dA, dO Sig^T: every term); those that only
 // reach the bf16 dQ and dK take two terms of each operand.
+// The fp32 matrices come by the copy engine (as the threads' loads they took most of the kernel's time), 64 columns a
+// line, and a warp turns a line of 256 bytes into its first two terms in place.
 struct GradMaps {
-    CUtensorMap q, k, v, o;
+    CUtensorMap q, k, v, o, Sig, D;
 };
-// Shared memory, sizes from dv: K, Q, dO rows | U, dR first two terms | U, dR third terms, dP and beta dA (before them
-// v's rows), M; in the place of the last, when they have been read, 64 columns of Sig and D.
+// Shared memory, sizes from dv: K, Q, dO rows | U, dR | U's and dR's third terms, dP and beta dA (before them Z), M (before
+// it v's rows), X where there is room; in the place of the third terms to M, when they have been read, 64 columns of Sig, of D
+// and Sig's third terms.
 template <int NF> struct GradLayout {
     static constexpr int kSlabs = (NF + 3) / 4, kTile = kSlabs * C * 128, kT = C * (16 * NF + 4) * 4, kPA = kT > 32768 ? kT : 32768;
-    int plane, K, Q, O, UR, last, PA, M, total;
+    int plane, K, Q, O, UR, last, PA, M, X, total;  // X: 0 where it would not fit
     __host__ __device__ explicit GradLayout(int dv) {
         plane = dv * 128;
         K = 0;
@@ -1364,7 +1368,12 @@ template <int NF> struct GradLayout {
         last = UR + 4 * plane;
         PA = last + 2 * plane;
         M = PA + kPA;
-        total = M + C * (C + 1) * 4;  // 5 planes of Sig and D fit behind `last`: 3 planes are at most 48 KB
+        X = M + C * (C + 1) * 4;  // 5 planes of Sig and D fit between `last` and X: 3 planes are at most 48 KB
+        total = X + 2 * plane;
+        if (total > 222 * 1024) {
+            total = X;
+            X = 0;
+        }
     }
 };
 
@@ -1373,9 +1382,9 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                                                         const __grid_constant__ GradMaps maps) {
     constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4, PM = C + 1;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(16) float gates[3][C], part_sums[8][3][C];  // read and written in pairs
+    __shared__ __align__(16) float gates[3][C];  // read in pairs
     __shared__ float into[C], past[C], db[C], sums[4][C], dg[C], red[8];
-    __shared__ uint64_t bar[1];
+    __shared__ uint64_t bar[2];
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
     const int mt = warp & 3, role = warp >> 2, dv = p.dv, nvf = dv / 16;
@@ -1387,23 +1396,28 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     const uint32_t base = sm100::smem_u32(sm), plane = at.plane;
     if (tid == 0) {
         sm100::mbar_init(&bar[0], 1);
+        sm100::mbar_init(&bar[1], 1);
         sm100::fence_barrier_init();
     }
     __syncthreads();
-    const float *Um = w.U + idx * dv * C, *Rm = w.dR + idx * dv * C, *Sm = w.Sig + idx * dv * DK, *Dm = w.D + idx * dv * DK;
+    const float *Um = w.U + idx * dv * C, *Rm = w.dR + idx * dv * C, *Xm = w.X + idx * dv * C, *Zm = w.Z + idx * dv * C;
     if (tid == 32) {  // into L2 for later
-        sm100::bulk_prefetch_l2(Sm, dv * DK * 4);
-        sm100::bulk_prefetch_l2(Dm, dv * DK * 4);
+        sm100::bulk_prefetch_l2(w.Sig + idx * dv * DK, dv * DK * 4);
+        sm100::bulk_prefetch_l2(w.D + idx * dv * DK, dv * DK * 4);
         sm100::bulk_prefetch_l2(w.gam + idx * kUnits * 32, kUnits * 32 * 16);
     }
     if (tid == 0) {
-        sm100::mbar_arrive_expect_tx(&bar[0], 2 * at.kTile + (dv + 63) / 64 * 2 * C * 128);
+        sm100::mbar_arrive_expect_tx(&bar[0], 2 * at.kTile + (dv + 63) / 64 * 2 * C * 128 + (at.X ? 8 : 6) * plane);
+        sm100::bulk_copy_g2s(sm + at.UR, Um, 2 * plane, &bar[0]);
+        sm100::bulk_copy_g2s(sm + at.UR + 2 * plane, Rm, 2 * plane, &bar[0]);
+        sm100::bulk_copy_g2s(sm + at.PA, Zm, 2 * plane, &bar[0]);
+        if (at.X) sm100::bulk_copy_g2s(sm + at.X, Xm, 2 * plane, &bar[0]);
         for (int x = 0; x < kSlabs; ++x) {
             sm100::tma_load_3d(sm + at.K + x * C * 128, &maps.k, &bar[0], 64 * x, hk, (int)ch.first);
             sm100::tma_load_3d(sm + at.Q + x * C * 128, &maps.q, &bar[0], 64 * x, hk, (int)ch.first);
         }
         for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.O + x * C * 128, &maps.o, &bar[0], 64 * x, h, (int)ch.first);
-        for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.PA + x * C * 128, &maps.v, &bar[0], 64 * x, h, (int)ch.first);
+        for (int x = 0; x < (dv + 63) / 64; ++x) sm100::tma_load_3d(sm + at.M + x * C * 128, &maps.v, &bar[0], 64 * x, h, (int)ch.first);
     }
     if (tid < 3 * C) gates[0][tid] = w.gates[idx * 3 * C + tid];
     const int i0 = 16 * mt + lane / 4, j0 = 2 * (lane & 3);  // this lane's rows i0, i0 + 8; its columns 8 t + j0, + 1
@@ -1416,34 +1430,34 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         zero_tail((bf16 *)(sm + at.K), kSlabs, 8, ch.rows);
         zero_tail((bf16 *)(sm + at.Q), kSlabs, 8, ch.rows);
         zero_tail((bf16 *)(sm + at.O), (dv + 63) / 64, 8, ch.rows);
-        zero_tail((bf16 *)(sm + at.PA), (dv + 63) / 64, 8, ch.rows);
+        zero_tail((bf16 *)(sm + at.M), (dv + 63) / 64, 8, ch.rows);
         __syncthreads();
     }
-    {  // U and dR as terms, and the sums over dv: past = U . Z, into = -beta dR . X (k's part), db = dR . (V - X).  A pair of
-       // tokens a lane, dv over the warps
+    // A warp's line n (64 columns, fp32) becomes its first two terms, and a third one of `third`'s lines where that is given.
+    auto line_terms = [&](uint32_t line, int n, float2 x, uint32_t third) {
+        uint32_t a[3];
+        split(x.x, x.y, a);
+        const uint32_t piece = ((lane >> 2 ^ (n & 7)) << 4) + (lane & 3) * 4;
+        sts(line + piece, a[0]);
+        sts(line + 128 + piece, a[1]);
+        if (third) sts(third + piece, a[2]);
+    };
+    {  // U and dR, and the sums over dv: past = U . Z, into = -beta dR . X (k's part), db = dR . (V - X).  A pair of tokens a lane
         const float2 be = *reinterpret_cast<const float2 *>(&gates[2][2 * lane]);
+        const float *Xs = at.X ? reinterpret_cast<const float *>(sm + at.X) : Xm;
         float s[3][2] = {};
-#pragma unroll 4
+#pragma unroll 2
         for (int n = warp; n < dv; n += 8) {
-            const size_t from = (size_t)n * C + 2 * lane;
-            const float2 u = *reinterpret_cast<const float2 *>(Um + from), r = *reinterpret_cast<const float2 *>(Rm + from),
-                         x = *reinterpret_cast<const float2 *>(w.X + idx * dv * C + from),
-                         z = *reinterpret_cast<const float2 *>(w.Z + idx * dv * C + from);
-            const uint32_t line = base + n * 128 + ((lane >> 2 ^ (n & 7)) << 4) + (lane & 3) * 4;
-            uint32_t a[3], b[3];
-            split(u.x, u.y, a);
-            split(r.x, r.y, b);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                sts(line + at.UR + i * plane, a[i]);
-                sts(line + at.UR + (2 + i) * plane, b[i]);
-            }
-            sts(line + at.last, a[2]);
-            sts(line + at.last + plane, b[2]);
+            const int from = n * C + 2 * lane;
+            const float2 u = *reinterpret_cast<const float2 *>(sm + at.UR + from * 4), r = *reinterpret_cast<const float2 *>(sm + at.UR + 2 * plane + from * 4),
+                         z = *reinterpret_cast<const float2 *>(sm + at.PA + from * 4), x = *reinterpret_cast<const float2 *>(Xs + from);
             float v[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                v[e] = __bfloat162float(*reinterpret_cast<const bf16 *>(sm + at.PA + sw_byte(C, 2 * lane + e, n) + (n & 7) * 2));
+                v[e] = __bfloat162float(*reinterpret_cast<const bf16 *>(sm + at.M + sw_byte(C, 2 * lane + e, n) + (n & 7) * 2));
+            __syncwarp();
+            line_terms(base + at.UR + n * 256, n, u, base + at.last + n * 128);
+            line_terms(base + at.UR + 2 * plane + n * 256, n, r, base + at.last + plane + n * 128);
             s[0][0] = fmaf(u.x, z.x, s[0][0]);
             s[0][1] = fmaf(u.y, z.y, s[0][1]);
             s[1][0] = fmaf(-be.x * r.x, x.x, s[1][0]);
@@ -1451,15 +1465,18 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             s[2][0] = fmaf(r.x, v[0] - x.x, s[2][0]);
             s[2][1] = fmaf(r.y, v[1] - x.y, s[2][1]);
         }
+        __syncthreads();  // the terms are there; Z and v have been read
+        float *sum = reinterpret_cast<float *>(sm + at.PA);  // [8][3][64]
 #pragma unroll
-        for (int i = 0; i < 3; ++i) *reinterpret_cast<float2 *>(&part_sums[warp][i][2 * lane]) = make_float2(s[i][0], s[i][1]);
-        __syncthreads();  // the terms are there, v has been read
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<float2 *>(sum + (warp * 3 + i) * C + 2 * lane) = make_float2(s[i][0], s[i][1]);
+        __syncthreads();
         if (tid < 3 * C) {
             float x = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x += part_sums[i][tid / C][tid % C];
+            for (int i = 0; i < 8; ++i) x += sum[i * 3 * C + tid];
             (tid < C ? past : tid < 2 * C ? into : db)[tid % C] = x;
         }
+        __syncthreads();
     }
     const uint32_t aK = base + at.K, aQ = base + at.Q, aO = base + at.O;
     // lane parts: an A operand from token rows; from [dv][64 tokens] lines; two n-tiles of a B operand from 64-column lines
@@ -1467,10 +1484,17 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     auto row_a = [&](uint32_t tile, int ks) {
         return tile + rows_at + (ks >> 2) * C * 128 + (((2 * (ks & 3) + (lane >> 4)) ^ (lane & 7)) << 4);
     };
-    const uint32_t lines_a = ((lane >> 4) * 8 + (lane & 7)) * 128 + (((2 * mt + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
-    uint32_t lines_b[4];
+    // lines of 128 bytes (a third term, dP and beta dA) and of 256 (two terms): a line's part, and the 16 bytes in it
+    const uint32_t row_l = (lane >> 4) * 8 + (lane & 7), piece_a = ((2 * mt + ((lane >> 3) & 1)) ^ (lane & 7)) << 4;
+    const uint32_t a128 = row_l * 128 + piece_a, a256 = row_l * 256 + piece_a;
+    const uint32_t row_b = ((lane >> 3) & 1) * 8 + (lane & 7);
+    uint32_t b128[4], b256[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) lines_b[g] = bt_lane(0, 16 * g, lane);
+    for (int g = 0; g < 4; ++g) {
+        const uint32_t piece = ((2 * g + (lane >> 4)) ^ (lane & 7)) << 4;
+        b128[g] = row_b * 128 + piece;
+        b256[g] = row_b * 256 + piece;
+    }
     auto pair = [&](int tile, int row, int col) {  // of a row of K or Q
         return *reinterpret_cast<const uint32_t *>(sm + tile + sw_byte(C, row, col) + (col & 7) * 2);
     };
@@ -1494,17 +1518,17 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             if (role == 0) {
                 ldsm4(a[0], row_a(aO, ks));
             } else {
-                ldsm4_t(a[0], u01 + 2 * plane + lines_a + ks * 2048);
-                ldsm4_t(a[1], u01 + 3 * plane + lines_a + ks * 2048);
-                ldsm4_t(a[2], u2 + plane + lines_a + ks * 2048);
+                ldsm4_t(a[0], u01 + 2 * plane + a256 + ks * 4096);
+                ldsm4_t(a[1], u01 + 2 * plane + a256 + ks * 4096 + 128);
+                ldsm4_t(a[2], u2 + plane + a128 + ks * 2048);
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 if (g > mt) break;
                 uint32_t b[3][4];
-                ldsm4_t(b[0], u01 + lines_b[g] + ks * 2048);
-                ldsm4_t(b[1], u01 + plane + lines_b[g] + ks * 2048);
-                ldsm4_t(b[2], u2 + lines_b[g] + ks * 2048);
+                ldsm4_t(b[0], u01 + b256[g] + ks * 4096);
+                ldsm4_t(b[1], u01 + b256[g] + ks * 4096 + 128);
+                ldsm4_t(b[2], u2 + b128[g] + ks * 2048);
 #pragma unroll
                 for (int x = 2; x >= 0; --x)
 #pragma unroll
@@ -1517,6 +1541,10 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                 }
             }
         }
+        float4 gam[8];  // on their way under the products that follow
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            gam[t] = t / 2 <= mt ? w.gam[(idx * kUnits + mt * (mt + 1) + t) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
         const uint32_t left = role ? aK : aQ;
 #pragma unroll 1
         for (int ks = 0; ks < NF; ++ks) {
@@ -1534,12 +1562,10 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         }
         float *M = reinterpret_cast<float *>(sm + at.M);
         const uint32_t aPA = base + at.PA + role * 2 * C * 128;
-        const float4 *gam = w.gam + (idx * kUnits + mt * (mt + 1)) * 32 + lane;
         const float be0 = role ? gates[2][i0] : 1.f, be1 = role ? gates[2][i0 + 8] : 1.f;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const float4 g4 = t / 2 <= mt ? gam[t * 32] : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float gm[4] = {g4.x, g4.y, g4.z, g4.w};
+            const float gm[4] = {gam[t].x, gam[t].y, gam[t].z, gam[t].w};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int i = i0 + 8 * half, j = 8 * t + j0;
@@ -1618,7 +1644,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         for (int t = 0; t < 2 * kMine; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-        const uint32_t pa = base + at.PA + lines_a;
+        const uint32_t pa = base + at.PA + a128;
 #pragma unroll 1
         for (int kb = mt; kb < 4; ++kb) {
             uint32_t a[4][4];
@@ -1686,6 +1712,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             s = quad(s);
             if ((tid & 3) == 0) dg[i] = s;
         }
+        sm100::fence_proxy_async_smem();
         __syncthreads();  // all that the state's columns take the place of has been read
     }
     // ---- through the states
@@ -1695,27 +1722,27 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         constexpr int kLast = NF % 4 ? NF % 4 : 4;
         constexpr int kFull = 4;
         const int groups = slab + 1 < kSlabs ? kFull : kLast;  // of 16 columns
-        // Sig's and D's columns as terms, and <D, Sig> over them
-        const int pieces = 4 * groups;  // of four columns a line
-#pragma unroll 4
-        for (int i = tid; i < dv * pieces; i += 256) {
-            const int n = i / pieces, c4 = i % pieces;
-            const float4 s = *reinterpret_cast<const float4 *>(Sm + (size_t)n * DK + 64 * slab + 4 * c4);
-            const float4 d = *reinterpret_cast<const float4 *>(Dm + (size_t)n * DK + 64 * slab + 4 * c4);
-            all = fmaf(s.x, d.x, fmaf(s.y, d.y, fmaf(s.z, d.z, fmaf(s.w, d.w, all))));
-            uint32_t a[3], b[3], e[2], f[2];
-            split(s.x, s.y, a);
-            split(s.z, s.w, b);
-            split(d.x, d.y, e);
-            split(d.z, d.w, f);
-            unsigned char *line = sm + at.last + n * 128 + ((c4 >> 1 ^ (n & 7)) << 4) + (c4 & 1) * 8;
-#pragma unroll
-            for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2 *>(line + x * plane) = make_uint2(a[x], b[x]);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) *reinterpret_cast<uint2 *>(line + (3 + x) * plane) = make_uint2(e[x], f[x]);
+        if (tid == 0) {
+            sm100::mbar_arrive_expect_tx(&bar[1], 4 * plane);
+            sm100::tma_load_2d(sm + at.last, &maps.Sig, &bar[1], 64 * slab, (int)(idx * dv));
+            sm100::tma_load_2d(sm + at.last + 2 * plane, &maps.D, &bar[1], 64 * slab, (int)(idx * dv));
+        }
+        if (!__syncthreads_and(sm100::mbar_wait(&bar[1], slab, w.err))) {
+            sm100::mbar_wait(&bar[1], slab, w.err, sm100::kWaitLimitNs, true);
+            if (p.status && tid == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
+            return;
+        }
+        const uint32_t s0 = base + at.last, d0 = s0 + 2 * plane, s2 = s0 + 4 * plane, u01 = base + at.UR;
+#pragma unroll 2
+        for (int n = warp; n < dv; n += 8) {  // their terms, and <D, Sig>
+            const float2 s = *reinterpret_cast<const float2 *>(sm + at.last + n * 256 + lane * 8),
+                         d = *reinterpret_cast<const float2 *>(sm + at.last + 2 * plane + n * 256 + lane * 8);
+            __syncwarp();
+            all = fmaf(s.x, d.x, fmaf(s.y, d.y, all));  // columns behind d_k are zeros
+            line_terms(s0 + n * 256, n, s, s2 + n * 128);
+            line_terms(d0 + n * 256, n, d, 0);
         }
         __syncthreads();
-        const uint32_t s0 = base + at.last, u01 = base + at.UR;
         float x[8][4], y[8][4];  // role 0: leading and small products; role 1: dR Sig^T and U D^T
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -1731,7 +1758,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                     if (g >= groups) break;
                     uint32_t b[3][4];
 #pragma unroll
-                    for (int n = 0; n < 3; ++n) ldsm4_t(b[n], s0 + n * plane + lines_b[g] + ks * 2048);
+                    for (int n = 0; n < 3; ++n) ldsm4_t(b[n], n < 2 ? s0 + b256[g] + ks * 4096 + n * 128 : s2 + b128[g] + ks * 2048);
 #pragma unroll
                     for (int n = 2; n >= 0; --n)
 #pragma unroll
@@ -1744,8 +1771,8 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                 uint32_t r[2][4], u[2][4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    ldsm4_t(u[n], u01 + n * plane + lines_a + ks * 2048);
-                    ldsm4_t(r[n], u01 + (2 + n) * plane + lines_a + ks * 2048);
+                    ldsm4_t(u[n], u01 + a256 + ks * 4096 + n * 128);
+                    ldsm4_t(r[n], u01 + 2 * plane + a256 + ks * 4096 + n * 128);
                 }
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -1753,8 +1780,8 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                     uint32_t b[2][4], d[2][4];
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        ldsm4_t(b[n], s0 + n * plane + lines_b[g] + ks * 2048);
-                        ldsm4_t(d[n], s0 + (3 + n) * plane + lines_b[g] + ks * 2048);
+                        ldsm4_t(b[n], s0 + b256[g] + ks * 4096 + n * 128);
+                        ldsm4_t(d[n], d0 + b256[g] + ks * 4096 + n * 128);
                     }
 #pragma unroll
                     for (int n = 2; n >= 0; --n)  // terms (0, 1), (1, 0), (0, 0)
@@ -1786,6 +1813,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                 }
             }
         }
+        sm100::fence_proxy_async_smem();
         __syncthreads();
     }
 #pragma unroll
@@ -1916,7 +1944,9 @@ template <int NF> cudaError_t bwd(const SeqProblem &p, const ChunkWork &w, cudaS
     g.q = m.q;
     g.k = m.k;
     if (!seq_row_map(&g.v, p.v, p.n_tokens, p.v_stride, p.H, p.dv, 64) ||
-        !seq_row_map(&g.o, p.d_o, p.n_tokens, (long long)p.H * p.dv, p.H, p.dv, 64))
+        !seq_row_map(&g.o, p.d_o, p.n_tokens, (long long)p.H * p.dv, p.H, p.dv, 64) ||
+        !seq_matrix_map(&g.Sig, w.Sig, seq_max_chunks(p) * p.H * p.dv, p.dk, p.dv) ||
+        !seq_matrix_map(&g.D, w.D, seq_max_chunks(p) * p.H * p.dv, p.dk, p.dv))
         return cudaErrorInvalidValue;
     const int bytes = GradLayout<NF>(p.dv).total + 1024;
     if (!e) e = cudaFuncSetAttribute(k_chunk_grads<NF>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
