@@ -1368,7 +1368,7 @@ template <int NF> struct GradLayout {
         last = UR + 4 * plane;
         PA = last + 2 * plane;
         M = PA + kPA;
-        X = M + C * (C + 1) * 4;  // 5 planes of Sig and D fit between `last` and X: 3 planes are at most 48 KB
+        X = M + C * (C + 4) * 4;  // 5 planes of Sig and D fit between `last` and X: 3 planes are at most 48 KB
         total = X + 2 * plane;
         if (total > 222 * 1024) {
             total = X;
@@ -1380,11 +1380,11 @@ template <int NF> struct GradLayout {
 template <int NF>
 __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ SeqProblem p, const __grid_constant__ ChunkWork w,
                                                         const __grid_constant__ GradMaps maps) {
-    constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4, PM = C + 1;
+    constexpr int DK = 16 * NF, kSlabs = (NF + 3) / 4, PM = C + 4;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(16) float gates[3][C];  // read in pairs
     __shared__ float into[C], past[C], db[C], sums[4][C], dg[C], red[8];
-    __shared__ uint64_t bar[2];
+    __shared__ uint64_t bar[4];
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
     const int mt = warp & 3, role = warp >> 2, dv = p.dv, nvf = dv / 16;
@@ -1395,8 +1395,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     unsigned char *const sm = raw + (-sm100::smem_u32(raw) & 1023);
     const uint32_t base = sm100::smem_u32(sm), plane = at.plane;
     if (tid == 0) {
-        sm100::mbar_init(&bar[0], 1);
-        sm100::mbar_init(&bar[1], 1);
+        for (int i = 0; i < 4; ++i) sm100::mbar_init(&bar[i], 1);
         sm100::fence_barrier_init();
     }
     __syncthreads();
@@ -1465,10 +1464,15 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             s[2][0] = fmaf(r.x, v[0] - x.x, s[2][0]);
             s[2][1] = fmaf(r.y, v[1] - x.y, s[2][1]);
         }
-        __syncthreads();  // the terms are there; Z and v have been read
+        sm100::fence_proxy_async_smem();
+        __syncthreads();  // the terms are there; X, Z and v have been read
         float *sum = reinterpret_cast<float *>(sm + at.PA);  // [8][3][64]
 #pragma unroll
         for (int i = 0; i < 3; ++i) *reinterpret_cast<float2 *>(sum + (warp * 3 + i) * C + 2 * lane) = make_float2(s[i][0], s[i][1]);
+        if (tid == 0 && at.X) {  // X has been read: the first columns of Sig take its place
+            sm100::mbar_arrive_expect_tx(&bar[1], 2 * plane);
+            sm100::tma_load_2d(sm + at.X, &maps.Sig, &bar[1], 0, (int)(idx * dv));
+        }
         __syncthreads();
         if (tid < 3 * C) {
             float x = 0.f;
@@ -1575,7 +1579,6 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                 for (int e = 0; e < 2; ++e) {
                     x[e] = gm[2 * half + e] * (hi[t][2 * half + e] + lo[t][2 * half + e]);
                     if (role) x[e] = j + e < i ? -x[e] : 0.f;
-                    if (role == 0) M[i * PM + j + e] = x[e] * kk[t][2 * half + e];  // role 1 adds its own behind the barrier
                 }
                 uint32_t s[2];
                 split(x[0], x[1], s);
@@ -1583,6 +1586,8 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                 for (int n = 0; n < 2; ++n) op[t / 2][n][half + 2 * (t & 1)] = s[n];
                 hi[t][2 * half] = be * x[0] * kk[t][2 * half];
                 hi[t][2 * half + 1] = be * x[1] * kk[t][2 * half + 1];
+                if (role == 0)  // role 1 adds its own behind the barrier
+                    *reinterpret_cast<float2 *>(&M[i * PM + j]) = make_float2(hi[t][2 * half], hi[t][2 * half + 1]);
                 if (role) split(be * x[0], be * x[1], s);
 #pragma unroll
                 for (int n = 0; n < 2; ++n) sts(aPA + n * C * 128 + sw_byte(0, i, 8 * t) + j0 * 2, s[n]);
@@ -1593,7 +1598,10 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
 #pragma unroll
             for (int t = 0; t < 8; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) M[(i0 + (e >> 1) * 8) * PM + 8 * t + j0 + (e & 1)] += hi[t][e];
+                for (int half = 0; half < 2; ++half) {
+                    float2 &m = *reinterpret_cast<float2 *>(&M[(i0 + 8 * half) * PM + 8 * t + j0]);
+                    m = make_float2(m.x + hi[t][2 * half], m.y + hi[t][2 * half + 1]);
+                }
         }
         // rows x K
         float part[2] = {};
@@ -1722,27 +1730,54 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         constexpr int kLast = NF % 4 ? NF % 4 : 4;
         constexpr int kFull = 4;
         const int groups = slab + 1 < kSlabs ? kFull : kLast;  // of 16 columns
+        // Places: Sig in X's and behind `last` + 2 planes in turn, D in `last` and then X's, so that the second columns come
+        // under the first ones' products; without X's place both wait for them.
+        const uint32_t where_s = !at.X ? at.last : slab ? at.last + 2 * plane : at.X, where_d = !at.X ? at.last + 2 * plane : slab ? at.X : at.last;
         if (tid == 0) {
-            sm100::mbar_arrive_expect_tx(&bar[1], 4 * plane);
-            sm100::tma_load_2d(sm + at.last, &maps.Sig, &bar[1], 64 * slab, (int)(idx * dv));
-            sm100::tma_load_2d(sm + at.last + 2 * plane, &maps.D, &bar[1], 64 * slab, (int)(idx * dv));
+            if (!at.X) {
+                sm100::mbar_arrive_expect_tx(&bar[1], 4 * plane);
+                sm100::tma_load_2d(sm + where_s, &maps.Sig, &bar[1], 64 * slab, (int)(idx * dv));
+                sm100::tma_load_2d(sm + where_d, &maps.D, &bar[1], 64 * slab, (int)(idx * dv));
+            } else {
+                sm100::mbar_arrive_expect_tx(&bar[2], 2 * plane);
+                sm100::tma_load_2d(sm + where_d, &maps.D, &bar[2], 64 * slab, (int)(idx * dv));
+                if (slab + 1 < kSlabs) {
+                    sm100::mbar_arrive_expect_tx(&bar[3], 2 * plane);
+                    sm100::tma_load_2d(sm + at.last + 2 * plane, &maps.Sig, &bar[3], 64, (int)(idx * dv));
+                }
+            }
         }
-        if (!__syncthreads_and(sm100::mbar_wait(&bar[1], slab, w.err))) {
-            sm100::mbar_wait(&bar[1], slab, w.err, sm100::kWaitLimitNs, true);
+        uint64_t *const bar_s = at.X && slab ? &bar[3] : &bar[1];
+        const uint32_t parity_s = at.X ? 0 : slab;
+        bool ok = sm100::mbar_wait(bar_s, parity_s, w.err);
+        const uint32_t s0 = base + where_s, d0 = base + where_d, s2 = base + at.last + 4 * plane, u01 = base + at.UR;
+        // their terms, a warp a line, and <D, Sig> (columns behind d_k are zeros)
+        float2 mine[16];  // this lane's columns of the warp's lines of Sig
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int n = warp + 8 * i;
+            if (n >= dv) break;
+            mine[i] = *reinterpret_cast<const float2 *>(sm + where_s + n * 256 + lane * 8);
+            __syncwarp();
+            line_terms(s0 + n * 256, n, mine[i], s2 + n * 128);
+        }
+        if (at.X) ok = sm100::mbar_wait(&bar[2], slab, w.err) && ok;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int n = warp + 8 * i;
+            if (n >= dv) break;
+            const float2 d = *reinterpret_cast<const float2 *>(sm + where_d + n * 256 + lane * 8);
+            __syncwarp();
+            all = fmaf(mine[i].x, d.x, fmaf(mine[i].y, d.y, all));
+            line_terms(d0 + n * 256, n, d, 0);
+        }
+        if (!__syncthreads_and(ok)) {  // what is on its way lands before the block's shared memory goes
+            sm100::mbar_wait(bar_s, parity_s, w.err, sm100::kWaitLimitNs, true);
+            if (at.X) sm100::mbar_wait(&bar[2], slab, w.err, sm100::kWaitLimitNs, true);
+            if (at.X && kSlabs > 1) sm100::mbar_wait(&bar[3], 0, w.err, sm100::kWaitLimitNs, true);
             if (p.status && tid == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
             return;
         }
-        const uint32_t s0 = base + at.last, d0 = s0 + 2 * plane, s2 = s0 + 4 * plane, u01 = base + at.UR;
-#pragma unroll 2
-        for (int n = warp; n < dv; n += 8) {  // their terms, and <D, Sig>
-            const float2 s = *reinterpret_cast<const float2 *>(sm + at.last + n * 256 + lane * 8),
-                         d = *reinterpret_cast<const float2 *>(sm + at.last + 2 * plane + n * 256 + lane * 8);
-            __syncwarp();
-            all = fmaf(s.x, d.x, fmaf(s.y, d.y, all));  // columns behind d_k are zeros
-            line_terms(s0 + n * 256, n, s, s2 + n * 128);
-            line_terms(d0 + n * 256, n, d, 0);
-        }
-        __syncthreads();
         float x[8][4], y[8][4];  // role 0: leading and small products; role 1: dR Sig^T and U D^T
 #pragma unroll
         for (int t = 0; t < 8; ++t)
