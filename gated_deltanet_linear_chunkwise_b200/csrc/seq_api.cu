@@ -134,12 +134,19 @@ int check(const gdn_seq_args &a, Which which, gdn::SeqProblem &p) {
     return GDN_OK;
 }
 
-// Which form serves a gdn_packed or gdn_bwd call: the tensor cores take bf16 operands.
-bool chunked(const gdn::SeqProblem &p) { return p.dtype == GDN_DTYPE_BF16 && p.n_tokens > 0; }
+// Which form serves a gdn_packed or gdn_bwd call.  The tensor cores take bf16 operands.  Few tokens for the states that
+// they pass through go token by token: about 0.36 us a token of the longest sequence, against 18 us and 2 us a sequence
+// of 140 slices (16 columns of a head's state) in chunks.  The longest sequence is not known on the host, so the rule
+// takes all tokens for one's.  Measured (20 heads, d = 112, us, recurrent / chunks): 1 sequence of 16 tokens 8.5 / 19, of 64
+// 25 / 18; 40 sequences with 128 tokens 31 / 91, with 400 54 / 92, with 800 95 / 92.
+bool chunked(const gdn::SeqProblem &p, Which which) {
+    if (p.dtype != GDN_DTYPE_BF16 || p.n_tokens == 0) return false;
+    return which == kBwd || p.n_tokens >= 50 + (long long)p.n_seqs * p.H * (p.dv / 16) / 20;
+}
 
 size_t workspace_for(const gdn::SeqProblem &p, Which which) {
     if (which == kDecode) return 0;
-    if (chunked(p)) return gdn::seq_chunk_workspace(p, which == kBwd);
+    if (chunked(p, which)) return gdn::seq_chunk_workspace(p, which == kBwd);
     return which == kBwd ? gdn::seq_bwd_workspace(p, nullptr, nullptr) : 0;
 }
 
@@ -171,8 +178,8 @@ int run(const gdn_seq_args *a, Which which) noexcept {
             }
         }
         cudaError_t e = cudaSuccess;
-        if (which == kBwd) e = chunked(p) ? gdn::launch_seq_bwd_chunk(p, ws, s) : gdn::launch_seq_bwd_simt(p, ws, s);
-        else if (p.n_seqs && which == kPacked && chunked(p)) e = gdn::launch_seq_chunk(p, ws, s);
+        if (which == kBwd) e = chunked(p, which) ? gdn::launch_seq_bwd_chunk(p, ws, s) : gdn::launch_seq_bwd_simt(p, ws, s);
+        else if (p.n_seqs && which == kPacked && chunked(p, which)) e = gdn::launch_seq_chunk(p, ws, s);
         else if (p.n_seqs) e = gdn::launch_seq_recurrent(p, which == kDecode, s);
         if (owned) {
             cudaError_t e2 = cudaFreeAsync(ws, s);

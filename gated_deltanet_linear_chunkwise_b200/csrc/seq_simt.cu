@@ -19,7 +19,7 @@
 //
 // Four kernels: prep (T, P, decays; every chunk by itself), the chain forwards (Sig, Y, U; 16 columns of
 // Sig a block, they are independent), the chain backwards (D, dR, dV, dS_in) and the gradients of
-// a chunk.  This file serves fp32 inputs; its bound is the fp32 pipe.
+// a chunk.  This file serves fp32 inputs (and calls without tokens); its bound is the fp32 pipe.
 #include <cuda_bf16.h>
 
 #include "gates.cuh"
@@ -32,17 +32,14 @@ constexpr int C = kSeqChunk;
 constexpr int LC = C + 1;  // row pitch of a 64 x 64 matrix in shared memory
 constexpr int NC = 16;     // columns of Sig that a chain block holds
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 // rows x cols values of a token-major tensor into dst [64][pitch], zeros behind the chunk's end
-template <typename T>
-__device__ __forceinline__ void load_rows(float *dst, int pitch, const T *src, long long stride, int rows, int cols) {
+__device__ __forceinline__ void load_rows(float *dst, int pitch, const float *src, long long stride, int rows, int cols) {
     for (int i = threadIdx.x; i < C * cols; i += blockDim.x) {
         const int r = i / cols, c = i % cols;
-        dst[r * pitch + c] = r < rows ? to_f(src[r * stride + c]) : 0.f;
+        dst[r * pitch + c] = r < rows ? src[r * stride + c] : 0.f;
     }
 }
 
@@ -62,7 +59,6 @@ __device__ __forceinline__ void mm44(float (&acc)[4][4], int K, FA a, FB b) {
     }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(256) k_prep(const __grid_constant__ SeqProblem p, const __grid_constant__ SeqWork w) {
     extern __shared__ float sm[];
     const long long c = blockIdx.x / p.H;
@@ -71,8 +67,8 @@ __global__ void __launch_bounds__(256) k_prep(const __grid_constant__ SeqProblem
     if (ch.rows == 0) return;
     float *sK = sm, *sQ = sK + C * pk, *sA = sQ + C * pk, *sT = sA + C * LC, *sBeta = sT + C * LC;
     double *sG = reinterpret_cast<double *>(sBeta + C);
-    load_rows(sK, pk, (const T *)p.k + ch.first * p.k_stride + (size_t)hk * p.dk, p.k_stride, ch.rows, p.dk);
-    load_rows(sQ, pk, (const T *)p.q + ch.first * p.q_stride + (size_t)hk * p.dk, p.q_stride, ch.rows, p.dk);
+    load_rows(sK, pk, (const float *)p.k + ch.first * p.k_stride + (size_t)hk * p.dk, p.k_stride, ch.rows, p.dk);
+    load_rows(sQ, pk, (const float *)p.q + ch.first * p.q_stride + (size_t)hk * p.dk, p.q_stride, ch.rows, p.dk);
     if (tid < C) {
         const bool on = tid < ch.rows;
         const size_t g = (size_t)(ch.first + tid) * p.H + h;
@@ -134,12 +130,11 @@ __device__ __forceinline__ ChainTile chain_tile(float *sm, int dk) {
 }
 size_t chain_bytes(int dk) { return sizeof(float) * (size_t)(2 * C * (dk + 1) + 2 * C * LC + NC * (dk + 1) + 3 * C * NC + 3 * C); }
 
-template <typename T>
 __device__ __forceinline__ void chain_load(const SeqProblem &p, const SeqWork &w, const ChainTile &t, long long row, int rows,
-                                           size_t idx, int h, int c0, const T *v, long long v_stride) {
+                                           size_t idx, int h, int c0, const float *v, long long v_stride) {
     const int hk = h / (p.H / p.Hk), pk = p.dk + 1;
-    load_rows(t.K, pk, (const T *)p.k + row * p.k_stride + (size_t)hk * p.dk, p.k_stride, rows, p.dk);
-    load_rows(t.Q, pk, (const T *)p.q + row * p.q_stride + (size_t)hk * p.dk, p.q_stride, rows, p.dk);
+    load_rows(t.K, pk, (const float *)p.k + row * p.k_stride + (size_t)hk * p.dk, p.k_stride, rows, p.dk);
+    load_rows(t.Q, pk, (const float *)p.q + row * p.q_stride + (size_t)hk * p.dk, p.q_stride, rows, p.dk);
     load_rows(t.V, NC, v + row * v_stride + (size_t)h * p.dv + c0, v_stride, rows, NC);
     for (int i = threadIdx.x; i < C * C; i += blockDim.x) {
         t.T[i / C * LC + i % C] = w.T[idx * C * C + i];
@@ -152,7 +147,6 @@ __device__ __forceinline__ void chain_load(const SeqProblem &p, const SeqWork &w
     }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(256) k_chain_fwd(const __grid_constant__ SeqProblem p, const __grid_constant__ SeqWork w) {
     extern __shared__ float sm[];
     const int groups = p.dv / NC, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NC;
@@ -169,7 +163,7 @@ __global__ void __launch_bounds__(256) k_chain_fwd(const __grid_constant__ SeqPr
         const size_t idx = (size_t)(base + c) * p.H + h;
         const long long row = r.first + c * C;
         __syncthreads();
-        chain_load(p, w, t, row, (int)min((long long)C, r.len - c * C), idx, h, c0, (const T *)p.v, p.v_stride);
+        chain_load(p, w, t, row, (int)min((long long)C, r.len - c * C), idx, h, c0, (const float *)p.v, p.v_stride);
         __syncthreads();
         for (int e = tid; e < NC * p.dk; e += blockDim.x) w.Sig[(idx * dv + c0) * p.dk + e] = t.S[e / p.dk * pk + e % p.dk];
         float x[4] = {};
@@ -200,7 +194,6 @@ __global__ void __launch_bounds__(256) k_chain_fwd(const __grid_constant__ SeqPr
     }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(256) k_chain_bwd(const __grid_constant__ SeqProblem p, const __grid_constant__ SeqWork w) {
     extern __shared__ float sm[];
     const int groups = p.dv / NC, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NC;
@@ -220,7 +213,7 @@ __global__ void __launch_bounds__(256) k_chain_bwd(const __grid_constant__ SeqPr
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
         __syncthreads();
-        chain_load(p, w, t, row, rows, idx, h, c0, (const T *)p.d_o, (long long)p.H * dv);
+        chain_load(p, w, t, row, rows, idx, h, c0, (const float *)p.d_o, (long long)p.H * dv);
         __syncthreads();
         for (int e = tid; e < NC * p.dk; e += blockDim.x) w.D[(idx * dv + c0) * p.dk + e] = t.S[e / p.dk * pk + e % p.dk];
         float x[4] = {};
@@ -239,7 +232,7 @@ __global__ void __launch_bounds__(256) k_chain_bwd(const __grid_constant__ SeqPr
             for (int j = 0; j < 4; ++j) y[j] = fmaf(t.T[m * LC + i], t.X[m * NC + j0 + j], y[j]);
         for (int j = 0; j < 4; ++j) {
             w.dR[(idx * C + i) * dv + c0 + j0 + j] = y[j];
-            if (i < rows) put((T *)p.dv_out + ((row + i) * p.H + h) * dv + c0 + j0 + j, t.beta[i] * y[j]);
+            if (i < rows) ((float *)p.dv_out)[((row + i) * p.H + h) * dv + c0 + j0 + j] = t.beta[i] * y[j];
             t.R[i * NC + j0 + j] = t.beta[i] * t.eg[i] * y[j];
             t.V[i * NC + j0 + j] *= t.eg[i];  // this thread's own entries; others read them only behind the barrier
         }
@@ -264,7 +257,7 @@ __device__ __forceinline__ float sum16(float x) {
 }
 
 struct GradTile {
-    float *K, *Q, *dO, *U, *dR, *P, *A, *eg, *el, *beta, *into, *past, *dg;
+    float *K, *Q, *dO, *U, *dR, *P, *A, *eg, *el, *beta, *into, *past, *red;
 };
 __device__ __forceinline__ GradTile grad_tile(float *sm, int dk, int dv) {
     GradTile t;
@@ -280,12 +273,11 @@ __device__ __forceinline__ GradTile grad_tile(float *sm, int dk, int dv) {
     t.beta = t.el + C;
     t.into = t.beta + C;
     t.past = t.into + C;
-    t.dg = t.past + C;
+    t.red = t.past + C;
     return t;
 }
-size_t grad_bytes(int dk, int dv) { return sizeof(float) * (size_t)(2 * C * dk + 3 * C * dv + 2 * C * LC + 6 * C + 8) + sizeof(double) * C; }
+size_t grad_bytes(int dk, int dv) { return sizeof(float) * (size_t)(2 * C * dk + 3 * C * dv + 2 * C * LC + 5 * C + 8) + sizeof(double) * C; }
 
-template <typename T>
 __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProblem p, const __grid_constant__ SeqWork w) {
     extern __shared__ float sm[];
     const long long c = blockIdx.x / p.H;
@@ -294,11 +286,10 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
     if (ch.rows == 0) return;
     const size_t idx = (size_t)c * p.H + h;
     const GradTile t = grad_tile(sm, dk, dv);
-    float *sRed = t.dg + C;                                  // [8]
-    double *sG = reinterpret_cast<double *>(sRed + 8);
-    load_rows(t.K, dk, (const T *)p.k + ch.first * p.k_stride + (size_t)hk * dk, p.k_stride, ch.rows, dk);
-    load_rows(t.Q, dk, (const T *)p.q + ch.first * p.q_stride + (size_t)hk * dk, p.q_stride, ch.rows, dk);
-    load_rows(t.dO, dv, (const T *)p.d_o + (ch.first * p.H + h) * dv, (long long)p.H * dv, ch.rows, dv);
+    double *sG = reinterpret_cast<double *>(t.red + 8);
+    load_rows(t.K, dk, (const float *)p.k + ch.first * p.k_stride + (size_t)hk * dk, p.k_stride, ch.rows, dk);
+    load_rows(t.Q, dk, (const float *)p.q + ch.first * p.q_stride + (size_t)hk * dk, p.q_stride, ch.rows, dk);
+    load_rows(t.dO, dv, (const float *)p.d_o + (ch.first * p.H + h) * dv, (long long)p.H * dv, ch.rows, dv);
     load_rows(t.U, dv, w.U + idx * C * dv, (long long)dv, C, dv);
     load_rows(t.dR, dv, w.dR + idx * C * dv, (long long)dv, C, dv);
     if (tid < C) {
@@ -367,8 +358,8 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
                         w.dqh[(g * p.H + h) * dk + col + b] = dq[a][b];
                         w.dkh[(g * p.H + h) * dk + col + b] = dkv;
                     } else {
-                        put((T *)p.dq + (g * p.H + h) * dk + col + b, dq[a][b]);
-                        put((T *)p.dk_out + (g * p.H + h) * dk + col + b, dkv);
+                        ((float *)p.dq)[(g * p.H + h) * dk + col + b] = dq[a][b];
+                        ((float *)p.dk_out)[(g * p.H + h) * dk + col + b] = dkv;
                     }
                 }
             }
@@ -379,7 +370,7 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
             db[a] += t.dR[(i0 + a) * dv + n] * w.Y[(idx * C + i0 + a) * dv + n];
     for (int e = tid; e < dk * dv; e += blockDim.x) all += Sig[e] * D[e];
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    if (tid % 32 == 0) sRed[tid / 32] = all;
+    if (tid % 32 == 0) t.red[tid / 32] = all;
     for (int a = 0; a < 4; ++a) {
         const float x = sum16(into[a]), y = sum16(past[a]), z = sum16(db[a]);
         if (cg == 0) {
@@ -397,7 +388,7 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
     __syncthreads();
     if (tid < ch.rows) {
         float g = 0.f;
-        for (int i = 0; i < 8; ++i) g += sRed[i];
+        for (int i = 0; i < 8; ++i) g += t.red[i];
         g *= t.eg[C - 1];
         for (int j = 0; j < tid; ++j) g += t.P[tid * LC + j] + t.past[j];
         for (int i = tid; i < C; ++i) g += t.into[i];
@@ -455,19 +446,19 @@ __global__ void __launch_bounds__(256) k_zero_rows(const __grid_constant__ SeqPr
     }
 }
 
-template <typename T> cudaError_t run(const SeqProblem &p, const SeqWork &w, cudaStream_t s) {
+cudaError_t run(const SeqProblem &p, const SeqWork &w, cudaStream_t s) {
     const unsigned chunks = (unsigned)(seq_max_chunks(p) * p.H), chains = (unsigned)(p.n_seqs * p.H * (p.dv / NC));
     const size_t prep = sizeof(float) * (size_t)(2 * C * (p.dk + 1) + 2 * C * LC + C) + sizeof(double) * C;
     const size_t chain = chain_bytes(p.dk), grad = grad_bytes(p.dk, p.dv);
     cudaError_t e;
-    if ((e = cudaFuncSetAttribute(k_prep<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep))) return e;
-    if ((e = cudaFuncSetAttribute(k_chain_fwd<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain))) return e;
-    if ((e = cudaFuncSetAttribute(k_chain_bwd<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain))) return e;
-    if ((e = cudaFuncSetAttribute(k_grads<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad))) return e;
-    if (chunks) k_prep<T><<<chunks, 256, prep, s>>>(p, w);
-    k_chain_fwd<T><<<chains, 256, chain, s>>>(p, w);
-    k_chain_bwd<T><<<chains, 256, chain, s>>>(p, w);
-    if (chunks) k_grads<T><<<chunks, 256, grad, s>>>(p, w);
+    if ((e = cudaFuncSetAttribute(k_prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep))) return e;
+    if ((e = cudaFuncSetAttribute(k_chain_fwd, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain))) return e;
+    if ((e = cudaFuncSetAttribute(k_chain_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chain))) return e;
+    if ((e = cudaFuncSetAttribute(k_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad))) return e;
+    if (chunks) k_prep<<<chunks, 256, prep, s>>>(p, w);
+    k_chain_fwd<<<chains, 256, chain, s>>>(p, w);
+    k_chain_bwd<<<chains, 256, chain, s>>>(p, w);
+    if (chunks) k_grads<<<chunks, 256, grad, s>>>(p, w);
     return cudaGetLastError();
 }
 
@@ -516,7 +507,7 @@ cudaError_t launch_seq_bwd_simt(const SeqProblem &p, void *ws, cudaStream_t s) {
     SeqWork w;
     seq_bwd_workspace(p, ws, &w);
     cudaError_t e = launch_seq_zero_rows(p, w.dqh, w.dkh, s);
-    if (e == cudaSuccess && p.n_seqs) e = p.dtype == GDN_DTYPE_BF16 ? run<__nv_bfloat16>(p, w, s) : run<float>(p, w, s);
+    if (e == cudaSuccess && p.n_seqs) e = run(p, w, s);
     return e == cudaSuccess ? launch_seq_share(p, w.dqh, w.dkh, s) : e;
 }
 

@@ -342,8 +342,8 @@ size_t gdn_workspace_bytes(int B, int H, long long T, int frame_len, int d_k, in
  * gave up and the outputs are not valid.
  *
  * Calls are asynchronous on `stream`, whose device must be the current one.
- * gdn_decode's and gdn_packed's results do not depend on how sequences are
- * batched, and no result depends on the order in which blocks run.
+ * The same call gives the same bits: no result depends on the order in which
+ * blocks run.  (The same sequence in another batch may take another kernel.)
  */
 enum { GDN_SEQ_BAD_SLOT = 1, GDN_SEQ_SAME_SLOT = 2, GDN_SEQ_BAD_ROWS = 4, GDN_SEQ_TIMEOUT = 8 };
 

@@ -260,6 +260,10 @@ PACKED = [
     ([129, 7, 256], 0, 0, 2, 2, 32, 64, "fp32", "slow"),
     ([33, 150], 2, 2, 4, 1, 128, 112, "fp32", "lit"),
     ([5] * 40, 0, 0, 2, 2, 48, 32, "bf16", "slow"),
+    # chains enough for a warp a slice of 16 columns (900 and more of them): blocks of four slices and of three
+    ([17] * 64, 0, 0, 4, 2, 48, 64, "bf16", "slow"),
+    ([64, 65, 1, 0, 130] * 13, 2, 3, 2, 1, 32, 112, "bf16", "slow"),
+    ([2, 40] * 32, 0, 0, 2, 2, 112, 112, "bf16", "lit"),
 ]
 
 
@@ -316,9 +320,10 @@ def test_packed_bad_ranges_and_slots():
     o = torch.full(v.shape, 7.0, dtype=v.dtype, device="cuda")
     _, S = g.gdn_packed(q, k, v, alpha, beta, cu, return_state=True, o=o, status=status)
     assert int(status) == binding.GDN_SEQ_BAD_ROWS
-    for s, (a, b) in {0: (0, 70), 3: (80, 100)}.items():
+    for s, (a, b) in {0: (0, 70), 3: (80, 100)}.items():  # alone a sequence may take another kernel: two TOL32 and a bf16 step
         o1, S1 = g.gdn_packed(*(t[None, a:b] for t in (q, k, v, alpha, beta)), return_state=True)
-        assert torch.equal(o[a:b], o1[0]) and torch.equal(S[s], S1[0])
+        close(o[a:b], o1[0], 2 * tol32(dk, 70) + 2.0 ** -8)
+        close(S[s], S1[0], 2 * tol32(dk, 70))
     assert (o[70:80] == 7).all() and (o[100:] == 7).all()
     # gradients: zeros where no good sequence is
     do = torch.randn_like(v)
@@ -341,6 +346,25 @@ def test_packed_bad_ranges_and_slots():
     o1, S1 = g.gdn_packed(*(t[None, :70] for t in (q, k, v, alpha, beta)), None, pool[1:2], return_state=True)
     assert torch.equal(o[:70], o1[0]) and torch.equal(S[1], S1[0]) and (o[70:] == 7).all()
     assert torch.equal(S[[0, 2]], pool[[0, 2]])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 75])
+def test_neighbours_do_not_mix(n):
+    """What is not finite in one sequence stays there: chunks end inside the tiles that hold the next one's rows."""
+    H, dk, dv, L = 2, 64, 112, 70
+    q, k, v, alpha, beta = cuda(*draw(n * L, H, H, dk, dv, "bf16", 71))
+    do = torch.randn_like(v)
+    cu = torch.arange(0, n * L + 1, L, dtype=torch.int32, device="cuda")
+    clean = [*g.gdn_packed(q, k, v, alpha, beta, cu, return_state=True), *g.gdn_bwd(q, k, v, alpha, beta, do, cu, need_dS_in=True)]
+    for t in (q, k, v, do):
+        t[L:2 * L] = float("nan")
+        t[2 * L - 1] = float("inf")
+    dirty = [*g.gdn_packed(q, k, v, alpha, beta, cu, return_state=True), *g.gdn_bwd(q, k, v, alpha, beta, do, cu, need_dS_in=True)]
+    for x, y in zip(clean, dirty):
+        one = L if x.shape[0] == n * L else 1
+        assert torch.equal(x[:one], y[:one]) and torch.equal(x[2 * one:], y[2 * one:])
+        assert not torch.isfinite(y[one:2 * one].double()).all()
 
 
 @pytest.mark.gpu
