@@ -1,26 +1,30 @@
 // seq_chunk.cu -- the chunked gated delta rule over packed sequences on the tensor cores (bf16 q, k, v).
 //
-// Notation and formulas as in seq_simt.cu; chunks of 64 tokens.  Three kernels:
+// Notation and formulas as in seq_simt.cu; chunks of 64 tokens.
 //
-// k_prep       every (chunk, head) by itself: T, P and the decays.
-// k_chunk_fwd  a block walks the chunks of one sequence and head with 16 columns of the state
-//              (d_v columns are independent), S = Sig^T's 16 rows in registers:
-//                X^T = S [K;Q]^T,  Y = V - e^G X_K,  U^T = (beta Y)^T T^T,
-//                O^T = e^G X_Q^T + U^T P^T,  S <- e^{G_L} S + (e^{G_L-G} U)^T K
-// k_chunk_bwd  the same walk backwards with 16 rows of D^T:
-//                dU^T = e^{G_L-G} D^T K^T + dO^T P,  dR^T = dU^T T,
-//                D^T <- e^{G_L} D^T + (e^G dO)^T Q - (beta e^G dR)^T K
+// k_prep         every (chunk, head) by itself: T, P and the decays.
+// k_chunk_fwd    a block walks the chunks of one sequence and head with 16 columns of the state
+//                (d_v columns are independent), S = Sig^T's 16 rows in registers:
+//                  X^T = S [K;Q]^T,  Y = V - e^G X_K,  U^T = (beta Y)^T T^T,
+//                  O^T = e^G X_Q^T + U^T P^T,  S <- e^{G_L} S + (e^{G_L-G} U)^T K
+// k_chunk_bwd    the same walk backwards with 16 rows of D^T:
+//                  dU^T = e^{G_L-G} D^T K^T + dO^T P,  dR^T = dU^T T,
+//                  D^T <- e^{G_L} D^T + (e^G dO)^T Q - (beta e^G dR)^T K
+// k_walk_fwd, k_walk_bwd   the same with a warp for each 16 columns, where there are many chains.
+// k_chunk_grads  every (chunk, head) by itself: dQ, dK and the gates' gradients.
 //
-// The state leaves in fp32 and has to be as exact as a fp32 recurrence, so its products are split ones
-// (seq_mma.cuh); what only reaches a bf16 output (Q S, P U) takes two terms.  Every operand on the state's
-// side has 16 rows and every other one is read as it lies (K, Q by ldmatrix; T and P are
-// stored by k_prep in the order in which a lane needs them, and go to registers directly).
+// gdn_packed runs the first and a forward walk, gdn_bwd all of them (its forward walk keeps what the others read).
 //
-// Why warp-level products and not tcgen05: with 16 rows of the state a block, one sequence
-// of 20 heads fills 140 of 148 SMs and its 64-token step is as short as it gets.  A tcgen05 product has 128 rows of
-// K and Q against N = 16 here and is bound by its A operand's shared memory reads (128 rows x 16 x 2 bytes at
-// 128 B/clk: 32 clk an instruction, as long as the 16 warp products that it replaces), and pays a
-// round trip through tensor memory for each of three dependent products of a step.
+// Precision.  The state leaves in fp32 and has to be as exact as a fp32 recurrence, so its products are split ones
+// (seq_mma.cuh); what only reaches a bf16 output (Q S, P U) takes two terms, whose 2^-17 vanish in its 2^-9.  With two
+// terms everywhere the state would be 3.7e-6 off (2-norm, a 64-bit model of the walk, 2048 tokens, d = 112), with three 2e-7.
+//
+// Why warp-level products and not tcgen05.  One sequence of 20 heads has 140 slices of 16 columns, one for nearly every SM, and its
+// 64-token step is as short as it gets.  A tcgen05 product has 128 rows of K and Q against N = 16 there and is bound by its A
+// operand's shared memory reads (128 x 16 x 2 bytes at 128 B/clk: 32 clk an instruction, as long as the 16 warp products
+// that it replaces); with all terms of S side by side (N = 48) it would be three times faster, but T's terms have to come as
+// full 64 x 64 operands then (76 KB a step and slice instead of 60), which is more than L2 gives 140 blocks at that rate, and
+// each of the step's three dependent products pays a round trip through tensor memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -59,10 +63,12 @@ struct ChunkWork {
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
     int *order;              // [n_seqs]: the sequences, the longest first
+    uint64_t wait_ns;        // limit of the bounded waits
+    int drop;                // debug: the first block's K is never fetched, so its wait gives up
 };
 
 // The chains' blocks start with the longest sequences: a long one that starts last runs alone (16384 tokens in 24
-// sequences of 44 to 1971: NNN us against NNN in their order).  A sequence's place is the number of longer ones, ties by index.
+// sequences of 44 to 1971: 421 us against 505 in their order).  A sequence's place is the number of longer ones, ties by index.
 __device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order, int *len) {  // len: room for 2048
     const bool sort = p.cu && p.n_seqs <= 2048;
     if (sort)
@@ -304,14 +310,17 @@ template <int NF, bool BWD> struct ChainSmem {
 };
 enum { kBarK = 0, kBarV = 2, kBarT = 3, kBarP = 4 };
 // Four warps carry the state from chunk to chunk, four more (where O is wanted) compute it beside them, one fetches.
+// Bound by its latency: 3900 clocks a step of 64 tokens at d = 112, of which 1300 are the products' and 1700 shared memory's (every warp
+// reads all of S's terms); one sequence of 8209 tokens, 20 heads: 342 us with k_prep.
 constexpr int chain_threads(bool with_o) { return with_o ? 288 : 160; }
 
 struct ChainMaps {
     CUtensorMap q, k, v;  // v: v, or do
 };
 
-// One thread's fetches (a handful of copies a chunk; as 16-byte copies by the threads they were 900 address lookups a
-// chunk in ldmatrix's way, and loads of T and P to registers made every ldmatrix wait for them: 6400 clocks a step).
+// One thread's fetches, a handful of copies a chunk.  (As 16-byte copies by the threads they were 900 address lookups a
+// chunk in ldmatrix's way, and loads of T and P to registers made every ldmatrix wait for them: 6400 clocks a step against
+// 3900.  A copy a row, 193 of them, takes 4000 clocks to issue.)
 template <int NF, bool BWD> struct ChainFetch {
     ChainSmem<NF, BWD> &sm;
     const ChainMaps &maps;
@@ -325,7 +334,7 @@ template <int NF, bool BWD> struct ChainFetch {
     __device__ __forceinline__ void k(int b, int row, size_t idx) const {  // and the gates
         uint64_t *bar = &sm.bar[kBarK + b];
         sm100::mbar_arrive_expect_tx(bar, kTileBytes + 3 * C * 4);
-        tile(sm.K[b], &maps.k, bar, row);
+        if (!w.drop || blockIdx.x) tile(sm.K[b], &maps.k, bar, row);
         sm100::bulk_copy_g2s(&sm.gates[b][0][0], w.gates + idx * 3 * C, 3 * C * 4, bar);
     }
     __device__ __forceinline__ void v(int row, bool with_q) const {  // 16 columns of v (or do); forwards with Q
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err, w.wait_ns) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err, w.wait_ns);
         // behind this barrier the state's terms are there and the last step's buffers have been read
         if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, SAVE ? -1 : (int)c - 1, w.err);
         if (fetcher) {
@@ -611,7 +620,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         if (warp >= 4) {  // O^T = e^G S Q^T + U^T P^T
             float qh[2][4], ql[2][4], oh[2][4], ol[2][2][4];
             state_times<NF, 2>(qh, ql, aS, sm100::smem_u32(sm.Q), t0, t1, lane);
-            ok = ok && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
+            ok = ok && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err, w.wait_ns);
             __syncthreads();
             __syncthreads();
             times_triangle<true, 2, 2>(oh, ol, sm100::smem_u32(sm.W), aP, t0, t1, lane);
@@ -656,7 +665,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
                             be.y * (__bfloat162float(sm.V[tok + 1][n]) - y));
             }
         }
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns);
         __syncthreads();
         // U^T = (beta Y)^T T^T
         float uh[2][4], ul[2][2][4];
@@ -731,8 +740,8 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err) &&
-             sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err, w.wait_ns) &&
+             sm100::mbar_wait(&sm.bar[kBarV], parity, w.err, w.wait_ns) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err, w.wait_ns);
         if (!__syncthreads_and(ok)) return chain_leave(sm, p, turn, (int)turn, w.err);
         if (fetcher && c > 0) fetch.k(b ^ 1, first_row(c - 1), index(c - 1));
         if (rows < C) {
@@ -774,7 +783,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
                             eg.y * __bfloat162float(sm.V[tok + 1][n]));
             }
         }
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns);
         __syncthreads();
         // dR^T = dU^T T
         float rh[2][4], rl[2][2][4];
@@ -818,7 +827,9 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
 // ---------------------------------------------------------------- a warp a slice
 // The same walks with a warp for each 16 columns and no exchange between warps: a product's result lies in a lane as
 // the next product's A operand does (rows n, pairs along k), so S, beta Y, U, dU and dR stay in registers from
-// product to product and shared memory holds only what all slices read: K, Q, T, P and v.  A block has up to four
+// product to product and shared memory holds only what all slices read: K, Q, T, P and v (a step and slice takes a quarter of
+// the shared memory reads of k_chunk_fwd).  16384 tokens in 24 sequences, 20 heads, d = 112: 299 us (37 GFLOP executed in 628 products
+// a step and slice, 40 % of the warp products' rate of 1024 multiply-adds a clock and SM), against 492 us.  A block has up to four
 // slices of one sequence and head; one of its threads fetches.
 constexpr int kSlices = 4;
 constexpr int kWalkThreads = 32 * kSlices;  // eight warps an SM, two blocks, leave a thread its 255 registers
@@ -845,7 +856,7 @@ template <int NF, bool BWD> struct WalkFetch {
     __device__ __forceinline__ void k(int b, int row, size_t idx) const {  // and the gates
         uint64_t *bar = &sm.bar[kBarK + b];
         sm100::mbar_arrive_expect_tx(bar, kTileBytes + 3 * C * 4);
-        tile(sm.K[b], &maps.k, bar, row);
+        if (!w.drop || blockIdx.x) tile(sm.K[b], &maps.k, bar, row);
         sm100::bulk_copy_g2s(&sm.gates[b][0][0], w.gates + idx * 3 * C, 3 * C * 4, bar);
     }
     __device__ __forceinline__ void t(const uint2 *src) const {
@@ -1050,10 +1061,10 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_const
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) &&
-             sm100::mbar_wait(&sm.bar[kBarT], parity, w.err) && (SAVE || sm100::mbar_wait(&sm.bar[kBarP], parity, w.err));
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err, w.wait_ns) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err, w.wait_ns) &&
+             sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns) && (SAVE || sm100::mbar_wait(&sm.bar[kBarP], parity, w.err, w.wait_ns));
         if (!__syncthreads_and(ok)) {
-            const int last[5] = {(int)((c + (c & 1)) >> 1), c ? (int)((c - !(c & 1)) >> 1) : -1, (int)c, (int)c, SAVE ? -1 : (int)c};
+            const int last[5] = {(int)((c - (c & 1)) >> 1), c ? (int)((c - !(c & 1)) >> 1) : -1, (int)c, (int)c, SAVE ? -1 : (int)c};
             return walk_leave(sm, p, last, w.err);
         }
         if (fetcher && c + 1 < n_chunks) fetch.k(b ^ 1, first_row(c + 1), index(c + 1));
@@ -1217,10 +1228,10 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
         const size_t idx = index(c);
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err) &&
-             sm100::mbar_wait(&sm.bar[kBarT], parity, w.err) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err);
+        ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err, w.wait_ns) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err, w.wait_ns) &&
+             sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err, w.wait_ns);
         if (!__syncthreads_and(ok)) {
-            const int i = (int)turn, last[5] = {(i + (i & 1)) >> 1, i ? (i - !(i & 1)) >> 1 : -1, i, i, i};
+            const int i = (int)turn, last[5] = {(i - (i & 1)) >> 1, i ? (i - !(i & 1)) >> 1 : -1, i, i, i};
             return walk_leave(sm, p, last, w.err);
         }
         if (fetcher && c > 0) fetch.k(b ^ 1, first_row(c - 1), index(c - 1));
@@ -1420,7 +1431,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     }
     if (tid < 3 * C) gates[0][tid] = w.gates[idx * 3 * C + tid];
     const int i0 = 16 * mt + lane / 4, j0 = 2 * (lane & 3);  // this lane's rows i0, i0 + 8; its columns 8 t + j0, + 1
-    if (!__syncthreads_and(sm100::mbar_wait(&bar[0], 0, w.err))) {
+    if (!__syncthreads_and(sm100::mbar_wait(&bar[0], 0, w.err, w.wait_ns))) {
         sm100::mbar_wait(&bar[0], 0, w.err, sm100::kWaitLimitNs, true);
         if (p.status && tid == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
         return;
@@ -1749,7 +1760,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         }
         uint64_t *const bar_s = at.X && slab ? &bar[3] : &bar[1];
         const uint32_t parity_s = at.X ? 0 : slab;
-        bool ok = sm100::mbar_wait(bar_s, parity_s, w.err);
+        bool ok = sm100::mbar_wait(bar_s, parity_s, w.err, w.wait_ns);
         const uint32_t s0 = base + where_s, d0 = base + where_d, s2 = base + at.last + 4 * plane, u01 = base + at.UR;
         // their terms, a warp a line, and <D, Sig> (columns behind d_k are zeros)
         float2 mine[16];  // this lane's columns of the warp's lines of Sig
@@ -1761,7 +1772,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             __syncwarp();
             line_terms(s0 + n * 256, n, mine[i], s2 + n * 128);
         }
-        if (at.X) ok = sm100::mbar_wait(&bar[2], slab, w.err) && ok;
+        if (at.X) ok = sm100::mbar_wait(&bar[2], slab, w.err, w.wait_ns) && ok;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int n = warp + 8 * i;
@@ -2000,6 +2011,8 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
     };
     const size_t frag = n * kUnits * 32 * sizeof(uint2);  // a term of T or P
     ChunkWork w = {};
+    w.wait_ns = wait_limit_ns();
+    w.drop = debug_drop_signal();
     w.T = (uint2 *)take(3 * frag);
     w.gates = (float *)take(n * 3 * C * 4);
     w.err = (int *)take(sizeof(int));

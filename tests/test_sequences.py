@@ -167,6 +167,8 @@ DECODE = [
     (2, 8, 4, 1, 32, 128, "fp32", "slow"),
     (70, 1, 3, 3, 96, 80, "fp32", "lit"),
     (1, 33, 1, 1, 64, 112, "bf16", "slow"),
+    (75, 2, 20, 10, 32, 48, "bf16", "slow"),  # a block a head
+    (1, 0, 2, 2, 32, 32, "bf16", "slow"),     # no token: the states stay
 ]
 
 
@@ -177,7 +179,7 @@ def test_decode(B, n, H, Hk, dk, dv, dtype, gates):
     pool = torch.randn(B + 3, H, dv, dk, generator=torch.Generator().manual_seed(1))
     slots = torch.randperm(B + 3, generator=torch.Generator().manual_seed(2))[:B].int()
     rows, states = token_loop(q.double(), k.double(), v.double(), alpha.double(), beta.double(),
-                              pool.double()[slots.long()], [n] * B, range(0, B * n, n))
+                              pool.double()[slots.long()], [n] * B, [n * i for i in range(B)])
     want = pool.double()
     want[slots.long()] = torch.stack(states)
     S = pool.cuda()
@@ -185,7 +187,8 @@ def test_decode(B, n, H, Hk, dk, dv, dtype, gates):
     args = [t.cuda().reshape(B, n, *t.shape[1:]) for t in (q, k, v, alpha, beta)]
     o, S2 = g.gdn_decode(*args, S, slots.cuda(), status=status)
     assert S2 is S and int(status) == 0
-    close(o.reshape(B * n, H, dv), torch.stack([rows[t] for t in range(B * n)]), tol32(dk, n), "o")
+    if n:
+        close(o.reshape(B * n, H, dv), torch.stack([rows[t] for t in range(B * n)]), tol32(dk, n), "o")
     close(S, want, tol32(dk, n), "S")
     if n == 1:  # the n dimension left out; no slots: state b is sequence b's
         S3 = pool[slots.long()].cuda()
@@ -260,6 +263,7 @@ PACKED = [
     ([129, 7, 256], 0, 0, 2, 2, 32, 64, "fp32", "slow"),
     ([33, 150], 2, 2, 4, 1, 128, 112, "fp32", "lit"),
     ([5] * 40, 0, 0, 2, 2, 48, 32, "bf16", "slow"),
+    ([3, 0, 9, 20], 1, 1, 4, 2, 112, 48, "bf16", "lit"),   # few tokens: token by token
     # chains enough for a warp a slice of 16 columns (900 and more of them): blocks of four slices and of three
     ([17] * 64, 0, 0, 4, 2, 48, 64, "bf16", "slow"),
     ([64, 65, 1, 0, 130] * 13, 2, 3, 2, 1, 32, 112, "bf16", "slow"),
@@ -560,3 +564,29 @@ def test_same_bits_again():
     one, two = ([*g.gdn_packed(q, k, v, alpha, beta, cu, return_state=True), *g.gdn_bwd(q, k, v, alpha, beta, do, cu, need_dS_in=True)] for _ in range(2))
     for x, y in zip(one, two):
         assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seqs", [2, 75])  # four warps a slice, and one
+def test_a_wait_that_gives_up(seqs, monkeypatch):
+    """The first block's keys are never fetched: its wait runs out, the status says so, and the next call is right."""
+    H, L, d, dv = 4, 70, 64, 48
+    q, k, v, alpha, beta = [t.cuda().reshape(seqs, L, *t.shape[1:]) for t in draw(seqs * L, H, H, d, dv, "bf16", 81)]
+    do = torch.randn_like(v)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def both():
+        return [*g.gdn_packed(q, k, v, alpha, beta, return_state=True, status=status), *g.gdn_bwd(q, k, v, alpha, beta, do)]
+
+    want = both()
+    assert int(status) == 0
+    monkeypatch.setenv("GDN_DEBUG_DROP_SIGNAL", "1")
+    monkeypatch.setenv("GDN_DEBUG_WAIT_LIMIT_US", "1000")
+    g.gdn_packed(q, k, v, alpha, beta, status=status)
+    assert int(status) == binding.GDN_SEQ_TIMEOUT
+    g.gdn_bwd(q, k, v, alpha, beta, do, status=status)
+    assert int(status) == binding.GDN_SEQ_TIMEOUT
+    monkeypatch.undo()
+    for x, y in zip(both()[:7], want):
+        assert torch.equal(x, y)
+    assert int(status) == 0
