@@ -29,17 +29,33 @@ namespace gdn {
 namespace {
 
 constexpr int C = kSeqChunk;
-constexpr int LC = C + 1;  // row pitch of a 64 x 64 matrix in shared memory
+constexpr int LC = C + 4;  // row pitch of a 64 x 64 matrix in shared memory
 constexpr int NC = 16;     // columns of Sig that a chain block holds
 
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 // rows x cols values of a token-major tensor into dst [64][pitch], zeros behind the chunk's end
+// (cols a multiple of 4, rows 16-byte aligned), four pieces a thread on their way together.
 __device__ __forceinline__ void load_rows(float *dst, int pitch, const float *src, long long stride, int rows, int cols) {
-    for (int i = threadIdx.x; i < C * cols; i += blockDim.x) {
-        const int r = i / cols, c = i % cols;
-        dst[r * pitch + c] = r < rows ? src[r * stride + c] : 0.f;
+    const int pieces = cols / 4;
+    for (int i0 = threadIdx.x; i0 < C * pieces; i0 += 4 * blockDim.x) {
+        float4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * blockDim.x, r = i / pieces, c = i % pieces * 4;
+            x[k] = i < C * pieces && r < rows ? *reinterpret_cast<const float4 *>(src + r * stride + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * blockDim.x, r = i / pieces, c = i % pieces * 4;
+            if (i >= C * pieces) break;
+            float *to = dst + r * pitch + c;  // odd pitches: rows spread over the banks
+            to[0] = x[k].x;
+            to[1] = x[k].y;
+            to[2] = x[k].z;
+            to[3] = x[k].w;
+        }
     }
 }
 
@@ -98,10 +114,17 @@ __global__ void __launch_bounds__(256) k_prep(const __grid_constant__ SeqProblem
     __syncthreads();
     // column tid of T by forward substitution
     if (tid < C) {
+        for (int i = 0; i < C; ++i) sT[i * LC + tid] = 0.f;
         for (int i = 0; i < C; ++i) {
-            float x = i == tid ? 1.f : 0.f;
-            for (int j = tid; j < i; ++j) x = fmaf(-sA[i * LC + j], sT[j * LC + tid], x);
-            sT[i * LC + tid] = i < tid ? 0.f : x;
+            float x[4] = {i == tid ? 1.f : 0.f, 0.f, 0.f, 0.f};  // rows above the diagonal are zeros: whole fours
+            for (int j = tid & ~3; j < i; j += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(&sA[i * LC + j]);  // zeros from column i on
+                x[0] = fmaf(-a.x, sT[j * LC + tid], x[0]);
+                x[1] = fmaf(-a.y, sT[(j + 1) * LC + tid], x[1]);
+                x[2] = fmaf(-a.z, sT[(j + 2) * LC + tid], x[2]);
+                x[3] = fmaf(-a.w, sT[(j + 3) * LC + tid], x[3]);
+            }
+            sT[i * LC + tid] = i < tid ? 0.f : (x[0] + x[1]) + (x[2] + x[3]);
         }
     }
     __syncthreads();
@@ -131,15 +154,13 @@ __device__ __forceinline__ ChainTile chain_tile(float *sm, int dk) {
 size_t chain_bytes(int dk) { return sizeof(float) * (size_t)(2 * C * (dk + 1) + 2 * C * LC + NC * (dk + 1) + 3 * C * NC + 3 * C); }
 
 __device__ __forceinline__ void chain_load(const SeqProblem &p, const SeqWork &w, const ChainTile &t, long long row, int rows,
-                                           size_t idx, int h, int c0, const float *v, long long v_stride) {
+                                           size_t idx, int h, int c0, bool with_qp, const float *v, long long v_stride) {
     const int hk = h / (p.H / p.Hk), pk = p.dk + 1;
     load_rows(t.K, pk, (const float *)p.k + row * p.k_stride + (size_t)hk * p.dk, p.k_stride, rows, p.dk);
-    load_rows(t.Q, pk, (const float *)p.q + row * p.q_stride + (size_t)hk * p.dk, p.q_stride, rows, p.dk);
+    if (with_qp) load_rows(t.Q, pk, (const float *)p.q + row * p.q_stride + (size_t)hk * p.dk, p.q_stride, rows, p.dk);
     load_rows(t.V, NC, v + row * v_stride + (size_t)h * p.dv + c0, v_stride, rows, NC);
-    for (int i = threadIdx.x; i < C * C; i += blockDim.x) {
-        t.T[i / C * LC + i % C] = w.T[idx * C * C + i];
-        t.P[i / C * LC + i % C] = w.P[idx * C * C + i];
-    }
+    load_rows(t.T, LC, w.T + idx * C * C, C, C, C);
+    if (with_qp) load_rows(t.P, LC, w.P + idx * C * C, C, C, C);
     if (threadIdx.x < C) {
         t.eg[threadIdx.x] = w.eg[idx * C + threadIdx.x];
         t.el[threadIdx.x] = w.el[idx * C + threadIdx.x];
@@ -163,7 +184,7 @@ __global__ void __launch_bounds__(256) k_chain_fwd(const __grid_constant__ SeqPr
         const size_t idx = (size_t)(base + c) * p.H + h;
         const long long row = r.first + c * C;
         __syncthreads();
-        chain_load(p, w, t, row, (int)min((long long)C, r.len - c * C), idx, h, c0, (const float *)p.v, p.v_stride);
+        chain_load(p, w, t, row, (int)min((long long)C, r.len - c * C), idx, h, c0, false, (const float *)p.v, p.v_stride);
         __syncthreads();
         for (int e = tid; e < NC * p.dk; e += blockDim.x) w.Sig[(idx * dv + c0) * p.dk + e] = t.S[e / p.dk * pk + e % p.dk];
         float x[4] = {};
@@ -213,7 +234,7 @@ __global__ void __launch_bounds__(256) k_chain_bwd(const __grid_constant__ SeqPr
         const long long row = r.first + c * C;
         const int rows = (int)min((long long)C, r.len - c * C);
         __syncthreads();
-        chain_load(p, w, t, row, rows, idx, h, c0, (const float *)p.d_o, (long long)p.H * dv);
+        chain_load(p, w, t, row, rows, idx, h, c0, true, (const float *)p.d_o, (long long)p.H * dv);
         __syncthreads();
         for (int e = tid; e < NC * p.dk; e += blockDim.x) w.D[(idx * dv + c0) * p.dk + e] = t.S[e / p.dk * pk + e % p.dk];
         float x[4] = {};
@@ -262,11 +283,11 @@ struct GradTile {
 __device__ __forceinline__ GradTile grad_tile(float *sm, int dk, int dv) {
     GradTile t;
     t.K = sm;
-    t.Q = t.K + C * dk;
-    t.dO = t.Q + C * dk;
-    t.U = t.dO + C * dv;
-    t.dR = t.U + C * dv;
-    t.P = t.dR + C * dv;
+    t.Q = t.K + C * (dk + 1);
+    t.dO = t.Q + C * (dk + 1);
+    t.U = t.dO + C * (dv + 1);
+    t.dR = t.U + C * (dv + 1);
+    t.P = t.dR + C * (dv + 1);
     t.A = t.P + C * LC;
     t.eg = t.A + C * LC;
     t.el = t.eg + C;
@@ -276,22 +297,22 @@ __device__ __forceinline__ GradTile grad_tile(float *sm, int dk, int dv) {
     t.red = t.past + C;
     return t;
 }
-size_t grad_bytes(int dk, int dv) { return sizeof(float) * (size_t)(2 * C * dk + 3 * C * dv + 2 * C * LC + 5 * C + 8) + sizeof(double) * C; }
+size_t grad_bytes(int dk, int dv) { return sizeof(float) * (size_t)(2 * C * (dk + 1) + 3 * C * (dv + 1) + 2 * C * LC + 5 * C + 8) + sizeof(double) * C; }
 
 __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProblem p, const __grid_constant__ SeqWork w) {
     extern __shared__ float sm[];
     const long long c = blockIdx.x / p.H;
-    const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, dk = p.dk, dv = p.dv;
+    const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, dk = p.dk, dv = p.dv, pk = dk + 1, pv = dv + 1;
     const SeqChunk ch = seq_chunk(p, c);
     if (ch.rows == 0) return;
     const size_t idx = (size_t)c * p.H + h;
     const GradTile t = grad_tile(sm, dk, dv);
     double *sG = reinterpret_cast<double *>(t.red + 8);
-    load_rows(t.K, dk, (const float *)p.k + ch.first * p.k_stride + (size_t)hk * dk, p.k_stride, ch.rows, dk);
-    load_rows(t.Q, dk, (const float *)p.q + ch.first * p.q_stride + (size_t)hk * dk, p.q_stride, ch.rows, dk);
-    load_rows(t.dO, dv, (const float *)p.d_o + (ch.first * p.H + h) * dv, (long long)p.H * dv, ch.rows, dv);
-    load_rows(t.U, dv, w.U + idx * C * dv, (long long)dv, C, dv);
-    load_rows(t.dR, dv, w.dR + idx * C * dv, (long long)dv, C, dv);
+    load_rows(t.K, pk, (const float *)p.k + ch.first * p.k_stride + (size_t)hk * dk, p.k_stride, ch.rows, dk);
+    load_rows(t.Q, pk, (const float *)p.q + ch.first * p.q_stride + (size_t)hk * dk, p.q_stride, ch.rows, dk);
+    load_rows(t.dO, pv, (const float *)p.d_o + (ch.first * p.H + h) * dv, (long long)p.H * dv, ch.rows, dv);
+    load_rows(t.U, pv, w.U + idx * C * dv, (long long)dv, C, dv);
+    load_rows(t.dR, pv, w.dR + idx * C * dv, (long long)dv, C, dv);
     if (tid < C) {
         const bool on = tid < ch.rows;
         const size_t g = (size_t)(ch.first + tid) * p.H + h;
@@ -308,10 +329,10 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
     float M[4][4] = {};
     {
         float qk[4][4] = {}, kk[4][4] = {}, dP[4][4] = {}, dA[4][4] = {};
-        mm44(qk, dk, [&](int i, int k) { return t.Q[(i0 + i) * dk + k]; }, [&](int k, int j) { return t.K[(j0 + j) * dk + k]; });
-        mm44(kk, dk, [&](int i, int k) { return t.K[(i0 + i) * dk + k]; }, [&](int k, int j) { return t.K[(j0 + j) * dk + k]; });
-        mm44(dP, dv, [&](int i, int k) { return t.dO[(i0 + i) * dv + k]; }, [&](int k, int j) { return t.U[(j0 + j) * dv + k]; });
-        mm44(dA, dv, [&](int i, int k) { return t.dR[(i0 + i) * dv + k]; }, [&](int k, int j) { return t.U[(j0 + j) * dv + k]; });
+        mm44(qk, dk, [&](int i, int k) { return t.Q[(i0 + i) * pk + k]; }, [&](int k, int j) { return t.K[(j0 + j) * pk + k]; });
+        mm44(kk, dk, [&](int i, int k) { return t.K[(i0 + i) * pk + k]; }, [&](int k, int j) { return t.K[(j0 + j) * pk + k]; });
+        mm44(dP, dv, [&](int i, int k) { return t.dO[(i0 + i) * pv + k]; }, [&](int k, int j) { return t.U[(j0 + j) * pv + k]; });
+        mm44(dA, dv, [&](int i, int k) { return t.dR[(i0 + i) * pv + k]; }, [&](int k, int j) { return t.U[(j0 + j) * pv + k]; });
         for (int a = 0; a < 4; ++a)
             for (int b = 0; b < 4; ++b) {
                 const int i = i0 + a, j = j0 + b;
@@ -330,28 +351,28 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
         const bool on = col < dk;  // dk is a multiple of 16: a thread's four columns are all in or all out
         float dq[4][4] = {}, kin[4][4] = {}, kout[4][4] = {}, kA[4][4] = {}, kT[4][4] = {};
         if (on) {
-            mm44(dq, dv, [&](int i, int k) { return t.dO[(i0 + i) * dv + k]; }, [&](int k, int j) { return Sig[(size_t)k * dk + col + j]; });
-            mm44(kin, dv, [&](int i, int k) { return t.dR[(i0 + i) * dv + k]; }, [&](int k, int j) { return Sig[(size_t)k * dk + col + j]; });
-            mm44(kout, dv, [&](int i, int k) { return t.U[(i0 + i) * dv + k]; }, [&](int k, int j) { return D[(size_t)k * dk + col + j]; });
+            mm44(dq, dv, [&](int i, int k) { return t.dO[(i0 + i) * pv + k]; }, [&](int k, int j) { return Sig[(size_t)k * dk + col + j]; });
+            mm44(kin, dv, [&](int i, int k) { return t.dR[(i0 + i) * pv + k]; }, [&](int k, int j) { return Sig[(size_t)k * dk + col + j]; });
+            mm44(kout, dv, [&](int i, int k) { return t.U[(i0 + i) * pv + k]; }, [&](int k, int j) { return D[(size_t)k * dk + col + j]; });
             for (int a = 0; a < 4; ++a)
                 for (int b = 0; b < 4; ++b) {
                     const int i = i0 + a;
-                    const float qv = t.Q[i * dk + col + b], kv = t.K[i * dk + col + b];
+                    const float qv = t.Q[i * pk + col + b], kv = t.K[i * pk + col + b];
                     dq[a][b] *= t.eg[i];
                     kin[a][b] *= -t.beta[i] * t.eg[i];
                     kout[a][b] *= t.el[i];
                     into[a] += qv * dq[a][b] + kv * kin[a][b];
                     past[a] += kv * kout[a][b];
                 }
-            mm44(dq, C, [&](int i, int k) { return t.P[(i0 + i) * LC + k]; }, [&](int k, int j) { return t.K[k * dk + col + j]; });
-            mm44(kA, C, [&](int i, int k) { return t.A[(i0 + i) * LC + k]; }, [&](int k, int j) { return t.K[k * dk + col + j]; });
-            mm44(kT, C, [&](int i, int k) { return t.P[k * LC + i0 + i]; }, [&](int k, int j) { return t.Q[k * dk + col + j]; });
-            mm44(kT, C, [&](int i, int k) { return t.A[k * LC + i0 + i] * t.beta[k]; }, [&](int k, int j) { return t.K[k * dk + col + j]; });
+            mm44(dq, C, [&](int i, int k) { return t.P[(i0 + i) * LC + k]; }, [&](int k, int j) { return t.K[k * pk + col + j]; });
+            mm44(kA, C, [&](int i, int k) { return t.A[(i0 + i) * LC + k]; }, [&](int k, int j) { return t.K[k * pk + col + j]; });
+            mm44(kT, C, [&](int i, int k) { return t.P[k * LC + i0 + i]; }, [&](int k, int j) { return t.Q[k * pk + col + j]; });
+            mm44(kT, C, [&](int i, int k) { return t.A[k * LC + i0 + i] * t.beta[k]; }, [&](int k, int j) { return t.K[k * pk + col + j]; });
             for (int a = 0; a < 4; ++a) {
                 const int i = i0 + a;
                 const size_t g = (size_t)(ch.first + i);
                 for (int b = 0; b < 4; ++b) {
-                    db[a] += t.K[i * dk + col + b] * kA[a][b];
+                    db[a] += t.K[i * pk + col + b] * kA[a][b];
                     const float dkv = kin[a][b] + kout[a][b] + t.beta[i] * kA[a][b] + kT[a][b];
                     if (i >= ch.rows) continue;
                     if (w.dqh) {
@@ -367,7 +388,7 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
     }
     for (int a = 0; a < 4; ++a)
         for (int n = cg; n < dv; n += 16)
-            db[a] += t.dR[(i0 + a) * dv + n] * w.Y[(idx * C + i0 + a) * dv + n];
+            db[a] += t.dR[(i0 + a) * pv + n] * w.Y[(idx * C + i0 + a) * dv + n];
     for (int e = tid; e < dk * dv; e += blockDim.x) all += Sig[e] * D[e];
     for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     if (tid % 32 == 0) t.red[tid / 32] = all;
