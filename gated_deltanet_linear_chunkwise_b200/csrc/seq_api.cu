@@ -13,6 +13,11 @@ namespace {
 
 enum Which { kDecode, kPacked, kBwd };
 
+// In a batch of short prompts the ones up to this length go token by token and the others in chunks, two launches beside
+// one another's sequences: a chunk step and its block's start take as long as 24 tokens.  Where the average is over
+// kMixed, no more than a few can be short, and the chunks take them all.
+constexpr long long kShort = 24, kMixed = 256;
+
 int fail(int status, const char *fmt, ...) {
     char text[400];
     va_list ap;
@@ -131,6 +136,8 @@ int check(const gdn_seq_args &a, Which which, gdn::SeqProblem &p) {
     p.d_o = a.d_o; p.dS_out = a.dS_out; p.dq = a.dq; p.dk_out = a.dk; p.dv_out = a.dv;
     p.dalpha = a.dalpha; p.dbeta = a.dbeta; p.dS_in = a.dS_in;
     p.status = a.status_dev;
+    p.min_len = 0;
+    p.max_len = a.n_tokens;
     return GDN_OK;
 }
 
@@ -141,6 +148,7 @@ int check(const gdn_seq_args &a, Which which, gdn::SeqProblem &p) {
 // 25 / 18; 40 sequences with 128 tokens 31 / 91, with 400 54 / 92, with 800 95 / 92.
 bool chunked(const gdn::SeqProblem &p, Which which) {
     if (p.dtype != GDN_DTYPE_BF16 || p.n_tokens == 0) return false;
+    if (which == kPacked && !p.cu) return p.seq_len > kShort;
     return which == kBwd || p.n_tokens >= 50 + (long long)p.n_seqs * p.H * (p.dv / 16) / 20;
 }
 
@@ -179,7 +187,14 @@ int run(const gdn_seq_args *a, Which which) noexcept {
         }
         cudaError_t e = cudaSuccess;
         if (which == kBwd) e = chunked(p, which) ? gdn::launch_seq_bwd_chunk(p, ws, s) : gdn::launch_seq_bwd_simt(p, ws, s);
-        else if (p.n_seqs && which == kPacked && chunked(p, which)) e = gdn::launch_seq_chunk(p, ws, s);
+        else if (p.n_seqs && which == kPacked && chunked(p, which)) {
+            if (p.cu && p.n_tokens < kMixed * p.n_seqs) {
+                p.max_len = kShort;
+                e = gdn::launch_seq_recurrent(p, false, s);
+                p.min_len = kShort + 1;
+            }
+            if (e == cudaSuccess) e = gdn::launch_seq_chunk(p, ws, s);
+        }
         else if (p.n_seqs) e = gdn::launch_seq_recurrent(p, which == kDecode, s);
         if (owned) {
             cudaError_t e2 = cudaFreeAsync(ws, s);

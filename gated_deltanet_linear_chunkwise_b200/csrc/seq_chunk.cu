@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
         return;
     }
     const SeqChunk ch = seq_chunk(p, c);
-    if (ch.rows == 0) return;
+    if (ch.rows == 0 || (p.min_len > 0 && seq_rows(p, ch.seq).len < p.min_len)) return;
     for (int i = tid; i < C * (DK / 8); i += 128) {
         const int r = i / (DK / 8), col = i % (DK / 8) * 8, on = r < ch.rows ? 16 : 0;
         const long long row = ch.first + (on ? r : 0);
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = warp_number();
     const SeqRange r = seq_range(p, s);
     seq_report(p, r, h == 0 && c0 == 0 && threadIdx.x == 0);
-    if (r.slot < 0) return;
+    if (r.slot < 0 || r.len < p.min_len) return;
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);
     const size_t soff = (((size_t)r.slot * p.H + h) * p.dv + c0) * DK;
     const ChainFetch<NF, false> fetch = {sm, maps, w, hk, h, c0};
@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_const
     const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
     const SeqRange r = seq_range(p, at.s);
     seq_report(p, r, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
-    if (r.slot < 0) return;
+    if (r.slot < 0 || r.len < p.min_len) return;
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, at.s, r.first);
     const WalkFetch<NF, false> fetch = {sm, maps, w, at.hk, at.h, at.c0};
     const bool fetcher = threadIdx.x == 0, walks = at.slice < at.slices;

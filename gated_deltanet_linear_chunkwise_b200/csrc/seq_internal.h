@@ -26,6 +26,7 @@ struct SeqProblem {
     void *dq, *dk_out, *dv_out;
     float *dalpha, *dbeta, *dS_in;
     int *status;
+    long long min_len, max_len;  // gdn_packed: a kernel leaves sequences of other lengths to another one
 };
 
 // Rows and state entry of a sequence.  slot < 0: the sequence is skipped.

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kManyThreads) k_many(const __grid_constant__ S
     const int lr = threadIdx.x / 4, part = threadIdx.x & 3;
     const SeqRange range = seq_range(p, s);
     seq_report(p, range, rb == 0 && threadIdx.x == 0);
-    if (range.slot < 0) return;
+    if (range.slot < 0 || range.len > p.max_len) return;
     const size_t soff = (((size_t)range.slot * p.H + h) * p.dv + r0 + lr) * DK + part * 4;
     float4 S[NF];
     const bool zero = seq_starts_zero(p, s);
