@@ -9,8 +9,9 @@
 // k_few: one or a few tokens (gdn_decode).  The state is read and written once and dominates
 // (2 x 4 d_k d_v bytes a head against 2 (2 d_k + 2 d_v)): the bound is HBM.
 // k_many: sequences of tokens (gdn_packed, where the chunked form does not serve), with the
-// tokens' rows staged in shared memory a block ahead.  Its bound is the fp32 pipe: 4 d_k d_v
-// instructions' lanes a token and head.
+// tokens' rows staged in shared memory a block ahead.  A long sequence is bound by the chain of a token's two dot products
+// (996 tokens, d_k = 64: 140 us, 270 clocks a token), many short ones by the fp32 pipe: 4 d_k d_v instructions' lanes a token
+// and head.
 #include <cuda_bf16.h>
 #include <type_traits>
 
@@ -142,8 +143,9 @@ __global__ void __launch_bounds__(kFewThreads) k_few(const __grid_constant__ Seq
 constexpr int kTok = 16;
 constexpr int kManyThreads = 64;
 
+// Six blocks an SM: left to itself the compiler takes registers for five, and batches of short prompts run a fifth longer.
 template <typename T, int NF>
-__global__ void __launch_bounds__(kManyThreads) k_many(const __grid_constant__ SeqProblem p) {
+__global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant__ SeqProblem p) {
     constexpr int DK = 16 * NF;
     __shared__ __align__(16) float sk[2][kTok][DK], sq[2][kTok][DK];
     __shared__ float sv[2][kTok][16], sg[2][kTok][2];
@@ -197,6 +199,8 @@ __global__ void __launch_bounds__(kManyThreads) k_many(const __grid_constant__ S
         }
         if (threadIdx.x < 2 * kTok) sg[b][threadIdx.x / 2][threadIdx.x & 1] = ng;
     };
+    T *out = (T *)p.o + (range.first * p.H + h) * p.dv + r0 + lr;
+    const size_t out_step = (size_t)p.H * p.dv;
     if (range.len > 0) {
         fetch(0);
         stash(0);
@@ -207,15 +211,29 @@ __global__ void __launch_bounds__(kManyThreads) k_many(const __grid_constant__ S
         const bool more = t0 + kTok < range.len;
         if (more) fetch(t0 + kTok);
         const int n = (int)min((long long)kTok, range.len - t0);
-        for (int t = 0; t < n; ++t) {
+        const float *ks = &sk[b][0][part * 4], *qs = &sq[b][0][part * 4];
+        auto token = [&](int t) {
             float4 k[NF], q[NF];
 #pragma unroll
             for (int j = 0; j < NF; ++j) {
-                k[j] = ld4(&sk[b][t][part * 4 + 16 * j]);
-                q[j] = ld4(&sq[b][t][part * 4 + 16 * j]);
+                k[j] = ld4(ks + t * DK + 16 * j);
+                q[j] = ld4(qs + t * DK + 16 * j);
             }
-            const float o = token_step<NF>(S, k, q, sg[b][t][0], sg[b][t][1], sv[b][t][lr]);
-            if (part == 0) put((T *)p.o + ((range.first + t0 + t) * p.H + h) * p.dv + r0 + lr, o);
+            return token_step<NF>(S, k, q, sg[b][t][0], sg[b][t][1], sv[b][t][lr]);
+        };
+        // Four tokens' outputs are kept and then stored, a token a lane of a row's four
+        int t = 0;
+        for (; t + 4 <= n; t += 4) {
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = token(t + i);
+            put(out + part * out_step, part & 2 ? (part & 1 ? o[3] : o[2]) : (part & 1 ? o[1] : o[0]));
+            out += 4 * out_step;
+        }
+        for (; t < n; ++t) {
+            const float o = token(t);
+            if (part == 0) put(out, o);
+            out += out_step;
         }
         if (more) stash(b ^ 1);
         __syncthreads();
