@@ -332,7 +332,7 @@ def _tokens(name, t, dtype, device, lead, heads, d):
         raise GdnError(1, "%s must have q's device and dtype (%s, %s)" % (name, device, dtype))
     if t.shape != (*lead, heads, d):
         raise GdnError(2, "%s must have shape %s, got %s" % (name, (*lead, heads, d), tuple(t.shape)))
-    if t.is_contiguous():
+    if t.is_contiguous():  # as any single token with its heads in place is
         return heads * d
     st = t.stride()
     if st[-1] != 1 or (st[-2] != d and heads > 1) or (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * st[1]):

@@ -557,6 +557,29 @@ def test_streams_and_graphs():
 
 
 @pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls that run beside one another share no scratch."""
+    H, d, n = 4, 64, 300
+    sets = []
+    for seed in (1, 2):
+        q, k, v, alpha, beta = [t.cuda()[None] for t in draw(n, H, H, d, d, "bf16", seed)]
+        do = torch.randn_like(v)
+        sets.append((q, k, v, alpha, beta, do))
+    run = lambda s: [*g.gdn_packed(*s[:5], return_state=True), *g.gdn_bwd(*s)[:5]]  # noqa: E731
+    want = [run(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(run(s))
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
+@pytest.mark.gpu
 def test_same_bits_again():
     q, k, v, alpha, beta = cuda(*draw(700, 4, 2, 112, 112, "bf16", 61))
     cu = torch.tensor([0, 300, 301, 700], dtype=torch.int32, device="cuda")
