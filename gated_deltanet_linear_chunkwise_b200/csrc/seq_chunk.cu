@@ -828,8 +828,8 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
 // The same walks with a warp for each 16 columns and no exchange between warps: a product's result lies in a lane as
 // the next product's A operand does (rows n, pairs along k), so S, beta Y, U, dU and dR stay in registers from
 // product to product and shared memory holds only what all slices read: K, Q, T, P and v (a step and slice takes a quarter of
-// the shared memory reads of k_chunk_fwd).  16384 tokens in 24 sequences, 20 heads, d = 112: 299 us (37 GFLOP executed in 628 products
-// a step and slice, 40 % of the warp products' rate of 1024 multiply-adds a clock and SM), against 492 us.  A block has up to four
+// the shared memory reads of k_chunk_fwd).  16384 tokens in 24 sequences, 20 heads, d = 112: 297 us (97 GFLOP executed in 628 products
+// a step and slice, 56 % of the warp products' rate of 1024 multiply-adds a clock and SM), against 492 us.  A block has up to four
 // slices of one sequence and head; one of its threads fetches.
 constexpr int kSlices = 4;
 constexpr int kWalkThreads = 32 * kSlices;  // eight warps an SM, two blocks, leave a thread its 255 registers

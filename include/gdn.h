@@ -372,8 +372,8 @@ enum { GDN_SEQ_BAD_SLOT = 1, GDN_SEQ_SAME_SLOT = 2, GDN_SEQ_BAD_ROWS = 4, GDN_SE
  *                   d_k], or NULL.
  *   workspace, workspace_bytes
  *                   device scratch, 256-byte aligned, of at least
- *                   gdn_seq_workspace_bytes(); NULL takes stream-ordered scratch
- *                   from the library's pool.
+ *                   gdn_seq_workspace_bytes(), for one call at a time; NULL takes
+ *                   stream-ordered scratch from the library's pool.
  *   status_dev      optional device int: receives the GDN_SEQ_* bits.
  */
 typedef struct gdn_seq_args {

@@ -538,6 +538,15 @@ def test_streams_and_graphs():
     side.synchronize()
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+    side.wait_stream(torch.cuda.current_stream())
+    S = S0.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    o, S1 = g.gdn_packed(q, k, v, alpha, beta, None, S, return_state=True, stream=side)  # the stream as an argument
+    grads = g.gdn_bwd(q, k, v, alpha, beta, do, None, S, stream=side)
+    side.synchronize()
+    assert torch.equal(o, want[0])
+    for x, y in zip(grads, want[3:]):
+        assert torch.equal(x, y)
     graphs, results = [], []
     for _ in range(2):  # two graphs: each keeps scratch of its own
         graph = torch.cuda.CUDAGraph()
