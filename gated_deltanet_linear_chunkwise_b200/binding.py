@@ -338,7 +338,10 @@ def _tokens(name, t, dtype, device, lead, heads, d):
     if st[-1] != 1 or (st[-2] != d and heads > 1) or (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * st[1]):
         raise GdnError(1, "%s: the heads of a token must be contiguous and the tokens equally far apart" % name)
     # of a single sequence or token a stride says nothing
-    return st[-3] if lead[-1] > 1 or len(lead) == 1 else st[0]
+    step = st[-3] if lead[-1] > 1 or len(lead) == 1 else st[0]
+    if step < heads * d:  # an expanded tensor's 0 would read as "contiguous" behind the C interface
+        raise GdnError(1, "%s: tokens %d elements apart lie over one another (a token has %d): pass .contiguous()" % (name, step, heads * d))
+    return step
 
 
 def _plain(name, t, dtype, shape, device):
@@ -425,7 +428,7 @@ def gdn_decode(q, k, v, alpha, beta, S, slots=None, *, o=None, status=None, stre
     q, k [B, n, Hk, d_k], v [B, n, H, d_v] (bf16 or fp32), alpha, beta [B, n, H] fp32; for n = 1
     the n dimension may be left out of all of them.  H is a multiple of Hk: head h reads q/k head
     h // (H // Hk).  The heads of a token are contiguous; the tokens of q, k, v may be slices of a
-    fused projection (equally far apart, a multiple of 16 bytes).
+    fused projection (equally far apart, a multiple of 16 bytes), but not one row expanded to many.
     S fp32 [n_slots, H, d_v, d_k] holds the states and is updated in place: sequence b's is
     S[slots[b]] (slots int32 [B]; None: S[b]).  A negative slot is a padding entry: its o rows and
     every state are left alone.  So is a sequence with a slot >= n_slots or the slot of an earlier
