@@ -335,7 +335,7 @@ def _tokens(name, t, dtype, device, lead, heads, d):
     if t.is_contiguous():  # as any single token with its heads in place is
         return heads * d
     st = t.stride()
-    if st[-1] != 1 or (st[-2] != d and heads > 1) or (len(lead) == 2 and lead[0] > 1 and st[0] != lead[1] * st[1]):
+    if st[-1] != 1 or (st[-2] != d and heads > 1) or (len(lead) == 2 and min(lead) > 1 and st[0] != lead[1] * st[1]):
         raise GdnError(1, "%s: the heads of a token must be contiguous and the tokens equally far apart" % name)
     # of a single sequence or token a stride says nothing
     step = st[-3] if lead[-1] > 1 or len(lead) == 1 else st[0]
