@@ -471,7 +471,8 @@ def gdn_packed(q, k, v, alpha, beta, cu_seqlens=None, S_in=None, *, S_out=None, 
     S_in, S_out fp32 [n_slots, H, d_v, d_k] hold the states that enter (None: zeros) and leave
     (None: not stored, unless ``return_state`` makes a tensor of n_slots = n); they may be the same
     tensor.  ``fresh`` (bool or uint8 [n]) starts the marked sequences from zero without reading S_in.
-    ``status`` may also receive GDN_SEQ_BAD_ROWS (a range out of order or out of the tensors).
+    ``status`` may also receive GDN_SEQ_BAD_ROWS (a range out of order, out of the tensors or into an
+    earlier sequence's).
     Returns (o, S_out or None).
     """
     import torch

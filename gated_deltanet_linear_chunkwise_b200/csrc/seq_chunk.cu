@@ -62,7 +62,8 @@ struct ChunkWork {
     float *U, *dR, *X, *Z;   // [chunk x H][dv][64]; X = e^G K Sig, Z = e^{G_L-G} K D
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
-    int *order;              // [n_seqs]: the sequences, the longest first
+    int *order;              // [n_seqs]: the sequences, the longest first; -1 - s of one that starts inside an earlier one
+    SeqChunk *chunks;        // gdn_bwd: [chunks], what seq_chunk finds
     uint64_t wait_ns;        // limit of the bounded waits
     int drop;                // debug: the first block's K is never fetched, so its wait gives up
 };
@@ -71,17 +72,34 @@ struct ChunkWork {
 // sequences of 44 to 1971: 421 us against 505 in their order).  A sequence's place is the number of longer ones, ties by index.
 __device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order, int *len) {  // len: room for 2048
     const bool sort = p.cu && p.n_seqs <= 2048;
-    if (sort)
-        for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) len[s] = (int)seq_rows(p, s).len;
-    __syncthreads();
+    bool odd = false;
+    if (p.cu)
+        for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {
+            const SeqRange r = seq_rows(p, s);
+            if (sort) len[s] = (int)r.len;
+            odd |= r.bad != 0;
+        }
+    odd = __syncthreads_or(odd);  // else every range is in order
     for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {
         int place = s;
         if (sort) {
             place = 0;
             for (int j = 0; j < p.n_seqs; ++j) place += len[j] > len[s] || (len[j] == len[s] && j < s);
         }
-        order[place] = s;
+        bool late = false;
+        if (odd) {
+            const SeqRange r = seq_rows(p, s);
+            for (int j = 0; j < s && r.len > 0; ++j) late |= seq_reaches(p, j, r.first);
+        }
+        order[place] = late ? -1 - s : s;
     }
+}
+
+// dS_in's columns of a sequence that starts inside an earlier one (NULL in a forward call), by a whole block.
+__device__ __forceinline__ void no_state(const SeqProblem &p, int s, int h, int c0, int cols) {
+    if (!p.dS_in) return;
+    float *to = p.dS_in + (((size_t)s * p.H + h) * p.dv + c0) * p.dk;
+    for (int i = threadIdx.x; i < cols * p.dk; i += blockDim.x) to[i] = 0.f;
 }
 
 template <int NF>
@@ -103,6 +121,7 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
         return;
     }
     const SeqChunk ch = seq_chunk(p, c);
+    if (w.chunks && h == 0 && tid == 0) w.chunks[c] = ch;
     if (ch.rows == 0 || (p.min_len > 0 && seq_rows(p, ch.seq).len < p.min_len)) return;
     for (int i = tid; i < C * (DK / 8); i += 128) {
         const int r = i / (DK / 8), col = i % (DK / 8) * 8, on = r < ch.rows ? 16 : 0;
@@ -561,8 +580,13 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
     auto &sm = *reinterpret_cast<ChainSmem<NF, false> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const uint32_t aS = sm100::smem_u32(sm.S), aU = sm100::smem_u32(sm.U), aR = sm100::smem_u32(sm.R), aT = sm100::smem_u32(sm.T),
                    aP = sm100::smem_u32(sm.P);
-    const int groups = p.dv / NV, s = w.order[blockIdx.x / (p.H * groups)], h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
+    const int groups = p.dv / NV, next = w.order[blockIdx.x / (p.H * groups)], h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = warp_number();
+    if (next < 0) {
+        seq_report(p, kSeqLate, h == 0 && c0 == 0 && threadIdx.x == 0);
+        return no_state(p, -1 - next, h, c0, NV);
+    }
+    const int s = next;
     const SeqRange r = seq_range(p, s);
     seq_report(p, r, h == 0 && c0 == 0 && threadIdx.x == 0);
     if (r.slot < 0 || r.len < p.min_len) return;
@@ -704,8 +728,10 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
     auto &sm = *reinterpret_cast<ChainSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const uint32_t aS = sm100::smem_u32(sm.S), aU = sm100::smem_u32(sm.U), aR = sm100::smem_u32(sm.R), aT = sm100::smem_u32(sm.T),
                    aP = sm100::smem_u32(sm.P);
-    const int groups = p.dv / NV, s = w.order[blockIdx.x / (p.H * groups)], h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
+    const int groups = p.dv / NV, next = w.order[blockIdx.x / (p.H * groups)], h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = warp_number();
+    if (next < 0) return;  // the forward walk has written its dS_in
+    const int s = next;
     const SeqRange r = seq_rows(p, s);
     const size_t soff = (((size_t)s * p.H + h) * p.dv + c0) * DK;
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);  // 0 of a bad range
@@ -995,11 +1021,14 @@ __device__ __forceinline__ void walk_store(bf16 *dst, long long row_elems, const
 // Which slice a thread's warp walks.
 struct WalkPlace {
     int s, h, hk, c0, slice, slices;  // c0: the block's first column; slices: how many the block has
+    bool late;
 };
 __device__ __forceinline__ WalkPlace walk_place(const SeqProblem &p, const int *order) {
     const int groups = (p.dv + 16 * kSlices - 1) / (16 * kSlices);
     WalkPlace x;
-    x.s = order[blockIdx.x / (p.H * groups)];
+    const int next = order[blockIdx.x / (p.H * groups)];
+    x.late = next < 0;
+    x.s = x.late ? -1 - next : next;
     x.h = blockIdx.x / groups % p.H;
     x.hk = x.h / (p.H / p.Hk);
     x.c0 = blockIdx.x % groups * 16 * kSlices;
@@ -1021,6 +1050,10 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_const
     auto &sm = *reinterpret_cast<WalkSmem<NF, false> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const WalkPlace at = walk_place(p, w.order);
     const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
+    if (at.late) {
+        seq_report(p, kSeqLate, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
+        return no_state(p, at.s, at.h, at.c0, 16 * at.slices);
+    }
     const SeqRange r = seq_range(p, at.s);
     seq_report(p, r, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
     if (r.slot < 0 || r.len < p.min_len) return;
@@ -1189,6 +1222,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_bwd(const __grid_const
     auto &sm = *reinterpret_cast<WalkSmem<NF, true> *>(raw + (-sm100::smem_u32(raw) & 1023));
     const WalkPlace at = walk_place(p, w.order);
     const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
+    if (at.late) return;  // the forward walk has written its dS_in
     const SeqRange r = seq_rows(p, at.s);
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, at.s, r.first);  // 0 of a bad range
     const WalkFetch<NF, true> fetch = {sm, maps, w, at.hk, at.h, at.c0};
@@ -1399,7 +1433,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
     const long long c = blockIdx.x / p.H;
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
     const int mt = warp & 3, role = warp >> 2, dv = p.dv, nvf = dv / 16;
-    const SeqChunk ch = seq_chunk(p, c);
+    const SeqChunk ch = w.chunks[c];
     if (ch.rows == 0) return;
     const size_t idx = (size_t)c * p.H + h;
     const GradLayout<NF> at(dv);
@@ -2020,6 +2054,7 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
     if (!bwd) {
         w.P = (uint2 *)take(2 * frag);
     } else {
+        w.chunks = (SeqChunk *)take(seq_max_chunks(p) * sizeof(SeqChunk));
         w.Tt = (uint2 *)take(3 * frag);
         w.Pt = (uint2 *)take(3 * frag);
         w.gam = (float4 *)take(n * kUnits * 32 * sizeof(float4));

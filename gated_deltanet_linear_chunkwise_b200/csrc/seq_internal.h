@@ -37,7 +37,7 @@ struct SeqRange {
     int bad;  // GDN_SEQ_* bits
 };
 
-// Rows of sequence s, 0 of them where they are no ordered range inside the tensors.
+// Rows of sequence s by itself, 0 of them where they are no ordered range inside the tensors.
 __device__ __forceinline__ SeqRange seq_rows(const SeqProblem &p, int s) {
     SeqRange r;
     r.bad = 0;
@@ -58,7 +58,30 @@ __device__ __forceinline__ SeqRange seq_rows(const SeqProblem &p, int s) {
     return r;
 }
 
-// seq_rows with the slot looked up and checked; called by a whole block (it votes on an
+// Does sequence j, an ordered range by itself, reach behind row `first`?
+__device__ __forceinline__ bool seq_reaches(const SeqProblem &p, int j, long long first) {
+    const SeqRange r = seq_rows(p, j);
+    return r.len > 0 && r.first + r.len > first;
+}
+
+// Does an earlier sequence reach behind the first row of s?  Such a sequence is skipped, so that no two share rows or a
+// chunk's index.  Called by a whole block.
+__device__ __forceinline__ bool seq_late_odd(const SeqProblem &p, int s) {
+    const SeqRange r = seq_rows(p, s);
+    bool late = false;
+    for (int j = threadIdx.x; j < s; j += blockDim.x) late |= seq_reaches(p, j, r.first);
+    return __syncthreads_or(late && r.len > 0);
+}
+__device__ __forceinline__ bool seq_late(const SeqProblem &p, int s) {
+    if (!p.cu) return false;
+    bool odd = false;  // where every earlier range is in order by itself, all of them are
+    for (int j = threadIdx.x; j < s; j += blockDim.x) odd |= seq_rows(p, j).bad != 0;
+    return __syncthreads_or(odd) && seq_late_odd(p, s);
+}
+__device__ constexpr SeqRange kSeqLate = {0, 0, -1, GDN_SEQ_BAD_ROWS};
+__device__ __forceinline__ SeqRange seq_rows_in_order(const SeqProblem &p, int s) { return seq_late(p, s) ? kSeqLate : seq_rows(p, s); }
+
+// A sequence's range with its slot looked up and checked; called by a whole block (it votes on an
 // earlier sequence of the same slot, so that of two writers of one state only the first runs).
 __device__ __forceinline__ SeqRange seq_range(const SeqProblem &p, int s) {
     SeqRange r = seq_rows(p, s);
@@ -84,8 +107,8 @@ __device__ __forceinline__ bool seq_starts_zero(const SeqProblem &p, int s) {
     return !p.S_in || (p.fresh && p.fresh[s]);
 }
 
-// Chunks.  Chunk i of sequence s has the index seq_chunk_base(s) + i, unique without a table:
-// ceil(len / 64) <= floor(end / 64) - floor(first / 64) + 1.
+// Chunks.  Chunk i of sequence s has the index seq_chunk_base(s) + i, unique without a table where the sequences lie in
+// the order of their rows: ceil(len / 64) <= floor(end / 64) - floor(first / 64) + 1.
 __host__ __device__ __forceinline__ long long seq_chunks_of(long long len) {
     return (len + kSeqChunk - 1) / kSeqChunk;
 }
@@ -102,24 +125,48 @@ struct SeqChunk {
     int rows;
     int seq;
 };
-// Called by a whole block.  Every sequence is looked at, so that ranges out of order hide no other one.
+// Of the sequences that by themselves have a chunk c only the first can be in order (the others' bases lie behind its
+// end).  Called by a whole block, where a range is wrong.
+__device__ __forceinline__ SeqChunk seq_chunk_odd(const SeqProblem &p, long long c) {
+    __shared__ int least;
+    if (threadIdx.x == 0) least = p.n_seqs;
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {
+        const SeqRange r = seq_rows(p, s);
+        const long long t = (c - seq_chunk_base(p, s, r.first)) * kSeqChunk;
+        if (t >= 0 && t < r.len) atomicMin(&least, s);
+    }
+    __syncthreads();
+    const int s = least;
+    if (s == p.n_seqs) return {0, 0, -1};
+    const SeqRange r = seq_rows_in_order(p, s);
+    if (r.len == 0) return {0, 0, -1};
+    const long long t = (c - seq_chunk_base(p, s, r.first)) * kSeqChunk;
+    return {r.first + t, (int)min((long long)kSeqChunk, r.len - t), s};
+}
+// Called by a whole block.  Where every range is in order by itself, all of them are, and the one that has c is it.
 __device__ __forceinline__ SeqChunk seq_chunk(const SeqProblem &p, long long c) {
     __shared__ SeqChunk found;
+    __shared__ int odd;
     if (!p.cu) {
         const long long n = seq_chunks_of(p.seq_len);
         const int s = (int)(c / n);
         const long long t = (c % n) * kSeqChunk;
         return {s * p.seq_len + t, (int)min((long long)kSeqChunk, p.seq_len - t), s};
     }
-    if (threadIdx.x == 0) found = {0, 0, -1};
+    if (threadIdx.x == 0) {
+        found = {0, 0, -1};
+        odd = 0;
+    }
     __syncthreads();
     for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {
         const SeqRange r = seq_rows(p, s);
         const long long t = (c - seq_chunk_base(p, s, r.first)) * kSeqChunk;
         if (t >= 0 && t < r.len) found = {r.first + t, (int)min((long long)kSeqChunk, r.len - t), s};
+        if (r.bad) odd = 1;
     }
     __syncthreads();
-    return found;
+    return odd ? seq_chunk_odd(p, c) : found;
 }
 
 // What the chunk kernels keep of each (chunk, head), index chunk * H + head (fp32):

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kFewThreads) k_few(const __grid_constant__ Seq
     float4 S[NF], next[NF];
     size_t soff = (((size_t)(inside ? slot : 0) * p.H + h) * p.dv + r) * p.dk + part * 4;
     if (inside) load_state(S, p.S_in + soff);
-    const SeqRange range = seq_range(p, s);
+    const SeqRange range = seq_range(p, s);  // without cu_seqlens: in order
     seq_report(p, range, rb == 0 && threadIdx.x == 0);
     if (range.slot < 0) return;
     const int last = HEAD ? p.dv - 16 : 0;
@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant_
     const int s = blockIdx.x / per_seq, rb = blockIdx.x % per_seq;
     const int h = rb / (p.dv / 16), r0 = (rb % (p.dv / 16)) * 16, hk = h / (p.H / p.Hk);
     const int lr = threadIdx.x / 4, part = threadIdx.x & 3;
+    if (seq_late(p, s)) return seq_report(p, kSeqLate, rb == 0 && threadIdx.x == 0);
     const SeqRange range = seq_range(p, s);
     seq_report(p, range, rb == 0 && threadIdx.x == 0);
     if (range.slot < 0 || range.len > p.max_len) return;

@@ -337,9 +337,10 @@ size_t gdn_workspace_bytes(int B, int H, long long T, int frame_len, int d_k, in
  * sequence is skipped like a padding entry, and its bit set in *status_dev,
  * when its slot is >= n_slots (GDN_SEQ_BAD_SLOT), when an earlier sequence
  * has the same slot (GDN_SEQ_SAME_SLOT; the first one runs), or when its rows
- * are not an ordered range inside the n_tokens rows (GDN_SEQ_BAD_ROWS).  Two
- * sequences may not share rows.  GDN_SEQ_TIMEOUT: a bounded device-side wait
- * gave up and the outputs are not valid.
+ * are not an ordered range inside the n_tokens rows or begin before the end of
+ * an earlier sequence whose rows are one (GDN_SEQ_BAD_ROWS): sequences lie in
+ * the order of their rows and share none.  GDN_SEQ_TIMEOUT: a bounded
+ * device-side wait gave up and the outputs are not valid.
  *
  * Calls are asynchronous on `stream`, whose device must be the current one.
  * The same call gives the same bits: no result depends on the order in which

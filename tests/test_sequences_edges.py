@@ -1,10 +1,12 @@
 """The sequence operators at the edges of what their callers may pass.  Tolerances as in test_sequences.py."""
+import random
+
 import pytest
 import torch
 
 import gated_deltanet_linear_chunkwise_b200 as g
 from gated_deltanet_linear_chunkwise_b200 import binding
-from test_sequences import cuda, draw
+from test_sequences import F64, close, cuda, draw, exact_grads, tol32, token_loop
 
 
 # ---------------------------------------------------------------- rows of q, k and v
@@ -57,3 +59,67 @@ def test_one_token_slices_of_a_projection(dtype):
 
     for x, y in zip(everything(*slices), everything(q, k, v)):
         assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------- sequences out of order
+def in_order(cu, N):
+    """The sequences that run: ordered ranges inside the tensors, none of which an earlier one reaches into."""
+    ok = [0 <= a <= b <= N for a, b in zip(cu, cu[1:])]
+    ends = [b if o and b > a else 0 for o, a, b in zip(ok, cu, cu[1:])]
+    return [o and (a == b or a >= max(ends[:s], default=0)) for s, (o, a, b) in enumerate(zip(ok, cu, cu[1:]))]
+
+
+def shuffled(n, N, seed):
+    rng = random.Random(seed)
+    cu = sorted(rng.randint(0, N) for _ in range(n + 1))
+    for _ in range(n // 20):
+        i, j = rng.randint(0, n), rng.randint(0, n)
+        cu[i], cu[j] = cu[j], cu[i]
+    return cu
+
+
+OUT_OF_ORDER = [
+    [100, 200, 0, 64],          # two ranges that would share a chunk's index
+    [0, 150, 100, 200],         # two that share rows
+    [50, 50, 0, 30, 200],       # an empty one reaches nowhere
+    [0, 64, 10, 10, 64, 199],   # an empty one inside another
+    [130, 140, 0, 130, 140, 200],
+    shuffled(300, 2000, 3),     # chains enough for a warp a slice; more sequences than a block has threads
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cu", OUT_OF_ORDER, ids=lambda c: str(len(c) - 1))
+def test_sequences_out_of_order(cu, dtype):
+    N, H, Hk, dk, dv = max(cu), 4, 2, 32, 64
+    n = len(cu) - 1
+    good = in_order(cu, N)
+    assert not all(good) and any(good)
+    tensors = draw(N, H, Hk, dk, dv, dtype, 19)
+    gen = torch.Generator().manual_seed(5)
+    do = torch.randn(tensors[2].shape, generator=gen).to(tensors[2].dtype)
+    S, dS = torch.randn(n, H, dv, dk, generator=gen), torch.randn(n, H, dv, dk, generator=gen)
+    run = [s for s in range(n) if good[s]]
+    lens, starts = [cu[s + 1] - cu[s] for s in run], [cu[s] for s in run]
+    rows, states = token_loop(*(t.double() for t in tensors), S[run].double(), lens, starts)
+    tol, T = tol32(dk, max(lens)), max(lens)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, S_out = torch.full(tensors[2].shape, 7.0, dtype=tensors[2].dtype, device="cuda"), torch.full(S.shape, 7.0, device="cuda")
+    at = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    g.gdn_packed(*cuda(*tensors), at, S.cuda(), S_out=S_out, o=o, status=status)
+    assert int(status) == binding.GDN_SEQ_BAD_ROWS
+    covered, skipped = sorted(rows), [s for s in range(n) if not good[s]]
+    close(o[covered], torch.stack([rows[t] for t in covered]), tol, "o")
+    close(S_out[run], torch.stack(states), tol, "S")
+    left = [t for t in range(N) if t not in rows]
+    assert (o[left] == 7).all() and (S_out[skipped] == 7).all()
+    status.zero_()
+    got = g.gdn_bwd(*cuda(*tensors), do.cuda(), at, S.cuda(), dS_out=dS.cuda(), status=status)
+    assert int(status) == binding.GDN_SEQ_BAD_ROWS
+    want = exact_grads(tensors, starts, lens, S[run], do, dS[run])
+    for name, x, y in zip(("dq", "dk", "dv", "dalpha", "dbeta"), got, want):
+        close(x, y, tol32(dk, T, 4), name)
+        assert not x[left].any()
+    close(got[5][run], want[5], tol32(dk, T, 4), "dS_in")
+    assert not got[5][skipped].any()
