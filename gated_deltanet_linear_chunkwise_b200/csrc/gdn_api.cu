@@ -414,7 +414,7 @@ cudaError_t pool_scratch(void **ptr, size_t bytes, cudaStream_t s) { return scra
 
 int debug_drop_signal() {
     const char *e = getenv("GDN_DEBUG_DROP_SIGNAL");
-    return (e && e[0] == '1') ? 1 : 0;
+    return e && (e[0] == '1' || e[0] == '2') ? e[0] - '0' : 0;
 }
 
 uint64_t wait_limit_ns() {

@@ -113,7 +113,9 @@ struct NvtxRange {
 uint64_t wait_limit_ns();
 // Debug: GDN_DEBUG_DROP_SIGNAL=1 (read at every call) makes the diagonal-inverse kernel
 // withhold its first block's product, so the wait on it gives up at the limit above and the
-// pass reports GDN_ERR_TIMEOUT without any fault (the bounded-wait test).  0 otherwise.
+// pass reports GDN_ERR_TIMEOUT without any fault (the bounded-wait test).  The chunked sequence
+// kernels then never fetch their first block's K, or with 2 its T, and report GDN_SEQ_TIMEOUT.
+// 0 otherwise.
 int debug_drop_signal();
 
 // Argument validation of the C ABI (gdn_api.cu): fills p or returns a gdn_status.

@@ -220,7 +220,7 @@ cudaError_t launch_tc_forward(const Problem &p, void *ws, int scan_reverse, cuda
     if ((e = cudaGetLastError())) return e;
     if ((e = mark(ev, 1, s))) return e;
     if ((e = tc::launch_diag_inverse(tm_k, tm_t, p.beta, G, CF, p.L, p.dk, p.H, nblk, p.F, p.T, nfh, err, wait_ns,
-                                     debug_drop_signal(), s)))
+                                     debug_drop_signal() == 1, s)))
         return e;
     if ((e = mark(ev, 2, s))) return e;
     // the intra-frame solve also forms the frame's transition: fp32 M for the CUDA-core scan (and the

@@ -65,7 +65,7 @@ struct ChunkWork {
     int *order;              // [n_seqs]: the sequences, the longest first; -1 - s of one that starts inside an earlier one
     SeqChunk *chunks;        // gdn_bwd: [chunks], what seq_chunk finds
     uint64_t wait_ns;        // limit of the bounded waits
-    int drop;                // debug: the first block's K is never fetched, so its wait gives up
+    int drop;                // debug: the first block's K (1) or T (2) is never fetched, so its wait gives up
 };
 
 // The chains' blocks start with the longest sequences: a long one that starts last runs alone (16384 tokens in 24
@@ -353,7 +353,7 @@ template <int NF, bool BWD> struct ChainFetch {
     __device__ __forceinline__ void k(int b, int row, size_t idx) const {  // and the gates
         uint64_t *bar = &sm.bar[kBarK + b];
         sm100::mbar_arrive_expect_tx(bar, kTileBytes + 3 * C * 4);
-        if (!w.drop || blockIdx.x) tile(sm.K[b], &maps.k, bar, row);
+        if (w.drop != 1 || blockIdx.x) tile(sm.K[b], &maps.k, bar, row);
         sm100::bulk_copy_g2s(&sm.gates[b][0][0], w.gates + idx * 3 * C, 3 * C * 4, bar);
     }
     __device__ __forceinline__ void v(int row, bool with_q) const {  // 16 columns of v (or do); forwards with Q
@@ -364,7 +364,7 @@ template <int NF, bool BWD> struct ChainFetch {
     }
     __device__ __forceinline__ void t(const uint2 *src) const {
         sm100::mbar_arrive_expect_tx(&sm.bar[kBarT], sizeof(sm.T));
-        sm100::bulk_copy_g2s(sm.T, src, sizeof(sm.T), &sm.bar[kBarT]);
+        if (w.drop != 2 || blockIdx.x) sm100::bulk_copy_g2s(sm.T, src, sizeof(sm.T), &sm.bar[kBarT]);
     }
     __device__ __forceinline__ void p(const uint2 *src, int row, bool with_q) const {  // backwards with Q, read last
         sm100::mbar_arrive_expect_tx(&sm.bar[kBarP], sizeof(sm.P) + (with_q ? kTileBytes : 0));
@@ -389,14 +389,15 @@ __device__ __forceinline__ void chain_init(uint64_t (&bar)[5]) {
     }
     __syncthreads();
 }
-// A block that gave up leaves no copy in flight: the last copy of every barrier is waited for once more.
+// A block that gave up leaves no copy in flight: the last copy of every barrier is waited for once more.  k_turn, p_turn: the
+// last steps whose K and P were fetched (-1: no P).
 template <int NF, bool BWD>
-__device__ __forceinline__ void chain_leave(ChainSmem<NF, BWD> &sm, const SeqProblem &p, long long turn, int p_turn, int *err) {
+__device__ __forceinline__ void chain_leave(ChainSmem<NF, BWD> &sm, const SeqProblem &p, long long turn, long long k_turn, long long p_turn, int *err) {
     const uint32_t now = (uint32_t)turn & 1;
-    sm100::mbar_wait(&sm.bar[kBarK + now], (uint32_t)(turn >> 1) & 1, err, sm100::kWaitLimitNs, true);
+    sm100::mbar_wait(&sm.bar[kBarK + (k_turn & 1)], (uint32_t)(k_turn >> 1) & 1, err, sm100::kWaitLimitNs, true);
     sm100::mbar_wait(&sm.bar[kBarV], now, err, sm100::kWaitLimitNs, true);
     sm100::mbar_wait(&sm.bar[kBarT], now, err, sm100::kWaitLimitNs, true);
-    if (p_turn >= 0) sm100::mbar_wait(&sm.bar[kBarP], p_turn & 1, err, sm100::kWaitLimitNs, true);  // P's last fetch, if any
+    if (p_turn >= 0) sm100::mbar_wait(&sm.bar[kBarP], (uint32_t)p_turn & 1, err, sm100::kWaitLimitNs, true);
     if (p.status && threadIdx.x == 0) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         const int rows = (int)min((long long)C, r.len - c * C);
         ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(c >> 1) & 1, w.err, w.wait_ns) && sm100::mbar_wait(&sm.bar[kBarV], parity, w.err, w.wait_ns);
         // behind this barrier the state's terms are there and the last step's buffers have been read
-        if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, SAVE ? -1 : (int)c - 1, w.err);
+        if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, c, SAVE ? -1 : c - 1, w.err);
         if (fetcher) {
             if (c + 1 < n_chunks) fetch.k(b ^ 1, first_row(c + 1), index(c + 1));
             if (!SAVE) fetch.p(w.P + idx * 2 * kUnits * 32, 0, false);
@@ -634,8 +635,9 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
             zero_tail(&sm.V[0][0], 1, NV / 8, rows);
             __syncthreads();
         }
+        const long long k_turn = c + 1 < n_chunks ? c + 1 : c;
         if (warp == kFetchWarp) {  // it keeps the barriers' count
-            __syncthreads();
+            if (!__syncthreads_and(true)) return chain_leave(sm, p, c, k_turn, SAVE ? -1 : c, w.err);
             if (fetcher && c + 1 < n_chunks) fetch.v(first_row(c + 1), !SAVE);
             __syncthreads();
             if (fetcher && c + 1 < n_chunks) fetch.t(w.T + index(c + 1) * 3 * kUnits * 32);
@@ -644,8 +646,8 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         if (warp >= 4) {  // O^T = e^G S Q^T + U^T P^T
             float qh[2][4], ql[2][4], oh[2][4], ol[2][2][4];
             state_times<NF, 2>(qh, ql, aS, sm100::smem_u32(sm.Q), t0, t1, lane);
-            ok = ok && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err, w.wait_ns);
-            __syncthreads();
+            ok = sm100::mbar_wait(&sm.bar[kBarP], parity, w.err, w.wait_ns);
+            if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, k_turn, c, w.err);
             __syncthreads();
             times_triangle<true, 2, 2>(oh, ol, sm100::smem_u32(sm.W), aP, t0, t1, lane);
 #pragma unroll
@@ -689,8 +691,8 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
                             be.y * (__bfloat162float(sm.V[tok + 1][n]) - y));
             }
         }
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns);
-        __syncthreads();
+        ok = sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns);
+        if (!__syncthreads_and(ok)) return chain_leave(sm, p, c, k_turn, SAVE ? -1 : c, w.err);
         // U^T = (beta Y)^T T^T
         float uh[2][4], ul[2][2][4];
         times_triangle<true, 3, 3>(uh, ul, aR, aT, t0, t1, lane);
@@ -716,8 +718,6 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.S_out + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
-    // the last waits' answers: nobody reads buffers any more, so every thread may report for itself
-    if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
 template <int NF>
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         const int rows = (int)min((long long)C, r.len - c * C);
         ok = ok && sm100::mbar_wait(&sm.bar[kBarK + b], (uint32_t)(turn >> 1) & 1, w.err, w.wait_ns) &&
              sm100::mbar_wait(&sm.bar[kBarV], parity, w.err, w.wait_ns) && sm100::mbar_wait(&sm.bar[kBarP], parity, w.err, w.wait_ns);
-        if (!__syncthreads_and(ok)) return chain_leave(sm, p, turn, (int)turn, w.err);
+        if (!__syncthreads_and(ok)) return chain_leave(sm, p, turn, turn, turn, w.err);
         if (fetcher && c > 0) fetch.k(b ^ 1, first_row(c - 1), index(c - 1));
         if (rows < C) {
             zero_tail(sm.K[b], kSlabs, 8, rows);
@@ -776,8 +776,9 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
             zero_tail(&sm.V[0][0], 1, NV / 8, rows);
             __syncthreads();
         }
+        const long long k_turn = c > 0 ? turn + 1 : turn;
         if (warp == 4) {
-            __syncthreads();
+            if (!__syncthreads_and(true)) return chain_leave(sm, p, turn, k_turn, turn, w.err);
             if (fetcher && c > 0) fetch.v(first_row(c - 1), false);
             __syncthreads();
             if (fetcher && c > 0) fetch.t(w.Tt + index(c - 1) * 3 * kUnits * 32);
@@ -809,8 +810,8 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
                             eg.y * __bfloat162float(sm.V[tok + 1][n]));
             }
         }
-        ok = ok && sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns);
-        __syncthreads();
+        ok = sm100::mbar_wait(&sm.bar[kBarT], parity, w.err, w.wait_ns);
+        if (!__syncthreads_and(ok)) return chain_leave(sm, p, turn, k_turn, turn, w.err);
         // dR^T = dU^T T
         float rh[2][4], rl[2][2][4];
         times_triangle<false, 3, 3>(rh, rl, aR, aT, t0, t1, lane);
@@ -847,7 +848,6 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
         st.each(warp, lane, [&](int n, int col, float &x, float &y) {
             *reinterpret_cast<float2 *>(p.dS_in + soff + (size_t)n * DK + col) = make_float2(x, y);
         });
-    if (!ok && p.status) atomicOr(p.status, GDN_SEQ_TIMEOUT);
 }
 
 // ---------------------------------------------------------------- a warp a slice
@@ -882,12 +882,12 @@ template <int NF, bool BWD> struct WalkFetch {
     __device__ __forceinline__ void k(int b, int row, size_t idx) const {  // and the gates
         uint64_t *bar = &sm.bar[kBarK + b];
         sm100::mbar_arrive_expect_tx(bar, kTileBytes + 3 * C * 4);
-        if (!w.drop || blockIdx.x) tile(sm.K[b], &maps.k, bar, row);
+        if (w.drop != 1 || blockIdx.x) tile(sm.K[b], &maps.k, bar, row);
         sm100::bulk_copy_g2s(&sm.gates[b][0][0], w.gates + idx * 3 * C, 3 * C * 4, bar);
     }
     __device__ __forceinline__ void t(const uint2 *src) const {
         sm100::mbar_arrive_expect_tx(&sm.bar[kBarT], sizeof(sm.T));
-        sm100::bulk_copy_g2s(sm.T, src, sizeof(sm.T), &sm.bar[kBarT]);
+        if (w.drop != 2 || blockIdx.x) sm100::bulk_copy_g2s(sm.T, src, sizeof(sm.T), &sm.bar[kBarT]);
     }
     // forwards (not SAVE): Q and P, read at a step's end.  Backwards Q alone.
     __device__ __forceinline__ void qp(const uint2 *src, int row) const {

@@ -123,3 +123,30 @@ def test_sequences_out_of_order(cu, dtype):
         assert not x[left].any()
     close(got[5][run], want[5], tol32(dk, T, 4), "dS_in")
     assert not got[5][skipped].any()
+
+
+# ---------------------------------------------------------------- waits that give up in the middle of a step
+@pytest.mark.gpu
+@pytest.mark.parametrize("seqs", [2, 75])  # four warps a slice, and one
+def test_a_wait_inside_a_step_gives_up(seqs, monkeypatch):
+    """The first block's T is never fetched: its warps leave together, the status says so, and the next call is right."""
+    H, L, d, dv = 4, 150, 64, 48
+    q, k, v, alpha, beta = [t.cuda().reshape(seqs, L, *t.shape[1:]) for t in draw(seqs * L, H, H, d, dv, "bf16", 83)]
+    do = torch.randn_like(v)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def both():
+        return [*g.gdn_packed(q, k, v, alpha, beta, return_state=True, status=status), *g.gdn_bwd(q, k, v, alpha, beta, do)]
+
+    want = both()
+    assert int(status) == 0
+    monkeypatch.setenv("GDN_DEBUG_DROP_SIGNAL", "2")
+    monkeypatch.setenv("GDN_DEBUG_WAIT_LIMIT_US", "1000")
+    g.gdn_packed(q, k, v, alpha, beta, status=status)
+    assert int(status) == binding.GDN_SEQ_TIMEOUT
+    g.gdn_bwd(q, k, v, alpha, beta, do, status=status)
+    assert int(status) == binding.GDN_SEQ_TIMEOUT
+    monkeypatch.undo()
+    for x, y in zip(both()[:7], want):
+        assert torch.equal(x, y)
+    assert int(status) == 0
