@@ -28,8 +28,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include "gates.cuh"
-#include "seq_internal.h"
+#include "seq_gates.cuh"
 #include "seq_mma.cuh"
 
 namespace gdn {
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * lane + e;
             const size_t at = (size_t)(ch.first + i) * p.H + h;
-            g[e] = i < ch.rows ? fmax(log_gate<double>(p.alpha[at]), (double)floor_log) : 0.0;
+            g[e] = i < ch.rows ? seq_log_gate(p.alpha[at], floor_log) : 0.0;
             b[e] = i < ch.rows ? p.beta[at] : 0.f;
         }
         double run = g[0] + g[1];

@@ -181,6 +181,10 @@ size_t seq_bwd_workspace(const SeqProblem &p, void *base, SeqWork *w);
 
 constexpr float kSeqBwdLogFloor = -60.f;  // log alpha in gdn_bwd; see gdn.h
 
+// alpha as the token-by-token kernels multiply by it: one that is negative, which the kernels in log space cannot hold, is
+// not a number in either, so that a gate gone wrong shows the same in all of them.
+__device__ __forceinline__ float seq_alpha(float a) { return a >= 0.f ? a : __int_as_float(0x7fffffff); }
+
 // gdn_bwd on the CUDA cores (seq_simt.cu).
 cudaError_t launch_seq_bwd_simt(const SeqProblem &p, void *ws, cudaStream_t s);
 // Zeros in the gradients of rows that no sequence covers; with cu_seqlens only.

@@ -84,7 +84,7 @@ template <typename T, int NF> struct Token {
 #pragma unroll
         for (int j = 0; j < NF; ++j) q[j] = *reinterpret_cast<const Piece *>(qp + 16 * j);
         v = to_f(((const T *)p.v)[tok * p.v_stride + (size_t)h * p.dv + r]);
-        alpha = p.alpha[tok * p.H + h];
+        alpha = seq_alpha(p.alpha[tok * p.H + h]);
         beta = p.beta[tok * p.H + h];
     }
 };
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant_
             const int i = j * kManyThreads + threadIdx.x;
             sv[b][i / 16][i % 16] = nv[j];
         }
-        if (threadIdx.x < 2 * kTok) sg[b][threadIdx.x / 2][threadIdx.x & 1] = ng;
+        if (threadIdx.x < 2 * kTok) sg[b][threadIdx.x / 2][threadIdx.x & 1] = threadIdx.x & 1 ? ng : seq_alpha(ng);
     };
     T *out = (T *)p.o + (range.first * p.H + h) * p.dv + r0 + lr;
     const size_t out_step = (size_t)p.H * p.dv;

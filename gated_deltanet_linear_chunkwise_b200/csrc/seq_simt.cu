@@ -22,8 +22,7 @@
 // a chunk.  This file serves fp32 inputs (and calls without tokens); its bound is the fp32 pipe.
 #include <cuda_bf16.h>
 
-#include "gates.cuh"
-#include "seq_internal.h"
+#include "seq_gates.cuh"
 
 namespace gdn {
 namespace {
@@ -88,7 +87,7 @@ __global__ void __launch_bounds__(256) k_prep(const __grid_constant__ SeqProblem
     if (tid < C) {
         const bool on = tid < ch.rows;
         const size_t g = (size_t)(ch.first + tid) * p.H + h;
-        sG[tid] = on ? fmax(log_gate<double>(p.alpha[g]), (double)kSeqBwdLogFloor) : 0.0;
+        sG[tid] = on ? seq_log_gate(p.alpha[g], kSeqBwdLogFloor) : 0.0;
         sBeta[tid] = on ? p.beta[g] : 0.f;
     }
     __syncthreads();
@@ -319,7 +318,7 @@ __global__ void __launch_bounds__(256) k_grads(const __grid_constant__ SeqProble
         t.eg[tid] = w.eg[idx * C + tid];
         t.el[tid] = w.el[idx * C + tid];
         t.beta[tid] = on ? p.beta[g] : 0.f;
-        sG[tid] = on ? fmax(log_gate<double>(p.alpha[g]), (double)kSeqBwdLogFloor) : 0.0;
+        sG[tid] = on ? seq_log_gate(p.alpha[g], kSeqBwdLogFloor) : 0.0;
     }
     __syncthreads();
     if (tid == 0)

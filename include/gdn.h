@@ -342,6 +342,9 @@ size_t gdn_workspace_bytes(int B, int H, long long T, int frame_len, int d_k, in
  * the order of their rows and share none.  GDN_SEQ_TIMEOUT: a bounded
  * device-side wait gave up and the outputs are not valid.
  *
+ * An alpha that is negative or not a number makes the sequence's state, outputs
+ * and gradients of that head from there on not a number, in every kernel.
+ *
  * Calls are asynchronous on `stream`, whose device must be the current one.
  * The same call gives the same bits: no result depends on the order in which
  * blocks run.  (The same sequence in another batch may take another kernel.)

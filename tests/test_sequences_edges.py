@@ -150,3 +150,33 @@ def test_a_wait_inside_a_step_gives_up(seqs, monkeypatch):
     for x, y in zip(both()[:7], want):
         assert torch.equal(x, y)
     assert int(status) == 0
+
+
+# ---------------------------------------------------------------- gates that are no numbers
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate,value", [("alpha", float("nan")), ("alpha", -0.5), ("alpha", float("inf")), ("beta", float("nan"))])
+@pytest.mark.parametrize("n,L,dtype", [(3, 150, "bf16"), (75, 40, "bf16"), (20, 5, "bf16"), (3, 150, "fp32")],
+                         ids=["four warps a slice", "a warp a slice", "token by token", "fp32"])
+def test_a_bad_gate_shows(gate, value, n, L, dtype):
+    """One head's gate of one token of the second sequence: not finite from there on, and nowhere else."""
+    H, dk, dv, t = 2, 64, 112, L + L // 2
+    q, k, v, alpha, beta = cuda(*draw(n * L, H, H, dk, dv, dtype, 73))
+    do, S0 = torch.randn_like(v), torch.randn(n, H, dv, dk, device="cuda")
+    cu = torch.arange(0, n * L + 1, L, dtype=torch.int32, device="cuda")
+
+    def everything():
+        Sd = S0.clone()  # and the token alone, as a decode step
+        step = [x.unflatten(0, (n, L))[:, L // 2].contiguous() for x in (q, k, v, alpha, beta)]
+        return [*g.gdn_packed(q, k, v, alpha, beta, cu, S0, return_state=True), *g.gdn_decode(*step, Sd),
+                *g.gdn_bwd(q, k, v, alpha, beta, do, cu, S0)]
+
+    clean = everything()
+    {"alpha": alpha, "beta": beta}[gate][t, 1] = value
+    dirty = everything()
+    for x, y in zip(clean, dirty):
+        one = L if x.shape[0] == n * L else 1
+        assert torch.equal(x[:one], y[:one]) and torch.equal(x[2 * one:], y[2 * one:])
+        assert torch.equal(x[one:2 * one, 0], y[one:2 * one, 0])  # the other head
+    o, S, o1, S1, dq, dk_, dv_, da, db, dS = dirty
+    for x in (o[t:2 * L, 1], S[1, 1], o1[1, 1], S1[1, 1], dq[t:2 * L, 1], dv_[L:t, 1], da[t, 1], dS[1, 1]):
+        assert not torch.isfinite(x.double()).any()
