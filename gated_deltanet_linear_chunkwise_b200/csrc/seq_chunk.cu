@@ -62,6 +62,7 @@ struct ChunkWork {
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
     int *order;              // [n_seqs]: the sequences, the longest first; -1 - s of one that starts inside an earlier one
+    unsigned char *good;     // [n_seqs]: its rows are in order, by themselves and among the others
     SeqChunk *chunks;        // gdn_bwd: [chunks], what seq_chunk finds
     uint64_t wait_ns;        // limit of the bounded waits
     int drop;                // debug: the first block's K (1) or T (2) is never fetched, so its wait gives up
@@ -69,7 +70,7 @@ struct ChunkWork {
 
 // The chains' blocks start with the longest sequences: a long one that starts last runs alone (16384 tokens in 24
 // sequences of 44 to 1971: 421 us against 505 in their order).  A sequence's place is the number of longer ones, ties by index.
-__device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order, int *len) {  // len: room for 2048
+__device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order, unsigned char *good, int *len) {  // len: room for 2048
     const bool sort = p.cu && p.n_seqs <= 2048;
     bool odd = false;
     if (p.cu)
@@ -85,13 +86,26 @@ __device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order,
             place = 0;
             for (int j = 0; j < p.n_seqs; ++j) place += len[j] > len[s] || (len[j] == len[s] && j < s);
         }
-        bool late = false;
+        bool late = false, wrong = false;
         if (odd) {
             const SeqRange r = seq_rows(p, s);
+            wrong = r.bad;
             for (int j = 0; j < s && r.len > 0; ++j) late |= seq_reaches(p, j, r.first);
         }
         order[place] = late ? -1 - s : s;
+        good[s] = !late && !wrong;
     }
+}
+
+// A sequence's rows and slot with all bits but that of a start inside an earlier one; called by a whole block.
+__device__ __forceinline__ SeqRange seq_place(const SeqProblem &p, int s, const unsigned char *good) {
+    SeqRange r = seq_rows(p, s);
+    if (p.slots) {
+        const int slot = p.slots[s];
+        r.bad |= seq_slot_bits(p, s, slot, [&](int i) { return good[i] != 0; });
+        r.slot = r.bad || slot < 0 ? -1 : slot;
+    }
+    return r;
 }
 
 // dS_in's columns of a sequence that starts inside an earlier one (NULL in a forward call), by a whole block.
@@ -116,7 +130,7 @@ __global__ void __launch_bounds__(128) k_prep(const __grid_constant__ SeqProblem
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk), tid = threadIdx.x, lane = tid & 31, warp = warp_number();
     if (blockIdx.x == gridDim.x - 1) {  // one block more than chunks
         if (tid == 0) *w.err = 0;
-        order_sequences(p, w.order, reinterpret_cast<int *>(room));
+        order_sequences(p, w.order, w.good, reinterpret_cast<int *>(room));
         return;
     }
     const SeqChunk ch = seq_chunk(p, c);
@@ -583,12 +597,12 @@ __global__ void __launch_bounds__(chain_threads(!SAVE), 1) k_chunk_fwd(const __g
     const int groups = p.dv / NV, next = w.order[blockIdx.x / (p.H * groups)], h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NV;
     const int hk = h / (p.H / p.Hk), lane = threadIdx.x & 31, warp = warp_number();
     if (next < 0) {
-        seq_report(p, kSeqLate, h == 0 && c0 == 0 && threadIdx.x == 0);
+        seq_report(p, GDN_SEQ_BAD_ROWS, h == 0 && c0 == 0 && threadIdx.x == 0);
         return no_state(p, -1 - next, h, c0, NV);
     }
     const int s = next;
-    const SeqRange r = seq_range(p, s);
-    seq_report(p, r, h == 0 && c0 == 0 && threadIdx.x == 0);
+    const SeqRange r = seq_place(p, s, w.good);
+    seq_report(p, r.bad, h == 0 && c0 == 0 && threadIdx.x == 0);
     if (r.slot < 0 || r.len < p.min_len) return;
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, s, r.first);
     const size_t soff = (((size_t)r.slot * p.H + h) * p.dv + c0) * DK;
@@ -1050,11 +1064,11 @@ __global__ void __launch_bounds__(kWalkThreads, 2) k_walk_fwd(const __grid_const
     const WalkPlace at = walk_place(p, w.order);
     const int lane = threadIdx.x & 31, n0 = lane / 4, j0 = 2 * (lane & 3), col = at.c0 + 16 * at.slice;
     if (at.late) {
-        seq_report(p, kSeqLate, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
+        seq_report(p, GDN_SEQ_BAD_ROWS, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
         return no_state(p, at.s, at.h, at.c0, 16 * at.slices);
     }
-    const SeqRange r = seq_range(p, at.s);
-    seq_report(p, r, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
+    const SeqRange r = seq_place(p, at.s, w.good);
+    seq_report(p, r.bad, at.h == 0 && at.c0 == 0 && threadIdx.x == 0);
     if (r.slot < 0 || r.len < p.min_len) return;
     const long long n_chunks = seq_chunks_of(r.len), base = seq_chunk_base(p, at.s, r.first);
     const WalkFetch<NF, false> fetch = {sm, maps, w, at.hk, at.h, at.c0};
@@ -2050,6 +2064,7 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
     w.gates = (float *)take(n * 3 * C * 4);
     w.err = (int *)take(sizeof(int));
     w.order = (int *)take((size_t)p.n_seqs * sizeof(int));
+    w.good = (unsigned char *)take((size_t)p.n_seqs);
     if (!bwd) {
         w.P = (uint2 *)take(2 * frag);
     } else {

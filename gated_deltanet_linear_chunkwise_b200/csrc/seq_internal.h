@@ -81,26 +81,43 @@ __device__ __forceinline__ bool seq_late(const SeqProblem &p, int s) {
 __device__ constexpr SeqRange kSeqLate = {0, 0, -1, GDN_SEQ_BAD_ROWS};
 __device__ __forceinline__ SeqRange seq_rows_in_order(const SeqProblem &p, int s) { return seq_late(p, s) ? kSeqLate : seq_rows(p, s); }
 
-// A sequence's range with its slot looked up and checked; called by a whole block (it votes on an
-// earlier sequence of the same slot, so that of two writers of one state only the first runs).
-__device__ __forceinline__ SeqRange seq_range(const SeqProblem &p, int s) {
-    SeqRange r = seq_rows(p, s);
-    if (p.slots) {
-        const int slot = p.slots[s];
-        bool same = false;
-        if (slot >= 0)
-            for (int i = threadIdx.x; i < s; i += blockDim.x) same |= p.slots[i] == slot;
-        same = __syncthreads_or(same);
-        if (slot >= p.n_slots) r.bad |= GDN_SEQ_BAD_SLOT;
-        if (same) r.bad |= GDN_SEQ_SAME_SLOT;
-        r.slot = (r.bad || slot < 0) ? -1 : slot;
+// The slot's bits of a sequence; called by a whole block (it votes on an earlier sequence of the same slot whose rows are
+// good, so that of two writers of one state only the first runs).
+template <typename Good> __device__ __forceinline__ int seq_slot_bits(const SeqProblem &p, int s, int slot, Good good) {
+    if (!p.slots) return 0;
+    bool same = false;
+    if (slot >= 0)
+        for (int i = threadIdx.x; i < s; i += blockDim.x) same |= p.slots[i] == slot && good(i);
+    return (__syncthreads_or(same) ? GDN_SEQ_SAME_SLOT : 0) | (slot >= p.n_slots ? GDN_SEQ_BAD_SLOT : 0);
+}
+
+// All bits of a sequence (any of them: it is skipped), where nothing is known of the others; called by a whole block.  What
+// is rarely true is looked into behind one vote.  (The bits alone: a range put together on several paths cost k_many 340
+// bytes of spills.)
+__device__ __forceinline__ int seq_refused(const SeqProblem &p, int s, int slot) {
+    int bad = seq_rows(p, s).bad;
+    bool odd = false;
+    if (p.cu || p.slots)
+        for (int i = threadIdx.x; i < s; i += blockDim.x) {
+            if (p.cu) odd |= seq_rows(p, i).bad != 0;
+            if (p.slots) odd |= p.slots[i] == slot;
+        }
+    if (__syncthreads_or(odd)) {
+        if (p.cu && seq_late_odd(p, s)) bad |= GDN_SEQ_BAD_ROWS;
+        bad |= seq_slot_bits(p, s, slot, [&](int i) {
+            const SeqRange r = seq_rows(p, i);
+            bool good = !r.bad;
+            if (p.cu && r.len > 0)
+                for (int j = 0; j < i; ++j) good &= !seq_reaches(p, j, r.first);
+            return good;
+        });
     }
-    return r;
+    return p.slots && slot >= p.n_slots ? bad | GDN_SEQ_BAD_SLOT : bad;
 }
 
 // One block of a launch reports a sequence's bits.
-__device__ __forceinline__ void seq_report(const SeqProblem &p, const SeqRange &r, bool reporter) {
-    if (r.bad && p.status && reporter) atomicOr(p.status, r.bad);
+__device__ __forceinline__ void seq_report(const SeqProblem &p, int bad, bool reporter) {
+    if (bad && p.status && reporter) atomicOr(p.status, bad);
 }
 
 __device__ __forceinline__ bool seq_starts_zero(const SeqProblem &p, int s) {

@@ -114,9 +114,10 @@ __global__ void __launch_bounds__(kFewThreads) k_few(const __grid_constant__ Seq
     float4 S[NF], next[NF];
     size_t soff = (((size_t)(inside ? slot : 0) * p.H + h) * p.dv + r) * p.dk + part * 4;
     if (inside) load_state(S, p.S_in + soff);
-    const SeqRange range = seq_range(p, s);  // without cu_seqlens: in order
-    seq_report(p, range, rb == 0 && threadIdx.x == 0);
-    if (range.slot < 0) return;
+    const int bad = seq_slot_bits(p, s, slot, [](int) { return true; });
+    seq_report(p, bad, rb == 0 && threadIdx.x == 0);
+    const SeqRange range = seq_rows(p, s);
+    if (bad || slot < 0) return;
     const int last = HEAD ? p.dv - 16 : 0;
     for (int r0 = 0;; r0 += 16) {
         const size_t ahead = soff + (size_t)16 * p.dk;
@@ -153,11 +154,11 @@ __global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant_
     const int s = blockIdx.x / per_seq, rb = blockIdx.x % per_seq;
     const int h = rb / (p.dv / 16), r0 = (rb % (p.dv / 16)) * 16, hk = h / (p.H / p.Hk);
     const int lr = threadIdx.x / 4, part = threadIdx.x & 3;
-    if (seq_late(p, s)) return seq_report(p, kSeqLate, rb == 0 && threadIdx.x == 0);
-    const SeqRange range = seq_range(p, s);
-    seq_report(p, range, rb == 0 && threadIdx.x == 0);
-    if (range.slot < 0 || range.len > p.max_len) return;
-    const size_t soff = (((size_t)range.slot * p.H + h) * p.dv + r0 + lr) * DK + part * 4;
+    const int slot = p.slots ? p.slots[s] : s, bad = seq_refused(p, s, slot);
+    seq_report(p, bad, rb == 0 && threadIdx.x == 0);
+    const SeqRange range = seq_rows(p, s);
+    if (bad || slot < 0 || range.len > p.max_len) return;
+    const size_t soff = (((size_t)slot * p.H + h) * p.dv + r0 + lr) * DK + part * 4;
     float4 S[NF];
     const bool zero = seq_starts_zero(p, s);
 #pragma unroll

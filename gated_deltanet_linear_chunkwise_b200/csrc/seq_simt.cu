@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) k_chain_fwd(const __grid_constant__ SeqPr
     const int groups = p.dv / NC, s = blockIdx.x / (p.H * groups), h = blockIdx.x / groups % p.H, c0 = blockIdx.x % groups * NC;
     const int tid = threadIdx.x, pk = p.dk + 1, dv = p.dv;
     const SeqRange r = seq_rows_in_order(p, s);
-    seq_report(p, r, h == 0 && c0 == 0 && tid == 0);
+    seq_report(p, r.bad, h == 0 && c0 == 0 && tid == 0);
     if (r.slot < 0) return;
     const ChainTile t = chain_tile(sm, p.dk);
     for (int i = tid; i < NC * p.dk; i += blockDim.x)

@@ -336,11 +336,12 @@ size_t gdn_workspace_bytes(int B, int H, long long T, int frame_len, int d_k, in
  * Device-side checks.  slots and cu_seqlens are read on the GPU only.  A
  * sequence is skipped like a padding entry, and its bit set in *status_dev,
  * when its slot is >= n_slots (GDN_SEQ_BAD_SLOT), when an earlier sequence
- * has the same slot (GDN_SEQ_SAME_SLOT; the first one runs), or when its rows
- * are not an ordered range inside the n_tokens rows or begin before the end of
- * an earlier sequence whose rows are one (GDN_SEQ_BAD_ROWS): sequences lie in
- * the order of their rows and share none.  GDN_SEQ_TIMEOUT: a bounded
- * device-side wait gave up and the outputs are not valid.
+ * whose rows are good has the same slot (GDN_SEQ_SAME_SLOT; the first one
+ * runs), or when its rows are not an ordered range inside the n_tokens rows or
+ * begin before the end of an earlier sequence whose rows are one
+ * (GDN_SEQ_BAD_ROWS): sequences lie in the order of their rows and share none.
+ * GDN_SEQ_TIMEOUT: a bounded device-side wait gave up and the outputs are not
+ * valid.
  *
  * An alpha that is negative or not a number makes the sequence's state, outputs
  * and gradients of that head from there on not a number, in every kernel.

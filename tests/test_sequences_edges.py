@@ -180,3 +180,31 @@ def test_a_bad_gate_shows(gate, value, n, L, dtype):
     o, S, o1, S1, dq, dk_, dv_, da, db, dS = dirty
     for x in (o[t:2 * L, 1], S[1, 1], o1[1, 1], S1[1, 1], dq[t:2 * L, 1], dv_[L:t, 1], da[t, 1], dS[1, 1]):
         assert not torch.isfinite(x.double()).any()
+
+
+# ---------------------------------------------------------------- slots of sequences that are skipped
+@pytest.mark.gpu
+@pytest.mark.parametrize("more", [0, 80])  # four warps a slice (bf16), and one
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_skipped_sequence_blocks_no_slot(more, dtype):
+    """Of the sequences of one slot the first whose rows are good runs."""
+    H, Hk, dk, dv = 4, 2, 32, 64
+    cu, slots = [0, 64, 30, 64, 130, 160, 200], [0, 2, 3, 3, 2, 0]  # good, wrong, inside the first, good, good, a slot in use
+    cu, slots = cu + [200 + 30 * (i + 1) for i in range(more)], slots + [6 + i for i in range(more)]
+    N, n = cu[-1], len(slots)
+    run = [0, 3, 4, *range(6, n)]
+    tensors = draw(N, H, Hk, dk, dv, dtype, 91)
+    pool = torch.randn(6 + more, H, dv, dk, generator=torch.Generator().manual_seed(2))
+    at = [slots[s] for s in run]
+    rows, states = token_loop(*(t.double() for t in tensors), pool.double()[at], [cu[s + 1] - cu[s] for s in run], [cu[s] for s in run])
+    want = pool.double()
+    want[at] = torch.stack(states)
+    S, o = pool.cuda(), torch.full(tensors[2].shape, 7.0, dtype=tensors[2].dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    g.gdn_packed(*cuda(*tensors), ints(cu), S, S_out=S, slots=ints(slots), o=o, status=status)
+    assert int(status) == binding.GDN_SEQ_BAD_ROWS | binding.GDN_SEQ_SAME_SLOT
+    close(S, want, tol32(dk, 66), "S")
+    covered = sorted(rows)
+    close(o[covered], torch.stack([rows[t] for t in covered]), tol32(dk, 66), "o")
+    assert (o[[t for t in range(N) if t not in rows]] == 7).all()
