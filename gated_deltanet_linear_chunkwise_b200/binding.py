@@ -430,8 +430,8 @@ def gdn_decode(q, k, v, alpha, beta, S, slots=None, *, o=None, status=None, stre
     h // (H // Hk).  The heads of a token are contiguous; the tokens of q, k, v may be slices of a
     fused projection (equally far apart, a multiple of 16 bytes), but not one row expanded to many.
     S fp32 [n_slots, H, d_v, d_k] holds the states and is updated in place: sequence b's is
-    S[slots[b]] (slots int32 [B]; None: S[b]).  A negative slot is a padding entry: its o rows and
-    every state are left alone.  So is a sequence with a slot >= n_slots or the slot of an earlier
+    S[slots[b]] (slots int32 [B]; None: S[b]).  A negative slot is a padding entry: its o rows (in an o that
+    the call makes they hold nothing) and every state are left alone.  So is a sequence with a slot >= n_slots or the slot of an earlier
     sequence; `status` (a CUDA int32 tensor) then receives GDN_SEQ_BAD_SLOT / GDN_SEQ_SAME_SLOT.
     Returns (o, S).
     """
@@ -467,10 +467,11 @@ def gdn_packed(q, k, v, alpha, beta, cu_seqlens=None, S_in=None, *, S_out=None, 
     q, k [N, Hk, d_k], v [N, H, d_v] (bf16 or fp32), alpha, beta [N, H] fp32; sequence s covers
     the tokens cu_seqlens[s] .. cu_seqlens[s+1] - 1 (int32 [n + 1], on the GPU and read there only).
     Without cu_seqlens: [B, T, heads, d] tensors, B sequences of T tokens.  Heads, strides and slots
-    as in ``gdn_decode``; o rows of tokens that no sequence covers are left as they were.
+    as in ``gdn_decode``; o rows of tokens that no sequence covers are left as they were (in an o that the
+    call makes they hold nothing).
     S_in, S_out fp32 [n_slots, H, d_v, d_k] hold the states that enter (None: zeros) and leave
-    (None: not stored, unless ``return_state`` makes a tensor of n_slots = n); they may be the same
-    tensor.  ``fresh`` (bool or uint8 [n]) starts the marked sequences from zero without reading S_in.
+    (None: not stored, unless ``return_state`` makes a tensor of n_slots = n, zeros where a sequence is
+    skipped); they may be the same tensor.  ``fresh`` (bool or uint8 [n]) starts the marked sequences from zero without reading S_in.
     ``status`` may also receive GDN_SEQ_BAD_ROWS (a range out of order, out of the tensors or into an
     earlier sequence's).
     Returns (o, S_out or None).
@@ -490,7 +491,8 @@ def gdn_packed(q, k, v, alpha, beta, cu_seqlens=None, S_in=None, *, S_out=None, 
             o = torch.empty(v.shape, dtype=dtype, device=dev)
         if S_out is None and return_state:
             _need(slots is None, 1, "return_state makes one state a sequence: with slots pass S_out")
-            S_out = torch.empty((n, H, d_v, d_k), dtype=torch.float32, device=dev)
+            # a skipped sequence's entry is not written
+            S_out = (torch.empty if cu_seqlens is None else torch.zeros)((n, H, d_v, d_k), dtype=torch.float32, device=dev)
         a.o = _plain("o", o, dtype, v.shape, dev)
         pool = S_in if S_in is not None else S_out
         a.n_slots = n if pool is None else pool.shape[0] if pool.dim() else 0

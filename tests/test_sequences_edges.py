@@ -208,3 +208,36 @@ def test_a_skipped_sequence_blocks_no_slot(more, dtype):
     covered = sorted(rows)
     close(o[covered], torch.stack([rows[t] for t in covered]), tol32(dk, 66), "o")
     assert (o[[t for t in range(N) if t not in rows]] == 7).all()
+
+
+# ---------------------------------------------------------------- what no sequence covers, in a graph of gradients
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_autograd_of_rows_that_no_sequence_covers(dtype):
+    """Rows behind the last sequence and of a wrong range are zeros and stay out of every gradient, whatever the memory held."""
+    N, H, Hk, dk, dv = 210, 4, 2, 48, 64
+    cu = torch.tensor([0, 70, 400, 80, 200], dtype=torch.int32, device="cuda")  # [70, 400) and [400, 80) are wrong
+    covered = [*range(70), *range(80, 200)]
+    left = [t for t in range(N) if t not in covered]
+    tensors = draw(N, H, Hk, dk, dv, dtype, 95)
+    S_in = torch.randn(4, H, dv, dk, generator=torch.Generator().manual_seed(1))
+    mine = [t.cuda().requires_grad_(True) for t in (*tensors, S_in)]
+    for shape, t in ((tensors[2].shape, tensors[2].dtype), (S_in.shape, torch.float32)):
+        held = [torch.full(shape, float("nan"), dtype=t, device="cuda") for _ in range(4)]
+        del held  # the allocator hands it out again
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, S = g.gated_delta_rule(*mine, cu, status=status)
+    assert int(status) == binding.GDN_SEQ_BAD_ROWS
+    assert not o[left].any() and not S[[1, 2]].any()
+    status.zero_()
+    ((o.float() ** 2).sum() + S.sum()).backward()
+    assert int(status) == binding.GDN_SEQ_BAD_ROWS
+    do = 2 * o.detach()
+    want = exact_grads(tensors, [0, 80], [70, 120], S_in[[0, 3]], do.cpu(), torch.ones(2, H, dv, dk))
+    for name, x, y in zip(("q", "k", "v", "alpha", "beta"), mine, want):
+        close(x.grad, y, tol32(dk, 120, 4), name)
+        assert not x.grad[left].any()
+    close(mine[5].grad[[0, 3]], want[5], tol32(dk, 120, 4), "S_in")
+    assert not mine[5].grad[[1, 2]].any()
+    _, S = g.gdn_packed(*(t.detach() for t in mine[:5]), cu, return_state=True)
+    assert not S[[1, 2]].any()
