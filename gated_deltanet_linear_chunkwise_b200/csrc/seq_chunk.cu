@@ -1625,6 +1625,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
         float *M = reinterpret_cast<float *>(sm + at.M);
         const uint32_t aPA = base + at.PA + role * 2 * C * 128;
         const float be0 = role ? gates[2][i0] : 1.f, be1 = role ? gates[2][i0 + 8] : 1.f;
+        float part[2] = {};  // rowsum(dA o K K^T) reaches dbeta: from the fp32 values, before they become terms
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             const float gm[4] = {gam[t].x, gam[t].y, gam[t].z, gam[t].w};
@@ -1638,6 +1639,7 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                     x[e] = gm[2 * half + e] * (hi[t][2 * half + e] + lo[t][2 * half + e]);
                     if (role) x[e] = j + e < i ? -x[e] : 0.f;
                 }
+                if (role) part[half] += x[0] * kk[t][2 * half] + x[1] * kk[t][2 * half + 1];
                 uint32_t s[2];
                 split(x[0], x[1], s);
 #pragma unroll
@@ -1662,7 +1664,6 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
                 }
         }
         // rows x K
-        float part[2] = {};
 #pragma unroll
         for (int g = 0; g < NF; ++g) {
             float x[2][4];
@@ -1685,10 +1686,6 @@ __global__ void __launch_bounds__(256, 1) k_chunk_grads(const __grid_constant__ 
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    if (role) {
-                        const uint32_t kv = pair(at.K, i0 + 8 * half, 16 * g + 8 * t + j0);
-                        part[half] += low_of(kv) * x[t][2 * half] + high_of(kv) * x[t][2 * half + 1];
-                    }
                     const float be = half ? be1 : be0;
                     acc[2 * g + t][2 * half] = be * x[t][2 * half];
                     acc[2 * g + t][2 * half + 1] = be * x[t][2 * half + 1];

@@ -241,3 +241,21 @@ def test_autograd_of_rows_that_no_sequence_covers(dtype):
     assert not mine[5].grad[[1, 2]].any()
     _, S = g.gdn_packed(*(t.detach() for t in mine[:5]), cu, return_state=True)
     assert not S[[1, 2]].any()
+
+
+# ---------------------------------------------------------------- the gates' gradients of bf16 calls
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 40])  # four warps a slice, and one
+def test_gate_gradients_are_fp32(n):
+    """dalpha and dbeta leave in fp32 and are sums of fp32 accuracy: five sums lie one behind another (state, U, dU, dR, the row
+    sums), each within a half step, 2^-24, of the result's 2-norm.  Operands of two bf16 terms (2^-17 each) are not."""
+    H, Hk, d, L = 4, 2, 112, 140
+    tensors = draw(n * L, H, Hk, d, d, "bf16", 97)
+    do = torch.randn(tensors[2].shape, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16)
+    cu = torch.arange(0, n * L + 1, L, dtype=torch.int32)
+    got = g.gdn_bwd(*cuda(*tensors), do.cuda(), cu.cuda())
+    some = min(n, 3)  # the sequences do not meet
+    want = exact_grads([t[:some * L] for t in tensors], [s * L for s in range(some)], [L] * some, torch.zeros(some, H, d, d), do, torch.zeros(some, H, d, d))
+    for name, x, y in (("dalpha", got[3], want[3]), ("dbeta", got[4], want[4])):
+        off = (x[:some * L].cpu().to(F64) - y).norm() / y.norm()
+        assert off <= 5 * 2.0 ** -24, (name, float(off))
