@@ -158,6 +158,13 @@ def _stream_handle(stream, device):
     return stream.cuda_stream
 
 
+def _written(*tensors):
+    """The caller's tensors that a call has written, told to autograd: a graph that saved one of them
+    raises in its backward pass instead of reading the new values."""
+    import torch
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def gdn_fwd(q, k, v, alpha, beta, frame_len, S_in=None, *, S_out=None, o=None,
             return_state=False, reverse=False, accumulate=False, reset_every=0,
             check_finite=False, workspace=None, stream=None, stage_ms=None, mode="token", gamma=None,
@@ -251,6 +258,7 @@ def gdn_fwd(q, k, v, alpha, beta, frame_len, S_in=None, *, S_out=None, o=None,
     if stage_ms is not None:  # a ctypes float array of NUM_STAGES; the call synchronises
         a.stage_ms = ctypes.cast(stage_ms, ctypes.c_void_p)
     check(load_library().gdn_fwd_ex(ctypes.byref(a)))
+    _written(o, S_out, segment_map)
     return o, S_out
 
 
@@ -267,6 +275,7 @@ def apply_maps(S, maps, *, stream=None):
         raise GdnError(2, "maps must have shape [n, B, H, d_k + d_v, d_k]")
     check(load_library().gdn_apply_maps(_ptr(S), _ptr(maps), maps.shape[0], B, H, d_k, d_v,
                                         _stream_handle(stream, S.device)))
+    _written(S)
     return S
 
 
@@ -297,6 +306,7 @@ def gdn_fwd_host(q, k, v, alpha, beta, frame_len, S_in=None, *, S_out=None, o=No
     check(load_library().gdn_fwd_host(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(S_in),
                                       _ptr(S_out), _ptr(o), B, H, T, int(frame_len), d_k, d_v,
                                       _stream_handle(stream, device)))
+    _written(o, S_out)
     return o, S_out
 
 
@@ -451,12 +461,15 @@ def gdn_decode(q, k, v, alpha, beta, S, slots=None, *, o=None, status=None, stre
     if status is not None:
         a.status_dev = _plain("status", status, torch.int32, (1,), dev)
     with _On(dev, stream) as a.stream:
+        written = (S,)
         if o is None:
             o = torch.empty(v.shape, dtype=dtype, device=dev)
             a.o = o.data_ptr()
         else:
             a.o = _plain("o", o, dtype, v.shape, dev)
+            written = (S, o)
         check((_lib or load_library()).gdn_decode(ctypes.byref(a)))
+    torch._C._increment_version(written)  # as _written, in half its time
     return o, S
 
 
@@ -500,6 +513,7 @@ def gdn_packed(q, k, v, alpha, beta, cu_seqlens=None, S_in=None, *, S_out=None, 
         a.S_out = _plain("S_out", S_out, torch.float32, (a.n_slots, H, d_v, d_k), dev)
         _seq_workspace(a, workspace, dev, 0)
         check(load_library().gdn_packed(ctypes.byref(a)))
+    _written(o, S_out)
     return o, S_out
 
 

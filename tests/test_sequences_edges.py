@@ -259,3 +259,31 @@ def test_gate_gradients_are_fp32(n):
     for name, x, y in (("dalpha", got[3], want[3]), ("dbeta", got[4], want[4])):
         off = (x[:some * L].cpu().to(F64) - y).norm() / y.norm()
         assert off <= 5 * 2.0 ** -24, (name, float(off))
+
+
+# ---------------------------------------------------------------- states that a graph has saved
+@pytest.mark.gpu
+@pytest.mark.parametrize("entry", ["decode", "packed", "packed o", "frames", "maps"])
+def test_a_saved_state_that_is_overwritten_raises(entry):
+    """The backward pass recomputes from S_in: one that a later call has written does not go unnoticed."""
+    B, T, H, d = 2, 64, 2, 64
+    q, k, v, alpha, beta = [t.cuda().reshape(B, T, *t.shape[1:]) for t in draw(B * T, H, H, d, d, "fp32", 99)]
+    S, w = torch.randn(B, H, d, d, device="cuda"), v.clone()
+    leaf = q.clone().requires_grad_(True)
+    for spoil in (False, True):
+        o, _ = g.gated_delta_rule(leaf, k, w, alpha, beta, S)
+        if spoil and entry == "decode":
+            g.gdn_decode(*(x[:, 0].contiguous() for x in (q, k, v, alpha, beta)), S)
+        elif spoil and entry == "packed":
+            g.gdn_packed(q, k, v, alpha, beta, None, S, S_out=S)
+        elif spoil and entry == "packed o":
+            g.gdn_packed(q, k, v, alpha, beta, o=w)
+        elif spoil and entry == "frames":
+            g.gdn_step(q, k, v, alpha, beta, T, S, S_out=S)
+        elif spoil:
+            binding.apply_maps(S, torch.zeros(1, B, H, 2 * d, d, device="cuda"))
+        if not spoil:
+            o.sum().backward()
+            continue
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            o.sum().backward()
