@@ -1986,10 +1986,11 @@ unsigned num_sms() {
 }
 
 // A warp a slice, or four warps on each?  With few slices a step's length counts, and four warps halve it; with many
-// the SMs are full either way and a warp a slice moves less through shared memory.  Measured (20 heads, d = 112, us, a warp / four
-// warps): packed 140 slices 360 / 178, 560 455 / 347, 840 275 / 268, 1120 269 / 360, 5600 123 / 255; bwd 140 1066 / 682, 840
-// 1024 / 1025, 1120 1113 / 1340.
-bool walk(const SeqProblem &p) { return (long long)p.n_seqs * p.H * (p.dv / NV) >= 6ll * num_sms(); }
+// the SMs are full either way and a warp a slice moves less through shared memory.  Measured on 8192 tokens in equal
+// sequences, their gradients on 4096 (us, a warp / four warps): 20 heads, d = 112: 280 slices 387 / 339 and 678 / 651, 560
+// 315 / 339 and 615 / 655, 840 242 / 354 and 532 / 675, 1400 232 / 357 and 557 / 736.  8 heads, d = 128: 256 213 / 171 and
+// 393 / 364, 576 123 / 170 and 301 / 380.  16 heads, d = 64: 256 163 / 172 and 301 / 319, 576 104 / 173 and 259 / 345.
+bool walk(const SeqProblem &p) { return (long long)p.n_seqs * p.H * (p.dv / NV) >= 3ll * num_sms(); }
 unsigned walk_blocks(const SeqProblem &p) {
     return (unsigned)((long long)p.n_seqs * p.H * ((p.dv + 16 * kSlices - 1) / (16 * kSlices)));
 }
