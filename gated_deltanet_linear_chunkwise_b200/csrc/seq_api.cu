@@ -13,10 +13,18 @@ namespace {
 
 enum Which { kDecode, kPacked, kBwd };
 
-// In a batch of short prompts the ones up to this length go token by token and the others in chunks, two launches beside
-// one another's sequences: a chunk step and its block's start take as long as 24 tokens.  Where the average is over
-// kMixed, no more than a few can be short, and the chunks take them all.
-constexpr long long kShort = 24, kMixed = 256;
+// In a batch of short prompts the ones up to short_len() go token by token and the others in chunks, two launches beside one
+// another's sequences: a chunk step and its block's start take as long as about 12 tokens, or 24 where the token loop's blocks
+// are on the SMs together.  Where the average is kMixed or more, few can be short, and the chunks take them all.
+// Measured (us, both / chunks alone), up to 12: 20 heads, d = 112: 37 ragged prompts of 1201 tokens 83.6 / 101.8, 59 of 2537
+// 149 / 165, 60 of 8 tokens with 8 of 200 156 / 186; 8 heads, d = 128: 35 of 455 43 / 46, 60 of 8 with 8 of 200 94 / 87.
+// Up to 24 instead, 60 of 24 tokens with 8 of 200: 238 / 186 and 137 / 87; but 4 heads, d = 96, 9 of 72: 12 / 24 (up to 12: 23).
+// Averages of 64 (8 of 10 tokens, 16 long ones) 82.2 / 82.9 and 46 / 44, of 128 120 / 104 and 57 / 53, of 256 197 / 182, 98 / 88.
+constexpr long long kMixed = 48;
+long long short_len(const gdn::SeqProblem &p) {
+    return (long long)p.n_seqs * p.H * (p.dv / 16) <= 6ll * gdn::seq_num_sms() ? 24 : 12;
+}
+constexpr long long kEqual = 24;  // see chunked()
 
 int fail(int status, const char *fmt, ...) {
     char text[400];
@@ -142,13 +150,17 @@ int check(const gdn_seq_args &a, Which which, gdn::SeqProblem &p) {
 }
 
 // Which form serves a gdn_packed or gdn_bwd call.  The tensor cores take bf16 operands.  Few tokens for the states that
-// they pass through go token by token: about 0.36 us a token of the longest sequence, against 18 us and 2 us a sequence
+// they pass through go token by token: about 0.25 us a token of the longest sequence, against 16 us and 2 us a sequence
 // of 140 slices (16 columns of a head's state) in chunks.  The longest sequence is not known on the host, so the rule
-// takes all tokens for one's.  Measured (20 heads, d = 112, us, recurrent / chunks): 1 sequence of 16 tokens 8.5 / 19, of 64
-// 25 / 18; 40 sequences with 128 tokens 31 / 91, with 400 54 / 92, with 800 95 / 92.
+// takes all tokens for one's (of equal sequences it leaves the token loop too early, by a factor of two and more).  Measured
+// on equal sequences (us, token by token / chunks): 20 heads, d = 112: 1 of 32 tokens 10 / 17, of 64 18 / 16; 16 of together 128
+// 19 / 44, 256 30 / 44, 512 51 / 45; 40 of 200 34 / 90, 400 50 / 91, 800 83 / 91.  8 heads, d = 128: 1 of 32 11 / 17, of 64 21 / 17;
+// 16 of 128 13 / 28, 512 33 / 28; 40 of 400 26 / 49, 800 45 / 48.
+// Without cu_seqlens every length is known: up to kEqual tokens go token by token (16 x 16 tokens 30 / 44 and 19 / 28, 40 x 20
+// 83 / 91 and 45 / 48, 16 x 32 51 / 45 and 33 / 28).
 bool chunked(const gdn::SeqProblem &p, Which which) {
     if (p.dtype != GDN_DTYPE_BF16 || p.n_tokens == 0) return false;
-    if (which == kPacked && !p.cu) return p.seq_len > kShort;
+    if (which == kPacked && !p.cu) return p.seq_len > kEqual;
     return which == kBwd || p.n_tokens >= 50 + (long long)p.n_seqs * p.H * (p.dv / 16) / 20;
 }
 
@@ -189,9 +201,10 @@ int run(const gdn_seq_args *a, Which which) noexcept {
         if (which == kBwd) e = chunked(p, which) ? gdn::launch_seq_bwd_chunk(p, ws, s) : gdn::launch_seq_bwd_simt(p, ws, s);
         else if (p.n_seqs && which == kPacked && chunked(p, which)) {
             if (p.cu && p.n_tokens < kMixed * p.n_seqs) {
-                p.max_len = kShort;
+                const long long n = short_len(p);
+                p.max_len = n;
                 e = gdn::launch_seq_recurrent(p, false, s);
-                p.min_len = kShort + 1;
+                p.min_len = n + 1;
             }
             if (e == cudaSuccess) e = gdn::launch_seq_chunk(p, ws, s);
         }

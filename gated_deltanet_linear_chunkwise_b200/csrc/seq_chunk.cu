@@ -1979,18 +1979,12 @@ bool make_maps(ChainMaps &m, const SeqProblem &p, const void *v, long long v_str
            seq_row_map(&m.v, v, p.n_tokens, v_stride, p.H, p.dv, v_cols);
 }
 
-unsigned num_sms() {
-    int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return (unsigned)n;
-}
-
 // A warp a slice, or four warps on each?  With few slices a step's length counts, and four warps halve it; with many
 // the SMs are full either way and a warp a slice moves less through shared memory.  Measured on 8192 tokens in equal
 // sequences, their gradients on 4096 (us, a warp / four warps): 20 heads, d = 112: 280 slices 387 / 339 and 678 / 651, 560
 // 315 / 339 and 615 / 655, 840 242 / 354 and 532 / 675, 1400 232 / 357 and 557 / 736.  8 heads, d = 128: 256 213 / 171 and
 // 393 / 364, 576 123 / 170 and 301 / 380.  16 heads, d = 64: 256 163 / 172 and 301 / 319, 576 104 / 173 and 259 / 345.
-bool walk(const SeqProblem &p) { return (long long)p.n_seqs * p.H * (p.dv / NV) >= 3ll * num_sms(); }
+bool walk(const SeqProblem &p) { return (long long)p.n_seqs * p.H * (p.dv / NV) >= 3ll * seq_num_sms(); }
 unsigned walk_blocks(const SeqProblem &p) {
     return (unsigned)((long long)p.n_seqs * p.H * ((p.dv + 16 * kSlices - 1) / (16 * kSlices)));
 }
@@ -2084,6 +2078,12 @@ ChunkWork carve(const SeqProblem &p, void *base, bool bwd, size_t *total) {
 }
 
 }  // namespace
+
+int seq_num_sms() {
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
 
 size_t seq_chunk_workspace(const SeqProblem &p, bool bwd) {
     size_t n;

@@ -215,6 +215,8 @@ size_t seq_chunk_workspace(const SeqProblem &p, bool bwd);
 cudaError_t launch_seq_chunk(const SeqProblem &p, void *ws, cudaStream_t s);
 cudaError_t launch_seq_bwd_chunk(const SeqProblem &p, void *ws, cudaStream_t s);
 
+int seq_num_sms();  // of the current device
+
 // The recurrent form (seq_recurrent.cu).  `few`: one or a few tokens of each sequence.
 cudaError_t launch_seq_recurrent(const SeqProblem &p, bool few, cudaStream_t s);
 
