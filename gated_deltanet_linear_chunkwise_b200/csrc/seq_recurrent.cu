@@ -68,7 +68,6 @@ __device__ __forceinline__ float token_step(float4 (&S)[NF], const Piece (&k)[NF
     return quad_sum((a.x + a.y) + (a.z + a.w));
 }
 
-constexpr long long kManyHeads = 1480;
 constexpr int kFewThreads = 64;  // 16 rows: d_v is a multiple of 16, so a block stays in one head
 
 // A lane's pieces of a token's k and q rows as they lie in memory, and its row's v and gates.
@@ -248,9 +247,12 @@ __global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant_
 
 template <typename T, int NF> cudaError_t launch(const SeqProblem &p, bool few, cudaStream_t s) {
     const long long heads = (long long)p.n_seqs * p.H, blocks = heads * (p.dv / 16);
-    // A block a head once ten of them are on every SM: 256 sequences x 20 heads, d = 112: 92 us against 100 us with 16 rows a
-    // block (5.6 TB/s; an in-place product of the same bytes takes 78 us).  Below that the blocks are too few.
-    if (few && heads >= kManyHeads) k_few<T, NF, true><<<(unsigned)heads, kFewThreads, 0, s>>>(p);
+    // A block a head once there are 24 for every SM.  Below that the blocks are too few; above it the fewer looks at the slots
+    // count.  Measured with states that come from HBM (us, a head / 16 rows a block; heads 1280, 1920, 3200, 5120): d = 112 27.5 /
+    // 25.0, 39.4 / 35.5, 58.9 / 58.6, 90.7 / 90.3; 128 33.9 / 29.8, 48.7 / 44.1, 72.1 / 70.3, 110.7 / 110.7; 64 10.0 / 10.4, 14.8 /
+    // 14.2, 21.8 / 22.0, 31.6 / 33.6; 32 5.1 / 4.7, 5.8 / 6.2, 8.5 / 9.0, 12.0 / 13.2.  With new inputs too at every call, 256
+    // sequences of 20 heads, d = 112: 92.4 / 97.4 (5.6 TB/s; an in-place product of the same bytes takes 78).
+    if (few && heads >= 24ll * seq_num_sms()) k_few<T, NF, true><<<(unsigned)heads, kFewThreads, 0, s>>>(p);
     else if (few) k_few<T, NF, false><<<(unsigned)blocks, kFewThreads, 0, s>>>(p);
     else k_many<T, NF><<<(unsigned)blocks, kManyThreads, 0, s>>>(p);
     return cudaGetLastError();

@@ -287,3 +287,29 @@ def test_a_saved_state_that_is_overwritten_raises(entry):
             continue
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             o.sum().backward()
+
+
+# ---------------------------------------------------------------- decode of many heads
+@pytest.mark.gpu
+@pytest.mark.parametrize("dk,dv,n,dtype", [(128, 128, 1, "bf16"), (128, 48, 3, "fp32"), (112, 112, 1, "fp32"), (16, 16, 2, "bf16"), (80, 96, 2, "bf16")])
+def test_decode_of_many_heads(dk, dv, n, dtype):
+    """A block a head (24 of them an SM) gives what 16 rows a block give, and both the definition's."""
+    B, H, Hk = 190, 20, 5
+    q, k, v, alpha, beta = [t.reshape(B, n, *t.shape[1:]) for t in cuda(*draw(B * n, H, Hk, dk, dv, dtype, 27))]
+    S = torch.randn(B + 2, H, dv, dk, generator=torch.Generator().manual_seed(3)).cuda()
+    slots = torch.randperm(B + 2, generator=torch.Generator().manual_seed(4))[:B].int().cuda()
+    slots[[7, 100]] = torch.tensor([-1, 10 * B], dtype=torch.int32, device="cuda")
+    whole, parts = S.clone(), S.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, _ = g.gdn_decode(q, k, v, alpha, beta, whole, slots, o=torch.zeros_like(v), status=status)
+    assert int(status) == binding.GDN_SEQ_BAD_SLOT
+    for a in range(0, B, 19):
+        some = slice(a, a + 19)
+        o1, _ = g.gdn_decode(*(t[some] for t in (q, k, v, alpha, beta)), parts, slots[some], o=torch.zeros_like(v[some]))
+        assert torch.equal(o[some], o1)
+    assert torch.equal(whole, parts)
+    at = [0, 50, 189]
+    rows, states = token_loop(*(t[at].flatten(0, 1).cpu().double() for t in (q, k, v, alpha, beta)), S[slots[at].long()].cpu().double(),
+                              [n] * 3, [n * i for i in range(3)])
+    close(o[at].flatten(0, 1), torch.stack([rows[t] for t in range(3 * n)]), tol32(dk, n), "o")
+    close(whole[slots[at].long()], torch.stack(states), tol32(dk, n), "S")
