@@ -61,17 +61,21 @@ struct ChunkWork {
     float *U, *dR, *X, *Z;   // [chunk x H][dv][64]; X = e^G K Sig, Z = e^{G_L-G} K D
     float *dqh, *dkh;        // as in SeqWork
     int *err;                // a bounded wait that gave up (k_prep clears it)
-    int *order;              // [n_seqs]: the sequences, the longest first; -1 - s of one that starts inside an earlier one
+    int *order;              // [n_seqs]: the sequences, the longest first (up to kSorted); -1 - s of one that starts inside an earlier one
     unsigned char *good;     // [n_seqs]: its rows are in order, by themselves and among the others
     SeqChunk *chunks;        // gdn_bwd: [chunks], what seq_chunk finds
     uint64_t wait_ns;        // limit of the bounded waits
     int drop;                // debug: the first block's K (1) or T (2) is never fetched, so its wait gives up
 };
 
-// The chains' blocks start with the longest sequences: a long one that starts last runs alone (16384 tokens in 24
-// sequences of 44 to 1971: 421 us against 505 in their order).  A sequence's place is the number of longer ones, ties by index.
-__device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order, unsigned char *good, int *len) {  // len: room for 2048
-    const bool sort = p.cu && p.n_seqs <= 2048;
+// The chains' blocks start with the longest sequences: a long one that starts last runs alone.  A sequence's place is the
+// number of longer ones, ties by index.  One block counts them, so with more than 512 sequences they stay in their order:
+// counting n^2 / 128 steps then takes longer than it saves.  Measured (us, longest first / as they are, lengths 1 to 600, many of
+// them short; 20 heads, d = 112, and 4 heads, d = 64): 32 sequences 157 / 169 and 41 / 48, 128 677 / 695 and 84 / 99, 256
+// 1384 / 1425 and 131 / 157, 512 2492 / 2522 and 290 / 307, 1024 4935 / 4934 and 621 / 587, 2048 10252 / 10093 and 1373 / 1140.
+constexpr int kSorted = 512;
+__device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order, unsigned char *good, int *len) {  // len: room for kSorted
+    const bool sort = p.cu && p.n_seqs <= kSorted;
     bool odd = false;
     if (p.cu)
         for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {

@@ -153,10 +153,11 @@ __global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant_
     const int s = blockIdx.x / per_seq, rb = blockIdx.x % per_seq;
     const int h = rb / (p.dv / 16), r0 = (rb % (p.dv / 16)) * 16, hk = h / (p.H / p.Hk);
     const int lr = threadIdx.x / 4, part = threadIdx.x & 3;
+    const SeqRange range = seq_rows(p, s);
+    if (range.len > p.max_len) return;  // another kernel's, which looks at the others for it
     const int slot = p.slots ? p.slots[s] : s, bad = seq_refused(p, s, slot);
     seq_report(p, bad, rb == 0 && threadIdx.x == 0);
-    const SeqRange range = seq_rows(p, s);
-    if (bad || slot < 0 || range.len > p.max_len) return;
+    if (bad || slot < 0) return;
     const size_t soff = (((size_t)slot * p.H + h) * p.dv + r0 + lr) * DK + part * 4;
     float4 S[NF];
     const bool zero = seq_starts_zero(p, s);
