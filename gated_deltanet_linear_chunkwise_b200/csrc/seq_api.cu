@@ -2,6 +2,7 @@
 //
 // As in gdn_api.cu, everything the host can see is checked before anything is enqueued, and no
 // C++ exception crosses the ABI.  What only the GPU can see (slots, cu_seqlens) the kernels check.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -14,15 +15,17 @@ namespace {
 enum Which { kDecode, kPacked, kBwd };
 
 // In a batch of short prompts the ones up to short_len() go token by token and the others in chunks, two launches beside one
-// another's sequences: a chunk step and its block's start take as long as about 12 tokens, or 24 where the token loop's blocks
-// are on the SMs together.  Where the average is kMixed or more, few can be short, and the chunks take them all.
-// Measured (us, both / chunks alone), up to 12: 20 heads, d = 112: 37 ragged prompts of 1201 tokens 83.6 / 101.8, 59 of 2537
-// 149 / 165, 60 of 8 tokens with 8 of 200 156 / 186; 8 heads, d = 128: 35 of 455 43 / 46, 60 of 8 with 8 of 200 94 / 87.
-// Up to 24 instead, 60 of 24 tokens with 8 of 200: 238 / 186 and 137 / 87; but 4 heads, d = 96, 9 of 72: 12 / 24 (up to 12: 23).
-// Averages of 64 (8 of 10 tokens, 16 long ones) 82.2 / 82.9 and 46 / 44, of 128 120 / 104 and 57 / 53, of 256 197 / 182, 98 / 88.
+// another's sequences: a chunk step and its block's start take as long as some tokens of the state's size, and as 24 where the
+// token loop's blocks are on the SMs together.  Where the average is kMixed or more, few can be short, and the chunks take
+// them all.  Measured (us, token by token / in chunks; 64 prompts and 8 of 100 tokens): 20 heads, d = 64: prompts of 8 tokens
+// 56 / 91, 24 85 / 93; 16 heads, d = 80: 8 66 / 114, 24 102 / 115; 20 heads, d = 96: 8 106 / 160, 16 135 / 159, 20 166 / 160; 4 heads,
+// d = 96, 256 prompts: 16 79 / 111, 24 105 / 111; 20 heads, d = 112, 60 and 8 of 200: 8 156 / 186, 16 192 / 185, 24 238 / 186; 8 heads,
+// d = 128: 8 94 / 87, 24 137 / 87.  9 of together 72 tokens, 4 heads, d = 96: 12 / 24 (with 16 alone token by token 23).
+// Averages (20 heads, d = 112; both / chunks alone): 32 83 / 102, 43 149 / 165, 64 82.2 / 82.9, 128 120 / 104, 256 197 / 182.
 constexpr long long kMixed = 48;
 long long short_len(const gdn::SeqProblem &p) {
-    return (long long)p.n_seqs * p.H * (p.dv / 16) <= 6ll * gdn::seq_num_sms() ? 24 : 12;
+    if ((long long)p.n_seqs * p.H * (p.dv / 16) <= 6ll * gdn::seq_num_sms()) return 24;
+    return std::min(24, 153600 / (p.dk * p.dv));  // 12 at 112 x 112
 }
 constexpr long long kEqual = 24;  // see chunked()
 
@@ -146,6 +149,7 @@ int check(const gdn_seq_args &a, Which which, gdn::SeqProblem &p) {
     p.status = a.status_dev;
     p.min_len = 0;
     p.max_len = a.n_tokens;
+    p.good = nullptr;
     return GDN_OK;
 }
 
@@ -200,13 +204,8 @@ int run(const gdn_seq_args *a, Which which) noexcept {
         cudaError_t e = cudaSuccess;
         if (which == kBwd) e = chunked(p, which) ? gdn::launch_seq_bwd_chunk(p, ws, s) : gdn::launch_seq_bwd_simt(p, ws, s);
         else if (p.n_seqs && which == kPacked && chunked(p, which)) {
-            if (p.cu && p.n_tokens < kMixed * p.n_seqs) {
-                const long long n = short_len(p);
-                p.max_len = n;
-                e = gdn::launch_seq_recurrent(p, false, s);
-                p.min_len = n + 1;
-            }
-            if (e == cudaSuccess) e = gdn::launch_seq_chunk(p, ws, s);
+            const bool mixed = p.cu && p.n_tokens < kMixed * p.n_seqs;
+            e = gdn::launch_seq_chunk(p, mixed ? short_len(p) : -1, ws, s);
         }
         else if (p.n_seqs) e = gdn::launch_seq_recurrent(p, which == kDecode, s);
         if (owned) {

@@ -2001,16 +2001,21 @@ template <int NF, bool SAVE> cudaError_t walk_fwd(const SeqProblem &p, const Chu
     return cudaGetLastError();
 }
 
-template <int NF> cudaError_t fwd(const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
+template <int NF> cudaError_t fwd(SeqProblem p, const ChunkWork &w, long long short_len, cudaStream_t s) {
     ChainMaps m;
-    if (walk(p)) {
-        if (!make_maps(m, p, p.v, p.v_stride, 64)) return cudaErrorInvalidValue;
-        cudaError_t e = prep<NF>(p, w, kLogAlphaFloor, s);
-        return e ? e : walk_fwd<NF, false>(p, w, m, s);
-    }
-    if (!make_maps(m, p, p.v, p.v_stride, NV)) return cudaErrorInvalidValue;
+    const bool walks = walk(p);
+    if (!make_maps(m, p, p.v, p.v_stride, walks ? 64 : NV)) return cudaErrorInvalidValue;
+    p.min_len = short_len + 1;
     cudaError_t e = prep<NF>(p, w, kLogAlphaFloor, s);
-    return e ? e : chain<decltype(&k_chunk_fwd<NF, false>), NF, false>(k_chunk_fwd<NF, false>, chain_threads(true), p, w, m, s);
+    if (e == cudaSuccess && short_len >= 0) {
+        SeqProblem few = p;
+        few.max_len = short_len;
+        few.good = w.good;
+        e = launch_seq_recurrent(few, false, s);
+    }
+    if (e) return e;
+    if (walks) return walk_fwd<NF, false>(p, w, m, s);
+    return chain<decltype(&k_chunk_fwd<NF, false>), NF, false>(k_chunk_fwd<NF, false>, chain_threads(true), p, w, m, s);
 }
 
 template <int NF> cudaError_t bwd(const SeqProblem &p, const ChunkWork &w, cudaStream_t s) {
@@ -2095,17 +2100,17 @@ size_t seq_chunk_workspace(const SeqProblem &p, bool bwd) {
     return n;
 }
 
-cudaError_t launch_seq_chunk(const SeqProblem &p, void *ws, cudaStream_t s) {
+cudaError_t launch_seq_chunk(const SeqProblem &p, long long short_len, void *ws, cudaStream_t s) {
     const ChunkWork w = carve(p, ws, false, nullptr);
     switch (p.dk / 16) {
-        case 1: return fwd<1>(p, w, s);
-        case 2: return fwd<2>(p, w, s);
-        case 3: return fwd<3>(p, w, s);
-        case 4: return fwd<4>(p, w, s);
-        case 5: return fwd<5>(p, w, s);
-        case 6: return fwd<6>(p, w, s);
-        case 7: return fwd<7>(p, w, s);
-        default: return fwd<8>(p, w, s);
+        case 1: return fwd<1>(p, w, short_len, s);
+        case 2: return fwd<2>(p, w, short_len, s);
+        case 3: return fwd<3>(p, w, short_len, s);
+        case 4: return fwd<4>(p, w, short_len, s);
+        case 5: return fwd<5>(p, w, short_len, s);
+        case 6: return fwd<6>(p, w, short_len, s);
+        case 7: return fwd<7>(p, w, short_len, s);
+        default: return fwd<8>(p, w, short_len, s);
     }
 }
 

@@ -27,6 +27,7 @@ struct SeqProblem {
     float *dalpha, *dbeta, *dS_in;
     int *status;
     long long min_len, max_len;  // gdn_packed: a kernel leaves sequences of other lengths to another one
+    const unsigned char *good;   // k_many beside a walk: the verdicts that k_prep has left (the walk reports the bits), or null
 };
 
 // Rows and state entry of a sequence.  slot < 0: the sequence is skipped.
@@ -72,11 +73,23 @@ __device__ __forceinline__ bool seq_late_odd(const SeqProblem &p, int s) {
     for (int j = threadIdx.x; j < s; j += blockDim.x) late |= seq_reaches(p, j, r.first);
     return __syncthreads_or(late && r.len > 0);
 }
+// A thread's share of: is one of the ranges before s no ordered one?  Where none is, all of them are in order, and s, if it
+// is by itself, is too.  (Every block of a batch looks: with thousands of short sequences the loads count, four a thread.)
+__device__ __forceinline__ bool seq_odd_before(const SeqProblem &p, int s) {
+    bool odd = s > 0 && p.cu[0] < 0;
+    int from = 0;
+    if (((size_t)p.cu & 15) == 0) {
+        from = s & ~3;
+        for (int j = 4 * threadIdx.x; j < from; j += 4 * blockDim.x) {
+            const int4 x = *reinterpret_cast<const int4 *>(p.cu + j);
+            odd |= x.x > x.y || x.y > x.z || x.z > x.w || x.w > p.cu[j + 4];
+        }
+    }
+    for (int j = from + threadIdx.x; j < s; j += blockDim.x) odd |= p.cu[j] > p.cu[j + 1];
+    return odd;
+}
 __device__ __forceinline__ bool seq_late(const SeqProblem &p, int s) {
-    if (!p.cu) return false;
-    bool odd = false;  // where every earlier range is in order by itself, all of them are
-    for (int j = threadIdx.x; j < s; j += blockDim.x) odd |= seq_rows(p, j).bad != 0;
-    return __syncthreads_or(odd) && seq_late_odd(p, s);
+    return p.cu && __syncthreads_or(seq_odd_before(p, s)) && seq_late_odd(p, s);
 }
 __device__ constexpr SeqRange kSeqLate = {0, 0, -1, GDN_SEQ_BAD_ROWS};
 __device__ __forceinline__ SeqRange seq_rows_in_order(const SeqProblem &p, int s) { return seq_late(p, s) ? kSeqLate : seq_rows(p, s); }
@@ -96,12 +109,9 @@ template <typename Good> __device__ __forceinline__ int seq_slot_bits(const SeqP
 // bytes of spills.)
 __device__ __forceinline__ int seq_refused(const SeqProblem &p, int s, int slot) {
     int bad = seq_rows(p, s).bad;
-    bool odd = false;
-    if (p.cu || p.slots)
-        for (int i = threadIdx.x; i < s; i += blockDim.x) {
-            if (p.cu) odd |= seq_rows(p, i).bad != 0;
-            if (p.slots) odd |= p.slots[i] == slot;
-        }
+    bool odd = p.cu && seq_odd_before(p, s);
+    if (p.slots)
+        for (int i = threadIdx.x; i < s; i += blockDim.x) odd |= p.slots[i] == slot;
     if (__syncthreads_or(odd)) {
         if (p.cu && seq_late_odd(p, s)) bad |= GDN_SEQ_BAD_ROWS;
         bad |= seq_slot_bits(p, s, slot, [&](int i) {
@@ -212,7 +222,8 @@ cudaError_t launch_seq_share(const SeqProblem &p, const float *dqh, const float 
 
 // gdn_packed and gdn_bwd in chunks on the tensor cores, bf16 q, k, v (seq_chunk.cu).
 size_t seq_chunk_workspace(const SeqProblem &p, bool bwd);
-cudaError_t launch_seq_chunk(const SeqProblem &p, void *ws, cudaStream_t s);
+// Sequences of up to short_len go token by token.
+cudaError_t launch_seq_chunk(const SeqProblem &p, long long short_len, void *ws, cudaStream_t s);
 cudaError_t launch_seq_bwd_chunk(const SeqProblem &p, void *ws, cudaStream_t s);
 
 int seq_num_sms();  // of the current device

@@ -155,12 +155,13 @@ __global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant_
     const int lr = threadIdx.x / 4, part = threadIdx.x & 3;
     const SeqRange range = seq_rows(p, s);
     if (range.len > p.max_len) return;  // another kernel's, which looks at the others for it
-    const int slot = p.slots ? p.slots[s] : s, bad = seq_refused(p, s, slot);
-    seq_report(p, bad, rb == 0 && threadIdx.x == 0);
-    if (bad || slot < 0) return;
-    const size_t soff = (((size_t)slot * p.H + h) * p.dv + r0 + lr) * DK + part * 4;
+    const int slot = p.slots ? p.slots[s] : s;
+    // The state's and the first tokens' loads wait for nothing but an index in range: both are on their way while the other
+    // sequences are looked at.
+    const bool inside = !range.bad && slot >= 0 && (!p.slots || slot < p.n_slots);
+    const size_t soff = (((size_t)(inside ? slot : 0) * p.H + h) * p.dv + r0 + lr) * DK + part * 4;
     float4 S[NF];
-    const bool zero = seq_starts_zero(p, s);
+    const bool zero = !inside || seq_starts_zero(p, s);
 #pragma unroll
     for (int j = 0; j < NF; ++j) S[j] = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : ld4(p.S_in + soff + 16 * j);
 
@@ -203,10 +204,17 @@ __global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant_
     };
     T *out = (T *)p.o + (range.first * p.H + h) * p.dv + r0 + lr;
     const size_t out_step = (size_t)p.H * p.dv;
-    if (range.len > 0) {
-        fetch(0);
-        stash(0);
+    if (inside && range.len > 0) fetch(0);
+    int bad;
+    if (p.good) {
+        if (!p.good[s]) return;
+        bad = seq_slot_bits(p, s, slot, [&](int i) { return p.good[i] != 0; });
+    } else {
+        bad = seq_refused(p, s, slot);
+        seq_report(p, bad, rb == 0 && threadIdx.x == 0);
     }
+    if (bad || slot < 0) return;
+    if (range.len > 0) stash(0);
     __syncthreads();
     int b = 0;
     for (long long t0 = 0; t0 < range.len; t0 += kTok, b ^= 1) {
