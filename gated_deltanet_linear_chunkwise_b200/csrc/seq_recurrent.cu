@@ -143,9 +143,12 @@ __global__ void __launch_bounds__(kFewThreads) k_few(const __grid_constant__ Seq
 constexpr int kTok = 16;
 constexpr int kManyThreads = 64;
 
-// Six blocks an SM: left to itself the compiler takes registers for five, and batches of short prompts run a fifth longer.
-template <typename T, int NF>
-__global__ void __launch_bounds__(kManyThreads, 6) k_many(const __grid_constant__ SeqProblem p) {
+// BLOCKS an SM.  Left to itself the compiler takes the registers it likes (four blocks an SM at d_k = 128), which is best for a few
+// long chains; with many blocks six of them hide more, although d_k = 128 spills then (80 bytes).  Measured (us, free / six):
+// 5 fp32 sequences of up to 996 tokens, 6 heads: d = 64 132 / 136, 96 174 / 180, 112 197 / 218, 128 208 / 275; 40 prompts of 20
+// tokens, 20 heads: 64 36 / 31, 96 75 / 65, 112 97 / 83, 128 117 / 107.
+template <typename T, int NF, int BLOCKS>
+__global__ void __launch_bounds__(kManyThreads, BLOCKS) k_many(const __grid_constant__ SeqProblem p) {
     constexpr int DK = 16 * NF;
     __shared__ __align__(16) float sk[2][kTok][DK], sq[2][kTok][DK];
     __shared__ float sv[2][kTok][16], sg[2][kTok][2];
@@ -263,7 +266,8 @@ template <typename T, int NF> cudaError_t launch(const SeqProblem &p, bool few, 
     // sequences of 20 heads, d = 112: 92.4 / 97.4 (5.6 TB/s; an in-place product of the same bytes takes 78).
     if (few && heads >= 24ll * seq_num_sms()) k_few<T, NF, true><<<(unsigned)heads, kFewThreads, 0, s>>>(p);
     else if (few) k_few<T, NF, false><<<(unsigned)blocks, kFewThreads, 0, s>>>(p);
-    else k_many<T, NF><<<(unsigned)blocks, kManyThreads, 0, s>>>(p);
+    else if (blocks > 4ll * seq_num_sms()) k_many<T, NF, 6><<<(unsigned)blocks, kManyThreads, 0, s>>>(p);
+    else k_many<T, NF, 1><<<(unsigned)blocks, kManyThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
