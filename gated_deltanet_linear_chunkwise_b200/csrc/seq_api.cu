@@ -17,15 +17,16 @@ enum Which { kDecode, kPacked, kBwd };
 // In a batch of short prompts the ones up to short_len() go token by token and the others in chunks, two launches beside one
 // another's sequences: a chunk step and its block's start take as long as some tokens of the state's size, and as 24 where the
 // token loop's blocks are on the SMs together.  Where the average is kMixed or more, few can be short, and the chunks take
-// them all.  Measured (us, token by token / in chunks; 64 prompts and 8 of 100 tokens): 20 heads, d = 64: prompts of 8 tokens
-// 56 / 91, 24 85 / 93; 16 heads, d = 80: 8 66 / 114, 24 102 / 115; 20 heads, d = 96: 8 106 / 160, 16 135 / 159, 20 166 / 160; 4 heads,
-// d = 96, 256 prompts: 16 79 / 111, 24 105 / 111; 20 heads, d = 112, 60 and 8 of 200: 8 156 / 186, 16 192 / 185, 24 238 / 186; 8 heads,
-// d = 128: 8 94 / 87, 24 137 / 87.  9 of together 72 tokens, 4 heads, d = 96: 12 / 24 (with 16 alone token by token 23).
-// Averages (20 heads, d = 112; both / chunks alone): 32 83 / 102, 43 149 / 165, 64 82.2 / 82.9, 128 120 / 104, 256 197 / 182.
+// them all.  Measured (us, token by token / in chunks), 64 prompts of one length and 8 of 100 tokens: 20 heads, d = 64: 8 tokens
+// 56 / 91, 24 85 / 93; 16 heads, d = 80: 8 66 / 114, 24 102 / 115; 20 heads, d = 96: 8 101 / 159, 16 137 / 160, 20 166 / 160; 20
+// heads, d = 112: 8 135 / 174, 16 173 / 174, 20 202 / 174; 16 heads, d = 128: 8 127 / 155, 12 149 / 156, 16 168 / 155.  256 prompts
+// alone: d = 96: 16 401 / 480, 20 488 / 481; 112: 16 507 / 523, 20 605 / 526; 128: 12 430 / 473, 16 493 / 472.  9 of together 72
+// tokens, 4 heads, d = 96: 12 / 24.  Averages (20 heads, d = 112; both / chunks alone): 32 83 / 102, 43 149 / 165, 64 82.2 / 82.9,
+// 128 120 / 104, 256 197 / 182.
 constexpr long long kMixed = 48;
 long long short_len(const gdn::SeqProblem &p) {
     if ((long long)p.n_seqs * p.H * (p.dv / 16) <= 6ll * gdn::seq_num_sms()) return 24;
-    return std::min(24, 153600 / (p.dk * p.dv));  // 12 at 112 x 112
+    return std::min(24, 25 - p.dk * p.dv / 1200);  // through the even points: 18 at d = 96, 15 at 112, 12 at 128
 }
 constexpr long long kEqual = 24;  // see chunked()
 
