@@ -6,7 +6,7 @@ import torch
 
 import gated_deltanet_linear_chunkwise_b200 as g
 from gated_deltanet_linear_chunkwise_b200 import binding
-from test_sequences import F64, close, cuda, draw, exact_grads, tol32, token_loop
+from test_sequences import F64, close, cuda, draw, exact_grads, packed_case, tol32, token_loop
 
 
 # ---------------------------------------------------------------- rows of q, k and v
@@ -313,3 +313,98 @@ def test_decode_of_many_heads(dk, dv, n, dtype):
                               [n] * 3, [n * i for i in range(3)])
     close(o[at].flatten(0, 1), torch.stack([rows[t] for t in range(3 * n)]), tol32(dk, n), "o")
     close(whole[slots[at].long()], torch.stack(states), tol32(dk, n), "S")
+
+
+# ---------------------------------------------------------------- sizes and paths that the cases above leave out
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+def test_autograd_bf16(packed):
+    B, T, H, Hk, dk, dv = 2, 90, 4, 2, 48, 64
+    tensors = draw(B * T, H, Hk, dk, dv, "bf16", 43)
+    gen = torch.Generator().manual_seed(1)
+    S_in, wS = torch.randn(B, H, dv, dk, generator=gen), torch.randn(B, H, dv, dk, generator=gen)
+    w = torch.randn(B * T, H, dv, generator=gen).to(torch.bfloat16)
+    shape = (lambda t: t) if packed else (lambda t: t.reshape(B, T, *t.shape[1:]))
+    mine = [shape(t).cuda().requires_grad_(True) for t in tensors] + [S_in.cuda().requires_grad_(True)]
+    cu = torch.tensor([0, T, 2 * T], dtype=torch.int32, device="cuda") if packed else None
+    o, S = g.gated_delta_rule(*mine, cu)
+    torch.autograd.backward([o, S], [shape(w).cuda(), wS.cuda()])
+    rows, states = token_loop(*(t.double() for t in tensors), S_in.double(), [T] * B, [0, T])
+    close(o.reshape(B * T, H, dv), torch.stack([rows[t] for t in range(B * T)]), tol32(dk, T), "o")
+    close(S, torch.stack(states), tol32(dk, T), "S")
+    want = exact_grads(tensors, [0, T], [T] * B, S_in, w, wS)
+    for name, x, y in zip(("q", "k", "v", "alpha", "beta", "S_in"), mine, want):
+        assert x.grad.dtype == x.dtype
+        close(x.grad.reshape(y.shape), y, tol32(dk, T, 4), name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hk,dk,dv", [(2, 1, 128, 128), (4, 4, 128, 80), (4, 2, 96, 112)])
+def test_walks_of_large_states(H, Hk, dk, dv):
+    """Chains enough for a warp a slice, with the largest states."""
+    lens = [70, 130, 64] + [33] * 35
+    tensors, starts, cu = packed_case(lens, 0, 0, H, Hk, dk, dv, "bf16", "slow", seed=45)
+    n, some, N = len(lens), 3, sum(lens[:3])  # the sequences do not meet: three are looked at
+    gen = torch.Generator().manual_seed(6)
+    do = torch.randn(tensors[2].shape, generator=gen).to(torch.bfloat16)
+    S_in, dS_out = torch.randn(n, H, dv, dk, generator=gen), torch.randn(n, H, dv, dk, generator=gen)
+    first = [t[:N] for t in tensors]
+    rows, states = token_loop(*(t.double() for t in first), S_in[:some].double(), lens[:some], starts[:some])
+    o, S = g.gdn_packed(*cuda(*tensors), cu.cuda(), S_in.cuda(), return_state=True)
+    close(o[:N], torch.stack([rows[t] for t in range(N)]), tol32(dk, 130), "o")
+    close(S[:some], torch.stack(states), tol32(dk, 130), "S")
+    want = exact_grads(first, starts[:some], lens[:some], S_in[:some], do[:N], dS_out[:some])
+    got = g.gdn_bwd(*cuda(*tensors), do.cuda(), cu.cuda(), S_in.cuda(), dS_out=dS_out.cuda())
+    for name, x, y in zip(("dq", "dk", "dv", "dalpha", "dbeta", "dS_in"), got, want):
+        close(x[:some if name == "dS_in" else N], y, tol32(dk, 130, 4), name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_long_sequence(dtype):
+    T, H, dk, dv = 2500, 1, 48, 32
+    tensors = draw(T, H, H, dk, dv, dtype, 47)
+    gen = torch.Generator().manual_seed(7)
+    do = torch.randn(tensors[2].shape, generator=gen).to(tensors[2].dtype)
+    S_in, dS = torch.randn(1, H, dv, dk, generator=gen), torch.randn(1, H, dv, dk, generator=gen)
+    rows, states = token_loop(*(t.double() for t in tensors), S_in.double(), [T], [0])
+    one = [t.cuda()[None] for t in tensors]
+    o, S = g.gdn_packed(*one, None, S_in.cuda(), return_state=True)
+    close(o[0], torch.stack([rows[t] for t in range(T)]), tol32(dk, T), "o")
+    close(S, torch.stack(states), tol32(dk, T), "S")
+    want = exact_grads(tensors, [0], [T], S_in, do, dS)
+    got = g.gdn_bwd(*one, do.cuda()[None], None, S_in.cuda(), dS_out=dS.cuda())
+    for name, x, y in zip(("dq", "dk", "dv", "dalpha", "dbeta", "dS_in"), got, want):
+        close(x if name == "dS_in" else x[0], y, tol32(dk, T, 4), name)
+
+
+@pytest.mark.gpu
+def test_one_captured_call_serves_other_sequences():
+    """A graph replayed with other lengths, slots and gates in the same tensors: nothing of the first ones is kept."""
+    N, n, H, d = 400, 6, 4, 64
+    sets = [draw(N, H, 2, d, d, "bf16", seed) for seed in (101, 102)]
+    cus = [[0, 100, 100, 164, 300, 310, 400], [0, 3, 9, 50, 51, 390, 400]]
+    slots = [[3, 1, 0, 7, 2, 4], [0, 1, 2, 3, 4, 5]]
+    pool = torch.randn(8, H, d, d, generator=torch.Generator().manual_seed(1)).cuda()
+    do = torch.randn(N, H, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def everything(x, cu, sl, S):
+        o, _ = g.gdn_packed(*x, cu, S, S_out=S, slots=sl)
+        return [o, S, *g.gdn_bwd(*x, do, cu, need_dS_in=True)]
+
+    want = [[t.clone() for t in everything(cuda(*s), ints(c), ints(sl), pool.clone())] for s, c, sl in zip(sets, cus, slots)]
+    x, cu, sl, S = cuda(*sets[0]), ints(cus[0]), ints(slots[0]), pool.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = everything(x, cu, sl, S)
+    for i in (1, 0, 1):
+        for a, b in zip(x, sets[i]):
+            a.copy_(b)
+        cu.copy_(ints(cus[i]))
+        sl.copy_(ints(slots[i]))
+        S.copy_(pool)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b)
