@@ -84,20 +84,16 @@ __device__ __forceinline__ void order_sequences(const SeqProblem &p, int *order,
             odd |= r.bad != 0;
         }
     odd = __syncthreads_or(odd);  // else every range is in order
+    if (odd) seq_each_in_order<128>(p, p.n_seqs, [&](int s, const SeqRange &r, bool late) { good[s] = !late && !r.bad; });
+    __syncthreads();
     for (int s = threadIdx.x; s < p.n_seqs; s += blockDim.x) {
         int place = s;
         if (sort) {
             place = 0;
             for (int j = 0; j < p.n_seqs; ++j) place += len[j] > len[s] || (len[j] == len[s] && j < s);
         }
-        bool late = false, wrong = false;
-        if (odd) {
-            const SeqRange r = seq_rows(p, s);
-            wrong = r.bad;
-            for (int j = 0; j < s && r.len > 0; ++j) late |= seq_reaches(p, j, r.first);
-        }
-        order[place] = late ? -1 - s : s;
-        good[s] = !late && !wrong;
+        if (!odd) good[s] = 1;
+        order[place] = odd && !good[s] && !seq_rows(p, s).bad ? -1 - s : s;
     }
 }
 

@@ -104,23 +104,51 @@ template <typename Good> __device__ __forceinline__ int seq_slot_bits(const SeqP
     return (__syncthreads_or(same) ? GDN_SEQ_SAME_SLOT : 0) | (slot >= p.n_slots ? GDN_SEQ_BAD_SLOT : 0);
 }
 
-// All bits of a sequence (any of them: it is skipped), where nothing is known of the others; called by a whole block.  What
-// is rarely true is looked into behind one vote.  (The bits alone: a range put together on several paths cost k_many 340
-// bytes of spills.)
-__device__ __forceinline__ int seq_refused(const SeqProblem &p, int s, int slot) {
+// f(i, range, late) for the sequences before n, a thread each: the running maximum of the ends says where an earlier one
+// reaches behind a sequence's first row.  Called by a whole block of THREADS.
+template <int THREADS, typename F> __device__ __forceinline__ void seq_each_in_order(const SeqProblem &p, int n, F f) {
+    __shared__ int ends[THREADS / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    int reached = 0;  // by the sequences before these THREADS
+    for (int i0 = 0; i0 < n; i0 += THREADS) {
+        const int i = i0 + threadIdx.x;
+        SeqRange r = {0, 0, -1, 0};
+        if (i < n) r = seq_rows(p, i);
+        int end = r.len > 0 ? (int)(r.first + r.len) : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end = max(end, x);
+        }
+        __syncthreads();
+        if (lane == 31) ends[warp] = end;
+        __syncthreads();
+        int before = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) before = 0;
+        before = max(before, reached);
+        for (int k = 0; k < THREADS / 32; ++k) {
+            if (k < warp) before = max(before, ends[k]);
+            reached = max(reached, ends[k]);
+        }
+        if (i < n) f(i, r, r.len > 0 && r.first < before);
+    }
+}
+
+// All bits of a sequence (any of them: it is skipped), where nothing is known of the others; called by a whole block of
+// THREADS.  What is rarely true is looked into behind one vote.  (The bits alone: a range put together on several paths
+// cost k_many 340 bytes of spills.)
+template <int THREADS> __device__ __forceinline__ int seq_refused(const SeqProblem &p, int s, int slot) {
     int bad = seq_rows(p, s).bad;
     bool odd = p.cu && seq_odd_before(p, s);
     if (p.slots)
         for (int i = threadIdx.x; i < s; i += blockDim.x) odd |= p.slots[i] == slot;
     if (__syncthreads_or(odd)) {
-        if (p.cu && seq_late_odd(p, s)) bad |= GDN_SEQ_BAD_ROWS;
-        bad |= seq_slot_bits(p, s, slot, [&](int i) {
-            const SeqRange r = seq_rows(p, i);
-            bool good = !r.bad;
-            if (p.cu && r.len > 0)
-                for (int j = 0; j < i; ++j) good &= !seq_reaches(p, j, r.first);
-            return good;
+        bool rows = false, same = false;
+        seq_each_in_order<THREADS>(p, s + 1, [&](int i, const SeqRange &r, bool late) {
+            if (i == s) rows = late;
+            else same |= p.slots && p.slots[i] == slot && !r.bad && !late;
         });
+        if (__syncthreads_or(rows)) bad |= GDN_SEQ_BAD_ROWS;
+        if (__syncthreads_or(same) && slot >= 0) bad |= GDN_SEQ_SAME_SLOT;
     }
     return p.slots && slot >= p.n_slots ? bad | GDN_SEQ_BAD_SLOT : bad;
 }

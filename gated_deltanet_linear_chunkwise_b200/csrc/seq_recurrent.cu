@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kManyThreads, BLOCKS) k_many(const __grid_cons
         if (!p.good[s]) return;
         bad = seq_slot_bits(p, s, slot, [&](int i) { return p.good[i] != 0; });
     } else {
-        bad = seq_refused(p, s, slot);
+        bad = seq_refused<kManyThreads>(p, s, slot);
         seq_report(p, bad, rb == 0 && threadIdx.x == 0);
     }
     if (bad || slot < 0) return;

@@ -435,38 +435,16 @@ __global__ void k_share(const __grid_constant__ SeqProblem p, const float *dqh, 
     }
 }
 
-// 64 rows a block; a row is covered where a range that is in order holds it (seq_rows_in_order): the running maximum of
-// the ends, 256 sequences at a time, says where an earlier one reaches behind a sequence's first row.
+// 64 rows a block; a row is covered where a range that is in order holds it.
 __global__ void __launch_bounds__(256) k_zero_rows(const __grid_constant__ SeqProblem p, float *dqh, float *dkh) {
     __shared__ unsigned char covered[64];
-    __shared__ long long ends[8];
     const long long r0 = blockIdx.x * 64ll;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     if (threadIdx.x < 64) covered[threadIdx.x] = 0;
-    long long reached = 0;  // by the sequences before these 256
-    for (int s0 = 0; s0 < p.n_seqs; s0 += 256) {
-        const int s = s0 + threadIdx.x;
-        SeqRange r = {0, 0, -1, 0};
-        if (s < p.n_seqs) r = seq_rows(p, s);
-        long long end = r.len > 0 ? r.first + r.len : 0;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, end, o);
-            if (lane >= o) end = max(end, x);
-        }
-        __syncthreads();
-        if (lane == 31) ends[warp] = end;
-        __syncthreads();
-        long long before = __shfl_up_sync(0xffffffffu, end, 1);
-        if (lane == 0) before = 0;
-        before = max(before, reached);
-        for (int i = 0; i < 8; ++i) {
-            if (i < warp) before = max(before, ends[i]);
-            reached = max(reached, ends[i]);
-        }
-        if (r.len == 0 || r.first < before) continue;
+    seq_each_in_order<256>(p, p.n_seqs, [&](int, const SeqRange &r, bool late) {
+        if (late) return;
         const long long a = max(r.first, r0), b = min(r.first + r.len, r0 + 64);
         for (long long i = a; i < b; ++i) covered[i - r0] = 1;
-    }
+    });
     __syncthreads();
     const int es = p.dtype == GDN_DTYPE_BF16 ? 2 : 4;
     auto zero = [&](void *base, long long row, long long bytes) {  // 4-byte words: bytes is a multiple of 4

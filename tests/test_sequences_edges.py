@@ -408,3 +408,28 @@ def test_one_captured_call_serves_other_sequences():
         torch.cuda.synchronize()
         for a, b in zip(got, want[i]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_thousands_of_wrong_sequences(dtype):
+    """Many entries of one slot and a range that is wrong: looked through once a block, not once an entry."""
+    n, H, d = 3000, 2, 32
+    q, k, v, alpha, beta = cuda(*draw(64 + n, H, H, d, d, dtype, 103))
+    cu = torch.cat([torch.tensor([0, 64, -1]), 64 + torch.arange(n - 1)]).int().cuda()  # good, two wrong ones, then a token each
+    assert cu.numel() == n + 2
+    slots = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    pool = torch.randn(2, H, d, d, device="cuda")
+    S, status = pool.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = torch.full(v.shape, 7.0, dtype=v.dtype, device="cuda")
+    g.gdn_packed(q, k, v, alpha, beta, cu, S, S_out=S, slots=slots, o=o, status=status)  # warm
+    assert int(status) == binding.GDN_SEQ_SAME_SLOT | binding.GDN_SEQ_BAD_ROWS
+    assert (o[64:] == 7).all() and not (o[:64] == 7).all(dim=-1).any() and torch.equal(S[1], pool[1])
+    o1, S1 = g.gdn_packed(*(t[None, :64] for t in (q, k, v, alpha, beta)), None, pool[:1], return_state=True)
+    close(S[:1], S1.double(), 2 * tol32(d, 64), "S")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    g.gdn_packed(q, k, v, alpha, beta, cu, S, S_out=S, slots=slots, o=o)
+    end.record()
+    end.synchronize()
+    assert start.elapsed_time(end) < 100  # ms: 3000 x 4 blocks that each look at 3000 entries; by pairs it would be seconds
