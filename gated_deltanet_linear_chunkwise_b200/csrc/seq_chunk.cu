@@ -2,7 +2,7 @@
 //
 // Notation and formulas as in seq_simt.cu; chunks of 64 tokens.
 //
-// k_prep         every (chunk, head) by itself: T, P and the decays.
+// k_prep         every (chunk, head) by itself: T, P and the decays; one block more: the sequences' order and verdicts.
 // k_chunk_fwd    a block walks the chunks of one sequence and head with 16 columns of the state
 //                (d_v columns are independent), S = Sig^T's 16 rows in registers:
 //                  X^T = S [K;Q]^T,  Y = V - e^G X_K,  U^T = (beta Y)^T T^T,
@@ -343,7 +343,7 @@ template <int NF, bool BWD> struct ChainSmem {
 enum { kBarK = 0, kBarV = 2, kBarT = 3, kBarP = 4 };
 // Four warps carry the state from chunk to chunk, four more (where O is wanted) compute it beside them, one fetches.
 // Bound by its latency: 3900 clocks a step of 64 tokens at d = 112, of which 1300 are the products' and 1700 shared memory's (every warp
-// reads all of S's terms); one sequence of 8209 tokens, 20 heads: 342 us with k_prep.
+// reads all of S's terms); one sequence of 8209 tokens, 20 heads: 344 us with k_prep.
 constexpr int chain_threads(bool with_o) { return with_o ? 288 : 160; }
 
 struct ChainMaps {
@@ -871,7 +871,8 @@ __global__ void __launch_bounds__(chain_threads(false), 1) k_chunk_bwd(const __g
 // a step and slice, 56 % of the warp products' rate of 1024 multiply-adds a clock and SM), against 492 us.  A block has up to four
 // slices of one sequence and head; one of its threads fetches.
 constexpr int kSlices = 4;
-constexpr int kWalkThreads = 32 * kSlices;  // eight warps an SM, two blocks, leave a thread its 255 registers
+// eight warps an SM, two blocks, leave a thread its 255 registers (d_k = 112 and 128 spill 8 to 88 bytes)
+constexpr int kWalkThreads = 32 * kSlices;
 
 template <int NF, bool BWD> struct WalkSmem {  // 1024-byte aligned
     static constexpr int kSlabs = (NF + 3) / 4, kTile = kSlabs * C * 64, kTermsP = BWD ? 3 : 2;

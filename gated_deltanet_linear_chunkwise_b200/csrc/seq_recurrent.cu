@@ -10,7 +10,7 @@
 // (2 x 4 d_k d_v bytes a head against 2 (2 d_k + 2 d_v)): the bound is HBM.
 // k_many: sequences of tokens (gdn_packed, where the chunked form does not serve), with the
 // tokens' rows staged in shared memory a block ahead.  A long sequence is bound by the chain of a token's two dot products
-// (996 tokens, d_k = 64: 140 us, 270 clocks a token), many short ones by the fp32 pipe: 4 d_k d_v instructions' lanes a token
+// (996 tokens, d_k = 64: 132 us, 260 clocks a token), many short ones by the fp32 pipe: 4 d_k d_v instructions' lanes a token
 // and head.
 #include <cuda_bf16.h>
 #include <type_traits>
