@@ -411,6 +411,35 @@ def test_one_captured_call_serves_other_sequences():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("more", [20, 100])
+def test_one_slot_of_a_short_and_a_long_sequence(more):
+    """In a batch of short prompts they go through different kernels, which have to agree on which one runs."""
+    H, Hk, dk, dv = 4, 2, 48, 64
+    lens = [5, 40, 70, 6, 0, 33, 12] + [20] * more
+    slots = [0, 0, 1, 1, 2, 2, -1] + [3 + i for i in range(more)]  # the second of each slot is skipped, an empty one runs too
+    N, n = sum(lens), len(lens)
+    starts = [sum(lens[:i]) for i in range(n)]
+    run = [0, 2, 4, *range(7, n)]
+    tensors = draw(N, H, Hk, dk, dv, "bf16", 93)
+    pool = torch.randn(3 + more, H, dv, dk, generator=torch.Generator().manual_seed(2))
+    fresh = torch.arange(n) % 5 == 2
+    at = [slots[s] for s in run]
+    S0 = pool.double()[at] * ~fresh[run][:, None, None, None]
+    rows, states = token_loop(*(t.double() for t in tensors), S0, [lens[s] for s in run], [starts[s] for s in run])
+    want = pool.double()
+    want[at] = torch.stack(states)
+    S, o = pool.cuda(), torch.full(tensors[2].shape, 7.0, dtype=tensors[2].dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    g.gdn_packed(*cuda(*tensors), ints(starts + [N]), S, S_out=S, slots=ints(slots), fresh=fresh.cuda(), o=o, status=status)
+    assert int(status) == binding.GDN_SEQ_SAME_SLOT
+    close(S, want, tol32(dk, 70), "S")
+    covered = sorted(rows)
+    close(o[covered], torch.stack([rows[t] for t in covered]), tol32(dk, 70), "o")
+    assert (o[[t for t in range(N) if t not in rows]] == 7).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_thousands_of_wrong_sequences(dtype):
     """Many entries of one slot and a range that is wrong: looked through once a block, not once an entry."""
